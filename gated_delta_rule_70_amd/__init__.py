@@ -14,6 +14,9 @@ Layouts (dense, row-major, on the GPU): q, k ``[B,T,HK,dk]`` and v ``[B,T,HV,dv]
 bf16 or fp32; g ``[B,T,HV,dk]`` and beta ``[B,T,HV]`` in fp32; states ``[B,HV,dk,dv]``
 fp32; o ``[B,T,HV,dv]`` fp32, or bf16 with ``out_dtype=torch.bfloat16`` (or a bf16 ``o``
 passed in): every entry point then stores each fp32 output rounded to nearest even.
+
+The projections on either side of the delta rule, in 8-bit integers, are in
+:mod:`.quantized`: ``add_rmsnorm_i8``, ``matmul_i8`` and ``gated_rmsnorm_i8``.
 """
 from __future__ import annotations
 
@@ -22,11 +25,15 @@ import os
 
 import torch
 
+from . import quantized
+from .quantized import add_rmsnorm_i8, gated_rmsnorm_i8, matmul_i8, quantize_rows_i8
+
 __all__ = ["decode_step", "fused_recurrent", "chunk_prefill", "chunk_prefill_noalloc", "forward",
            "tree_verify", "chunk_prefill_varlen", "fused_recurrent_varlen", "workspace_bytes_varlen",
            "NOALLOC_SCRATCH_BYTES", "VARLEN_MAX_SEQS",
            "workspace_bytes", "GdrError", "lib", "Dims", "LIB_PATH", "ABI_VERSION",
-           "RECURRENT_MAX_T", "TREE_MAX_T", "O_BF16"]
+           "RECURRENT_MAX_T", "TREE_MAX_T", "O_BF16",
+           "add_rmsnorm_i8", "gated_rmsnorm_i8", "matmul_i8", "quantize_rows_i8"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdr.so")
 ABI_VERSION = 8
@@ -97,6 +104,7 @@ def lib():
     L.gdr_chunk_prefill_varlen.argtypes = [ctypes.POINTER(Dims)] + [_VP] * 10 + [ctypes.c_size_t, _VP]
     L.gdr_fused_recurrent_varlen.restype = ctypes.c_int
     L.gdr_fused_recurrent_varlen.argtypes = [ctypes.POINTER(Dims)] + [_VP] * 10
+    quantized.bind(L)
     if L.gdr_abi_version() != ABI_VERSION:
         raise RuntimeError("libgdr.so ABI version mismatch; rebuild it")
     _lib = L

@@ -1,0 +1,281 @@
+"""The 8-bit projections around a gated delta rule layer (C ABI in ``include/gdr_i8.h``).
+
+    q8, s8, hidden = gdr.add_rmsnorm_i8(x, norm_w, residual=hidden)            # norm, codes, scales
+    q, k, v, z = gdr.matmul_i8(q8, s8, w_in, w_in_scale, out=(2048, 2048, 4096, 4096))
+    o, state = gdr.chunk_prefill(...)                                          # the delta rule
+    q8, s8 = gdr.gated_rmsnorm_i8(o, z, head_norm_w)                           # codes for the way out
+    y = gdr.matmul_i8(q8, s8, w_out, w_out_scale)
+
+Activations and weights are int8 codes with an fp32 scale for each token and each output
+channel; residual stream, gate and outputs are bf16 or fp32.  Forward only.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+__all__ = ["add_rmsnorm_i8", "gated_rmsnorm_i8", "matmul_i8", "quantize_rows_i8", "NORM_MAX_COLS",
+           "MATMUL_I8_MAX_K", "MATMUL_I8_MAX_OUT"]
+
+NORM_MAX_COLS = 32768     # most values in one row of the norms
+MATMUL_I8_MAX_K = 131071  # longest reduction of matmul_i8
+MATMUL_I8_MAX_OUT = 8     # most separate outputs of one product
+_VP = ctypes.c_void_p
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("heads", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64)]
+
+
+class MatmulDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("K", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("out_cols", ctypes.c_int32 * MATMUL_I8_MAX_OUT),
+                ("out_stride", ctypes.c_int64 * MATMUL_I8_MAX_OUT), ("a_stride", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64)]
+
+
+_CODE = {torch.bfloat16: 0, torch.float32: 1}
+_bound = None
+
+
+def bind(L):
+    """Argument types of the entry points of gdr_i8.h on the loaded library."""
+    L.gdr_add_rmsnorm_i8.restype = ctypes.c_int
+    L.gdr_add_rmsnorm_i8.argtypes = [_VP] * 8
+    L.gdr_gated_rmsnorm_i8.restype = ctypes.c_int
+    L.gdr_gated_rmsnorm_i8.argtypes = [_VP] * 7
+    L.gdr_matmul_i8.restype = ctypes.c_int
+    L.gdr_matmul_i8.argtypes = [_VP] * 8
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        import gated_delta_rule_70_amd as gdr
+
+        _bound = gdr.lib()
+    return _bound
+
+
+def _check(status):
+    if status != 0:
+        import gated_delta_rule_70_amd as gdr
+
+        raise gdr.GdrError(status, _lib().gdr_status_str(status).decode())
+
+
+def _code(t, name):
+    c = _CODE.get(t.dtype)
+    if c is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return c
+
+
+def _device(stream, **tensors):
+    """All tensors on the current GPU; returns the stream's handle."""
+    at = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.get_device() != at:
+            raise ValueError(f"{name} is on GPU {t.get_device()}, the current one is {at}")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _rows(t, name, tail=1):
+    """Elements from one row to the next of ``t``, whose last ``tail`` dimensions make a row: a
+    row's values have to lie next to each other, and the rows evenly apart."""
+    shape, strides = t.shape, t.stride()
+    lead = len(shape) - tail
+    step = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and strides[i] != step:
+            raise ValueError(f"{name}: the values of a row must be contiguous")
+        step *= shape[i]
+    row = None
+    want = 0
+    for i in range(lead - 1, -1, -1):
+        if shape[i] == 1:
+            continue
+        if row is None:
+            row = strides[i]
+        elif strides[i] != want and t.numel():
+            raise ValueError(f"{name}: rows must be evenly spaced")
+        want = strides[i] * shape[i]
+    return step if row is None or t.numel() == 0 else row
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != torch.Size(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _eps(eps):
+    if not (eps >= 0 and math.isfinite(eps)):
+        raise ValueError(f"eps must be finite and not negative, got {eps}")
+    return eps
+
+
+def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=None, out_residual=None, stream=None):
+    """Residual addition, root-mean-square norm, int8 codes (gdr_add_rmsnorm_i8).
+
+    ``x`` and ``residual`` are ``[..., D]`` (bf16 or fp32, rows evenly spaced), ``weight`` ``[D]``
+    (their type, or fp32).  With ``s = x + residual`` rounded to x's type, the norm of s times
+    weight is returned as ``q`` (int8, ``[..., D]``) and ``scale`` (fp32, ``[...]``): it stands
+    for ``q * scale[..., None]``.  Returns ``(q, scale, s)``; s is written to ``out_residual``
+    (which may be ``x`` or ``residual`` itself), and is None without a residual.  A row of
+    zeros has scale 0, a row that holds NaN or infinity scale NaN and q 0.
+    """
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must be [..., D], got {list(x.shape)}")
+    D = x.shape[-1]
+    if D > NORM_MAX_COLS:
+        raise ValueError(f"x has {D} values in a row, at most {NORM_MAX_COLS} are supported")
+    xc = _code(x, "x")
+    if weight.shape != x.shape[-1:]:
+        raise ValueError(f"weight must be {[D]}, got {list(weight.shape)}")
+    if weight.dtype != x.dtype and weight.dtype != torch.float32:
+        raise TypeError(f"weight must be {x.dtype} or float32, got {weight.dtype}")
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    if residual is None:
+        if out_residual is not None:
+            raise ValueError("out_residual is given without a residual")
+    elif residual.shape != x.shape:
+        raise ValueError(f"residual must be {list(x.shape)}, got {list(residual.shape)}")
+    elif residual.dtype != x.dtype:
+        raise TypeError(f"residual must be {x.dtype}, got {residual.dtype}")
+    if out_residual is not None:
+        if out_residual.shape != x.shape:
+            raise ValueError(f"out_residual must be {list(x.shape)}, got {list(out_residual.shape)}")
+        if out_residual.dtype != x.dtype:
+            raise TypeError(f"out_residual must be {x.dtype}, got {out_residual.dtype}")
+    elif residual is not None:
+        out_residual = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    q = _out(q, "q", x.shape, torch.int8, x.device)
+    scale = _out(scale, "scale", x.shape[:-1], torch.float32, x.device)
+    d = NormDims(scale.numel(), 1, D, xc, 0, _CODE[weight.dtype], _eps(eps), _rows(x, "x"),
+                 0 if residual is None else _rows(residual, "residual"),
+                 0 if out_residual is None else _rows(out_residual, "out_residual"))
+    s = _device(stream, x=x, weight=weight, residual=residual, q=q, scale=scale, out_residual=out_residual)
+    _check(_lib().gdr_add_rmsnorm_i8(ctypes.addressof(d), x.data_ptr(), _ptr(residual), weight.data_ptr(),
+                                     q.data_ptr(), scale.data_ptr(), _ptr(out_residual), s))
+    return q, scale, out_residual
+
+
+def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, stream=None):
+    """Norm of each value head of ``o``, times ``weight`` and silu(``gate``), as int8 codes with a
+    scale for each token (gdr_gated_rmsnorm_i8).
+
+    ``o`` and ``gate`` are ``[..., HV, dv]`` (bf16 or fp32 each; dv 32, 64 or 128), ``weight``
+    ``[dv]`` (bf16 or fp32).  Returns ``q`` (int8, ``[..., HV * dv]``) and ``scale`` (fp32, ``[...]``).
+    """
+    if o.dim() < 2:
+        raise ValueError(f"o must be [..., HV, dv], got {list(o.shape)}")
+    H, V = o.shape[-2], o.shape[-1]
+    if V not in (32, 64, 128):
+        raise ValueError(f"dv must be 32, 64 or 128, got {V}")
+    if H < 1 or H * V > NORM_MAX_COLS:
+        raise ValueError(f"HV * dv must be in 1 .. {NORM_MAX_COLS}, got {H * V}")
+    if gate.shape != o.shape:
+        raise ValueError(f"gate must be {list(o.shape)}, got {list(gate.shape)}")
+    if weight.shape != o.shape[-1:]:
+        raise ValueError(f"weight must be {[V]}, got {list(weight.shape)}")
+    codes = _code(o, "o"), _code(gate, "gate"), _code(weight, "weight")
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    lead = o.shape[:-2]
+    q = _out(q, "q", (*lead, H * V), torch.int8, o.device)
+    scale = _out(scale, "scale", lead, torch.float32, o.device)
+    d = NormDims(scale.numel(), H, V, *codes, _eps(eps), _rows(o, "o", 2), _rows(gate, "gate", 2), 0)
+    s = _device(stream, o=o, gate=gate, weight=weight, q=q, scale=scale)
+    _check(_lib().gdr_gated_rmsnorm_i8(ctypes.addressof(d), o.data_ptr(), gate.data_ptr(), weight.data_ptr(),
+                                       q.data_ptr(), scale.data_ptr(), s))
+    return q, scale
+
+
+def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """``(a @ w.T) * a_scale[..., None] * w_scale (+ bias)`` for int8 codes (gdr_matmul_i8).
+
+    ``a`` is ``[..., K]`` and ``w`` ``[N, K]`` (int8, rows evenly spaced), ``a_scale`` ``[...]``,
+    ``w_scale`` and ``bias`` ``[N]`` (fp32).  The sum is exact; ``out_dtype`` is bf16 or fp32.
+
+    ``out`` says where the columns go: None for one new tensor ``[..., N]``, a tensor for one
+    output, a sequence of column counts for that many new tensors, or a sequence of tensors (of
+    one type; their rows may be strided).  Returns a tensor, or a tuple for a sequence.
+    """
+    if a.dim() < 1 or w.dim() != 2 or a.shape[-1] != w.shape[1]:
+        raise ValueError(f"a must be [..., K] and w [N, K], got {list(a.shape)} and {list(w.shape)}")
+    lead, (N, K) = a.shape[:-1], w.shape
+    if N < 1 or not 1 <= K <= MATMUL_I8_MAX_K:
+        raise ValueError(f"N must be at least 1 and K in 1 .. {MATMUL_I8_MAX_K}, got N={N} K={K}")
+    for t, name in ((a, "a"), (w, "w")):
+        if t.dtype != torch.int8:
+            raise TypeError(f"{name} must be int8, got {t.dtype}")
+    for t, name, shape in ((a_scale, "a_scale", lead), (w_scale, "w_scale", (N,)), (bias, "bias", (N,))):
+        if t is None:
+            if name == "bias":
+                continue
+            raise TypeError(f"{name} is required")
+        if t.shape != torch.Size(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    single = out is None or isinstance(out, torch.Tensor)
+    outs = (N,) if out is None else (out,) if single else tuple(out)
+    if not 1 <= len(outs) <= MATMUL_I8_MAX_OUT:
+        raise ValueError(f"1 to {MATMUL_I8_MAX_OUT} outputs are supported, got {len(outs)}")
+    cols = [t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() else t for t in outs]
+    if not all(isinstance(c, int) and c >= 1 for c in cols) or sum(cols) != N:
+        raise ValueError(f"the outputs' columns {cols} must be positive and add up to {N}")
+    outs = tuple(t if isinstance(t, torch.Tensor) else torch.empty(*lead, t, dtype=out_dtype, device=a.device)
+                 for t in outs)
+    oc = _code(outs[0], "out")
+    d = MatmulDims(a_scale.numel(), K, len(outs), oc)
+    for i, t in enumerate(outs):
+        if t.shape[:-1] != lead:
+            raise ValueError(f"out must be {[*lead, cols[i]]}, got {list(t.shape)}")
+        if t.dtype != outs[0].dtype:
+            raise TypeError(f"outputs must be of one type, got {outs[0].dtype} and {t.dtype}")
+        d.out_cols[i] = cols[i]
+        d.out_stride[i] = _rows(t, "out")
+    d.a_stride, d.w_stride = _rows(a, "a"), _rows(w, "w")
+    s = _device(stream, a=a, a_scale=a_scale, w=w, w_scale=w_scale, bias=bias,
+                **{f"out[{i}]": t for i, t in enumerate(outs)})
+    ptrs = (_VP * len(outs))(*[t.data_ptr() for t in outs])
+    _check(_lib().gdr_matmul_i8(ctypes.addressof(d), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
+                                w_scale.data_ptr(), _ptr(bias), ctypes.addressof(ptrs), s))
+    return outs[0] if single else outs
+
+
+def quantize_rows_i8(w):
+    """int8 codes and fp32 scales of a weight matrix ``[N, K]``, a scale for each row (ties to
+    even; a row of zeros has scale 0).  For preparing weights once; plain tensor operations on
+    w's device."""
+    if w.dim() != 2 or not w.is_floating_point():
+        raise ValueError(f"w must be a floating point matrix [N, K], got {list(w.shape)} {w.dtype}")
+    top = w.double().abs().amax(1)
+    codes = torch.round(w.double() * 127.0 / torch.where(top > 0, top, 1.0)[:, None])
+    return codes.to(torch.int8), (top / 127.0).float()
