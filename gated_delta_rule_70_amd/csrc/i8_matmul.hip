@@ -89,51 +89,297 @@ __device__ __forceinline__ void store_quad(const MatmulArgs& g, int m, int n, i3
         }
 }
 
-// One workgroup of 4 waves makes 64 x 64 outputs, each wave 32 x 32; 64 reduction bytes at a
-// time through LDS.
-template <bool BF16>
-__global__ __launch_bounds__(256) void matmul_i8_kernel(MatmulArgs g) {
-    __shared__ i32x4 sa[64 * 4], sw[64 * 4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int tiles_n = (g.N + 63) / 64;
-    const int m0 = (int)(blockIdx.x / tiles_n) * 64, n0 = (int)(blockIdx.x % tiles_n) * 64;
-    const int row = tid >> 2, chunk = tid & 3;
-    const int8_t* pa = g.a + (m0 + row) * g.a_stride;
-    const int8_t* pw = g.w + (n0 + row) * g.w_stride;
-    i32x4 acc[2][2] = {};
-    for (int k = 0; k < g.K; k += 64) {
-        sa[row * 4 + chunk] = load16(pa, k + chunk * 16, g.K, m0 + row < g.M);
-        sw[row * 4 + chunk] = load16(pw, k + chunk * 16, g.K, n0 + row < g.N);
-        __syncthreads();
-        i32x4 fa[2], fw[2];
+// ---- few rows ---------------------------------------------------------------------------
+// One workgroup makes 16 * NT columns for up to 16 * MT rows.  Its 8 waves share the reduction,
+// 256 bytes in turn, each straight from memory to registers to the matrix cores: every weight is
+// read once and used at once, so nothing is gained by LDS; the sums meet there at the end.
+template <int MT, int NT, bool BF16>
+__global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
+    constexpr int WAVES = 8, U = 4, STEP = 64 * U;
+    __shared__ i32x4 part[WAVES][MT * NT * 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n0 = blockIdx.x * (16 * NT), kq = (lane >> 4) * 16;
+    const int8_t *pw[NT], *pa[MT];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            fa[i] = sa[((wave >> 1) * 32 + i * 16 + (lane & 15)) * 4 + (lane >> 4)];
-            fw[i] = sw[((wave & 1) * 32 + i * 16 + (lane & 15)) * 4 + (lane >> 4)];
+    for (int j = 0; j < NT; ++j) pw[j] = g.w + min(n0 + j * 16 + (lane & 15), g.N - 1) * g.w_stride;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) pa[i] = g.a + min(i * 16 + (lane & 15), g.M - 1) * g.a_stride;
+    i32x4 acc[MT][NT] = {};
+    for (int k0 = wave * STEP; k0 < g.K; k0 += WAVES * STEP) {
+        i32x4 fw[U][NT], fa[U][MT];
+        if (k0 + STEP <= g.K) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) __builtin_memcpy(&fw[u][j], pw[j] + k0 + u * 64 + kq, 16);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) __builtin_memcpy(&fa[u][i], pa[i] + k0 + u * 64 + kq, 16);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) fw[u][j] = load16(pw[j], k0 + u * 64 + kq, g.K, true);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) fa[u][i] = load16(pa[i], k0 + u * 64 + kq, g.K, true);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8(fw[j], fa[i], acc[i][j]);
-        __syncthreads();
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[i][j] = mfma_i8(fw[u][j], fa[u][i], acc[i][j]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            store_quad<BF16>(g, m0 + (wave >> 1) * 32 + i * 16 + (lane & 15),
-                             n0 + (wave & 1) * 32 + j * 16 + (lane >> 4) * 4, acc[i][j]);
+        for (int j = 0; j < NT; ++j) part[wave][(i * NT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < MT * NT * 64; e += WAVES * 64) {
+        i32x4 s = part[0][e];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) s += part[w][e];
+        const int tile = e >> 6, l = e & 63;
+        store_quad<BF16>(g, (tile / NT) * 16 + (l & 15), n0 + (tile % NT) * 16 + (l >> 4) * 4, s);
+    }
+}
+
+// ---- tiles ------------------------------------------------------------------------------
+// One workgroup of WM x WN waves makes BM x BN outputs, 128 reduction bytes at a time through
+// STAGES buffers in LDS.  A row's 128 bytes are 8 chunks of 16; chunk c of row r sits at place
+// c ^ (r % 8), which spreads the 16 rows that a fragment reads over all banks.
+//   DMA   memory to LDS without registers (16 bytes a lane): pointers and row strides are
+//         multiples of 16 and a tile's rows lie within 2^31 bytes;
+//   else  through registers, at any alignment, a stage ahead.
+// Rows past the end repeat the last one (their results are dropped); the reduction's last
+// partial 128 bytes go through registers, with zeros behind them.
+constexpr int kBK = 128;
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+    asm volatile("" ::: "memory");
+}
+
+// 16 bytes a lane from r at voff + soff to LDS at `to` + 16 * lane, without registers.
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ void copy_to_lds(rsrc_t r, i32x4* to, int voff, int soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, voff, soff, 0, 0);
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool DMA, bool BF16>
+__global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, int m_base) {
+    constexpr int NT = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int LA = BM * 8 / NT, LW = BN * 8 / NT;
+    static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && TM >= 1 && TN >= 1);
+    __shared__ __align__(1024) i32x4 lds[STAGES][(BM + BN) * 8];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // Workgroups are dealt to the 8 XCDs in turn: give each XCD a run of neighbouring tiles, and
+    // lay a run out 8 tiles high, so that the tiles an XCD works on at a time share operands in
+    // its L2.
+    const int tiles_m = (g.M - m_base + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
+    const int total = tiles_m * tiles_n;
+    const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
+    const int id = xcd * (total >> 3) + min(xcd, total & 7) + nth;
+    const int band = id / (8 * tiles_n), in_band = id - band * 8 * tiles_n;
+    const int high = min(8, tiles_m - band * 8);
+    const int m0 = m_base + (band * 8 + in_band % high) * BM, n0 = in_band / high * BN;
+
+    const int last_m = min(BM, g.M - m0) - 1, last_n = min(BN, g.N - n0) - 1;
+    const int8_t* ga = g.a + m0 * g.a_stride;
+    const int8_t* gw = g.w + n0 * g.w_stride;
+    // chunk of 16 bytes that this thread brings with its load i: LDS place i * NT + tid
+    const int row = tid >> 3, chunk = (tid & 7) ^ (row & 7);
+    static_assert(NT % 64 == 0);
+
+    const int full = g.K / kBK;
+    int va[LA], vw[LW];
+    rsrc_t ra, rw;
+    if constexpr (DMA) {
+        ra = make_rsrc(ga, (uint32_t)(last_m * g.a_stride + g.K));
+        rw = make_rsrc(gw, (uint32_t)(last_n * g.w_stride + g.K));
+#pragma unroll
+        for (int i = 0; i < LA; ++i) va[i] = min(row + i * (NT / 8), last_m) * (int)g.a_stride + chunk * 16;
+#pragma unroll
+        for (int i = 0; i < LW; ++i) vw[i] = min(row + i * (NT / 8), last_n) * (int)g.w_stride + chunk * 16;
+    }
+    i32x4 hold[DMA ? 1 : LA + LW];
+    auto fetch = [&](int s) {
+        const int k = s * kBK;
+        if constexpr (DMA) {
+            i32x4* to = &lds[s % STAGES][wave * 64];
+#pragma unroll
+            for (int i = 0; i < LA; ++i) copy_to_lds(ra, to + i * NT, va[i], k);
+#pragma unroll
+            for (int i = 0; i < LW; ++i) copy_to_lds(rw, to + BM * 8 + i * NT, vw[i], k);
+        } else {
+#pragma unroll
+            for (int i = 0; i < LA; ++i)
+                __builtin_memcpy(&hold[i], ga + min(row + i * (NT / 8), last_m) * g.a_stride + (k + chunk * 16), 16);
+#pragma unroll
+            for (int i = 0; i < LW; ++i)
+                __builtin_memcpy(&hold[LA + i], gw + min(row + i * (NT / 8), last_n) * g.w_stride + (k + chunk * 16), 16);
+        }
+    };
+    auto put = [&](int s) {
+        if constexpr (!DMA) {
+#pragma unroll
+            for (int i = 0; i < LA; ++i) lds[s % STAGES][i * NT + tid] = hold[i];
+#pragma unroll
+            for (int i = 0; i < LW; ++i) lds[s % STAGES][BM * 8 + i * NT + tid] = hold[LA + i];
+        }
+    };
+
+    i32x4 acc[TM][TN] = {};
+    const int wm = wave / WN, wn = wave % WN;
+    // place of this lane's chunk of a fragment: row lane % 16, chunk lane / 16 (+ 4 for the second
+    // half of the 128 bytes)
+    const int place = (lane & 15) * 8 + ((lane >> 4) ^ (lane & 7));
+    auto compute = [&](int s) {
+        const i32x4* A = &lds[s % STAGES][wm * (TM * 128)];
+        const i32x4* W = &lds[s % STAGES][BM * 8 + wn * (TN * 128)];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            i32x4 fa[TM], fw[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fw[j] = W[j * 128 + (place ^ (h * 4))];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[i] = A[i * 128 + (place ^ (h * 4))];
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma_i8(fw[j], fa[i], acc[i][j]);
+        }
+    };
+
+    if constexpr (DMA) {
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < full) fetch(s);
+        for (int s = 0; s < full; ++s) {
+            if (s + STAGES - 2 < full)
+                wait_vmcnt<(STAGES - 2) * (LA + LW)>();
+            else
+                wait_vmcnt<0>();
+            lds_barrier();  // stage s is there for all; all are done with stage s - 1
+            if (s + STAGES - 1 < full) fetch(s + STAGES - 1);
+            compute(s);
+        }
+    } else {
+        if (full > 0) {
+            fetch(0);
+            put(0);
+        }
+        for (int s = 0; s < full; ++s) {
+            lds_barrier();
+            if (s + 1 < full) fetch(s + 1);
+            compute(s);
+            if (s + 1 < full) put(s + 1);
+        }
+    }
+    if (g.K % kBK != 0) {
+        const int s = full, k = full * kBK;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            lds[s % STAGES][i * NT + tid] =
+                load16(ga + min(row + i * (NT / 8), last_m) * g.a_stride, k + chunk * 16, g.K, true);
+#pragma unroll
+        for (int i = 0; i < LW; ++i)
+            lds[s % STAGES][BM * 8 + i * NT + tid] =
+                load16(gw + min(row + i * (NT / 8), last_n) * g.w_stride, k + chunk * 16, g.K, true);
+        __syncthreads();
+        compute(s);
+    }
+
+    // A lane holds columns nq .. nq+3 of rows lane % 16.
+    float sa[TM];
+    const int mr = m0 + wm * (TM * 16) + (lane & 15), nr = n0 + wn * (TN * 16) + (lane >> 4) * 4;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa[i] = g.a_scale[min(mr + i * 16, g.M - 1)];
+    constexpr int E = BF16 ? 2 : 4;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        const int n = nr + j * 16;
+        if (n >= g.N) continue;
+        f32x4 sw, bias = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            sw[c] = g.w_scale[min(n + c, g.N - 1)];
+            if (g.bias) bias[c] = g.bias[min(n + c, g.N - 1)];
+        }
+        if (g.out.quad && n + 4 <= g.N) {
+            const Where to = where(g.out, n, E);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int m = mr + i * 16;
+                if (m >= g.M) continue;
+                f32x4 v;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = (float)acc[i][j][c] * sa[i] * sw[c] + bias[c];
+                char* p = to.p + m * to.stride * E;
+                if constexpr (BF16)
+                    *reinterpret_cast<u32x2*>(p) = bf16x4_bits(v);
+                else
+                    *reinterpret_cast<f32x4*>(p) = v;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (n + c >= g.N) continue;
+                const Where to = where(g.out, n + c, E);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int m = mr + i * 16;
+                    if (m < g.M) store_value<BF16>(to.p + m * to.stride * E, (float)acc[i][j][c] * sa[i] * sw[c] + bias[c]);
+                }
+            }
+        }
+    }
+}
+
+template <int MT, int NT>
+void rows(const MatmulArgs& g) {
+    const dim3 grid((unsigned)((g.N + 16 * NT - 1) / (16 * NT)));
+    if (g.out_bf16)
+        hipLaunchKernelGGL((matmul_rows_kernel<MT, NT, true>), grid, dim3(512), 0, g.stream, g);
+    else
+        hipLaunchKernelGGL((matmul_rows_kernel<MT, NT, false>), grid, dim3(512), 0, g.stream, g);
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool DMA>
+void tiles(const MatmulArgs& g, int m_base) {
+    const dim3 grid((unsigned)(((int64_t)(g.M - m_base) + BM - 1) / BM * ((g.N + BN - 1) / BN)));
+    if (g.out_bf16)
+        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, true>), grid, dim3(WM * WN * 64), 0, g.stream, g, m_base);
+    else
+        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, false>), grid, dim3(WM * WN * 64), 0, g.stream, g, m_base);
+}
+
+bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows == 1 || stride % 16 == 0) &&
+           255 * stride + K < (int64_t(1) << 31);
 }
 
 }  // namespace
 
 hipError_t launch_matmul_i8(const MatmulArgs& g) {
     if (g.M < 1 || g.N < 1 || g.K < 1 || g.K > GDR_MATMUL_I8_MAX_K) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)((g.M + 63LL) / 64 * ((g.N + 63) / 64)));
-    if (g.out_bf16)
-        hipLaunchKernelGGL(matmul_i8_kernel<true>, grid, dim3(256), 0, g.stream, g);
+    const bool dma = dma_ok(g.a, g.a_stride, g.M, g.K) && dma_ok(g.w, g.w_stride, g.N, g.K);
+    if (g.M <= 16)
+        rows<1, 1>(g);
+    else if (g.M <= 32)
+        rows<2, 1>(g);
+    else if (g.M <= 64)
+        rows<4, 1>(g);
+    else if ((int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256) >= 200)
+        dma ? tiles<256, 256, 2, 4, 2, true>(g, 0) : tiles<256, 256, 2, 4, 2, false>(g, 0);
     else
-        hipLaunchKernelGGL(matmul_i8_kernel<false>, grid, dim3(256), 0, g.stream, g);
+        dma ? tiles<128, 128, 2, 2, 2, true>(g, 0) : tiles<128, 128, 2, 2, 2, false>(g, 0);
     return hipGetLastError();
 }
 
