@@ -3,6 +3,8 @@
 // Sums are int32 in the matrix cores (v_mfma_i32_16x16x64_i8), exact for K <= 131071.
 #include "i8_launch.h"
 
+#include <type_traits>
+
 #include "gdr_device.h"
 
 namespace gdr {
@@ -169,6 +171,18 @@ __device__ __forceinline__ void copy_to_lds(rsrc_t r, i32x4* to, int voff, int s
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, voff, soff, 0, 0);
 }
 
+// Order of issue: MF matrix products with R LDS reads and L copies to LDS spread among them.
+template <int MF, int R, int L, int I = 0>
+__device__ __forceinline__ void interleave() {
+    if constexpr (I < R) {
+        constexpr int mf = (I + 1) * MF / R - I * MF / R, ld = (I + 1) * L / R - I * L / R;
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, mf, 0);
+        if constexpr (ld > 0) __builtin_amdgcn_sched_group_barrier(0x020, ld, 0);
+        interleave<MF, R, L, I + 1>();
+    }
+}
+
 template <int BM, int BN, int WM, int WN, int STAGES, bool DMA, bool BF16>
 __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, int m_base) {
     constexpr int NT = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -239,35 +253,75 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, 
     // place of this lane's chunk of a fragment: row lane % 16, chunk lane / 16 (+ 4 for the second
     // half of the 128 bytes)
     const int place = (lane & 15) * 8 + ((lane >> 4) ^ (lane & 7));
-    auto compute = [&](int s) {
+    struct Frags {
+        i32x4 a[TM], w[TN];
+    };
+    auto read = [&](int s, int h, Frags& f) {
         const i32x4* A = &lds[s % STAGES][wm * (TM * 128)];
         const i32x4* W = &lds[s % STAGES][BM * 8 + wn * (TN * 128)];
 #pragma unroll
+        for (int j = 0; j < TN; ++j) f.w[j] = W[j * 128 + (place ^ (h * 4))];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) f.a[i] = A[i * 128 + (place ^ (h * 4))];
+    };
+    auto multiply = [&](const Frags& f) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma_i8(f.w[j], f.a[i], acc[i][j]);
+    };
+    auto compute = [&](int s) {
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-            i32x4 fa[TM], fw[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) fw[j] = W[j * 128 + (place ^ (h * 4))];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = A[i * 128 + (place ^ (h * 4))];
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma_i8(fw[j], fa[i], acc[i][j]);
+            Frags f;
+            read(s, h, f);
+            multiply(f);
         }
     };
 
     if constexpr (DMA) {
+        // Two sets of fragments: while one half of a stage is multiplied the next half is read
+        // from LDS, also across stages: the barrier that frees stage s (everyone has read it) and
+        // opens stage s + 1 stands between the halves of stage s.
+        constexpr int L = LA + LW, MF = TM * TN, RD = TM + TN;
+        Frags f0, f1;
+        auto step = [&](int s, auto more, auto next) {
+            read(s, 1, f1);
+            multiply(f0);
+            interleave<MF, RD, 0>();
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (decltype(next)::value) {
+                if constexpr (decltype(more)::value)
+                    wait_vmcnt<(STAGES - 2) * L>();
+                else
+                    wait_vmcnt<0>();
+                lds_barrier();
+                if constexpr (decltype(more)::value) fetch(s + STAGES);
+                read(s + 1, 0, f0);
+            }
+            multiply(f1);
+            if constexpr (decltype(more)::value)
+                interleave<MF, RD, L>();
+            else if constexpr (decltype(next)::value)
+                interleave<MF, RD, 0>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        using yes = std::true_type;
+        using no = std::false_type;
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
+        for (int s = 0; s < STAGES; ++s)
             if (s < full) fetch(s);
-        for (int s = 0; s < full; ++s) {
-            if (s + STAGES - 2 < full)
-                wait_vmcnt<(STAGES - 2) * (LA + LW)>();
-            else
-                wait_vmcnt<0>();
-            lds_barrier();  // stage s is there for all; all are done with stage s - 1
-            if (s + STAGES - 1 < full) fetch(s + STAGES - 1);
-            compute(s);
+        if (full >= STAGES)
+            wait_vmcnt<(STAGES - 1) * L>();
+        else
+            wait_vmcnt<0>();
+        lds_barrier();
+        if (full > 0) {
+            read(0, 0, f0);
+            int s = 0;
+            for (; s + STAGES < full; ++s) step(s, yes{}, yes{});
+            for (; s + 1 < full; ++s) step(s, no{}, yes{});
+            step(s, no{}, no{});
         }
     } else {
         if (full > 0) {
@@ -296,47 +350,72 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, 
         compute(s);
     }
 
-    // A lane holds columns nq .. nq+3 of rows lane % 16.
+    // Outputs leave through LDS, each wave's block for itself, so that stores are whole lines: a
+    // lane's accumulators are four columns of each of TM rows, 32 bytes of a line at a time (stored
+    // straight, a 256 x 256 tile took 15 us longer).  Chunk c of 16 bytes of row r sits at place
+    // c ^ (r % CH).
+    constexpr int E = BF16 ? 2 : 4, CW = TN * 16, EB = CW * E, CH = EB / 16, PER = 16 / E;
+    constexpr int SPACE = STAGES * (BM + BN) * kBK / (WM * WN), RP = SPACE / EB < TM * 16 ? SPACE / EB / 16 * 16 : TM * 16;
+    static_assert(RP >= 16 && TM * 16 % RP == 0 && CW <= 64);
     float sa[TM];
-    const int mr = m0 + wm * (TM * 16) + (lane & 15), nr = n0 + wn * (TN * 16) + (lane >> 4) * 4;
+    f32x4 sw[TN], bias[TN];
+    const int mw = m0 + wm * (TM * 16), nw = n0 + wn * CW;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = g.a_scale[min(mr + i * 16, g.M - 1)];
-    constexpr int E = BF16 ? 2 : 4;
+    for (int i = 0; i < TM; ++i) sa[i] = g.a_scale[min(mw + i * 16 + (lane & 15), g.M - 1)];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        const int n = nr + j * 16;
-        if (n >= g.N) continue;
-        f32x4 sw, bias = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            sw[c] = g.w_scale[min(n + c, g.N - 1)];
-            if (g.bias) bias[c] = g.bias[min(n + c, g.N - 1)];
+            const int n = min(nw + j * 16 + (lane >> 4) * 4 + c, g.N - 1);
+            sw[j][c] = g.w_scale[n];
+            bias[j][c] = g.bias ? g.bias[n] : 0.f;
         }
-        if (g.out.quad && n + 4 <= g.N) {
-            const Where to = where(g.out, n, E);
+    const bool wide = g.out.wide;
+    const int col = wide ? lane % CH * PER : lane % CW;          // of this lane's stores
+    const int first = wide ? lane / CH : lane / CW;              // and its first row
+    const int step_r = wide ? 64 / CH : 64 / CW;
+    const bool on = nw + col < g.N;
+    const Where to = where(g.out, min(nw + col, g.N - 1), E);
+    char* mine = reinterpret_cast<char*>(&lds[0][0]) + wave * SPACE;
+    lds_barrier();
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int m = mr + i * 16;
-                if (m >= g.M) continue;
+    for (int pass = 0; pass < TM * 16 / RP; ++pass) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < RP / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int t = pass * (RP / 16) + i, r = i * 16 + (lane & 15), q = lane >> 4;
                 f32x4 v;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] = (float)acc[i][j][c] * sa[i] * sw[c] + bias[c];
-                char* p = to.p + m * to.stride * E;
-                if constexpr (BF16)
-                    *reinterpret_cast<u32x2*>(p) = bf16x4_bits(v);
-                else
-                    *reinterpret_cast<f32x4*>(p) = v;
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (n + c >= g.N) continue;
-                const Where to = where(g.out, n + c, E);
-#pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const int m = mr + i * 16;
-                    if (m < g.M) store_value<BF16>(to.p + m * to.stride * E, (float)acc[i][j][c] * sa[i] * sw[c] + bias[c]);
+                for (int c = 0; c < 4; ++c) v[c] = (float)acc[t][j][c] * sa[t] * sw[j][c] + bias[j][c];
+                const int c16 = BF16 ? j * 2 + (q >> 1) : j * 4 + q;
+                char* at = mine + r * EB + (c16 ^ (r & (CH - 1))) * 16;
+                if constexpr (BF16) {
+                    const u32x2 b = bf16x4_bits(v);
+                    __builtin_memcpy(__builtin_assume_aligned(at + (q & 1) * 8, 8), &b, 8);
+                } else {
+                    __builtin_memcpy(__builtin_assume_aligned(at, 16), &v, 16);
                 }
+            }
+        asm volatile("" ::: "memory");
+        const int rows = min(RP, g.M - mw - pass * RP);
+        if (!on) continue;
+        char* p = to.p + (int64_t)(mw + pass * RP + first) * to.stride * E;
+        for (int r = first; r < rows; r += step_r, p += step_r * to.stride * E) {
+            const char* at = mine + r * EB + (col / PER ^ (r & (CH - 1))) * 16;
+            if (wide) {
+                u32x4 x;
+                __builtin_memcpy(&x, __builtin_assume_aligned(at, 16), 16);
+                *reinterpret_cast<u32x4*>(p) = x;
+            } else if constexpr (BF16) {
+                uint16_t x;
+                __builtin_memcpy(&x, __builtin_assume_aligned(at + col % PER * E, 2), 2);
+                *reinterpret_cast<uint16_t*>(p) = x;
+            } else {
+                float x;
+                __builtin_memcpy(&x, __builtin_assume_aligned(at + col % PER * E, 4), 4);
+                *reinterpret_cast<float*>(p) = x;
             }
         }
     }
