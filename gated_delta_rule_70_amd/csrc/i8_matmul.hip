@@ -21,21 +21,26 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// 16 bytes at p + k, zeros from K on and where the row does not exist.  Any alignment.
-__device__ __forceinline__ i32x4 load16(const int8_t* p, int k, int K, bool row) {
-    i32x4 v = {0, 0, 0, 0};
-    if (!row || k >= K) return v;
-    if (k + 16 <= K) {
-        __builtin_memcpy(&v, p + k, 16);
-        return v;
+// 16 bytes at p + k of a row of K bytes, zeros from K on.  Any alignment.  A last partial chunk of
+// a row of at least 16 bytes is the row's last 16, shifted.
+__device__ __forceinline__ i32x4 load16(const int8_t* p, int k, int K) {
+    const int past = k + 16 - K;  // bytes of the chunk that lie behind the row
+    uint64_t lo = 0, hi = 0;
+    if (past <= 0) {
+        __builtin_memcpy(&lo, p + k, 8);
+        __builtin_memcpy(&hi, p + k + 8, 8);
+    } else if (past < 16 && K >= 16) {
+        __builtin_memcpy(&lo, p + (K - 16), 8);
+        __builtin_memcpy(&hi, p + (K - 8), 8);
+        const int sh = past * 8;
+        lo = sh < 64 ? lo >> sh | hi << (64 - sh) : hi >> (sh - 64);
+        hi = sh < 64 ? hi >> sh : 0;
+    } else if (past < 16) {
+#pragma unroll
+        for (int i = 0; i < 15; ++i)
+            if (i < K) (i < 8 ? lo : hi) |= static_cast<uint64_t>(static_cast<uint8_t>(p[i])) << (i % 8 * 8);
     }
-    uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 15; ++i)
-        if (k + i < K) u[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[k + i])) << (8 * (i % 4));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = static_cast<int>(u[i]);
-    return v;
+    return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
 }
 
 // Where the outputs of columns n .. n+3 go: for each column its output's first value of row 0
@@ -91,59 +96,44 @@ __device__ __forceinline__ void store_quad(const MatmulArgs& g, int m, int n, i3
         }
 }
 
-// ---- few rows ---------------------------------------------------------------------------
-// One workgroup makes 16 * NT columns for up to 16 * MT rows.  Its 8 waves share the reduction,
-// 256 bytes in turn, each straight from memory to registers to the matrix cores: every weight is
-// read once and used at once, so nothing is gained by LDS; the sums meet there at the end.
-template <int MT, int NT, bool BF16>
+// ---- up to 16 rows --------------------------------------------------------------------------
+// One workgroup makes 16 columns.  Its 8 waves share the reduction, 256 bytes in turn, each
+// straight from memory to registers to the matrix cores: every weight is read once and used at
+// once, so nothing is gained by LDS; the sums meet there at the end.
+template <bool BF16>
 __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
     constexpr int WAVES = 8, U = 4, STEP = 64 * U;
-    __shared__ i32x4 part[WAVES][MT * NT * 64];
+    __shared__ i32x4 part[WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n0 = blockIdx.x * (16 * NT), kq = (lane >> 4) * 16;
-    const int8_t *pw[NT], *pa[MT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) pw[j] = g.w + min(n0 + j * 16 + (lane & 15), g.N - 1) * g.w_stride;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) pa[i] = g.a + min(i * 16 + (lane & 15), g.M - 1) * g.a_stride;
-    i32x4 acc[MT][NT] = {};
+    const int n0 = blockIdx.x * 16, kq = (lane >> 4) * 16;
+    const int8_t* pw = g.w + min(n0 + (lane & 15), g.N - 1) * g.w_stride;
+    const int8_t* pa = g.a + min(lane & 15, g.M - 1) * g.a_stride;
+    i32x4 acc = {};
     for (int k0 = wave * STEP; k0 < g.K; k0 += WAVES * STEP) {
-        i32x4 fw[U][NT], fa[U][MT];
+        i32x4 fw[U], fa[U];
         if (k0 + STEP <= g.K) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) __builtin_memcpy(&fw[u][j], pw[j] + k0 + u * 64 + kq, 16);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) __builtin_memcpy(&fa[u][i], pa[i] + k0 + u * 64 + kq, 16);
+                __builtin_memcpy(&fw[u], pw + k0 + u * 64 + kq, 16);
+                __builtin_memcpy(&fa[u], pa + k0 + u * 64 + kq, 16);
             }
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) fw[u][j] = load16(pw[j], k0 + u * 64 + kq, g.K, true);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) fa[u][i] = load16(pa[i], k0 + u * 64 + kq, g.K, true);
+                fw[u] = load16(pw, k0 + u * 64 + kq, g.K);
+                fa[u] = load16(pa, k0 + u * 64 + kq, g.K);
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = mfma_i8(fw[u][j], fa[u][i], acc[i][j]);
+        for (int u = 0; u < U; ++u) acc = mfma_i8(fw[u], fa[u], acc);
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) part[wave][(i * NT + j) * 64 + lane] = acc[i][j];
+    part[wave][lane] = acc;
     __syncthreads();
-    for (int e = threadIdx.x; e < MT * NT * 64; e += WAVES * 64) {
-        i32x4 s = part[0][e];
+    if (wave == 0) {
+        i32x4 s = part[0][lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) s += part[w][e];
-        const int tile = e >> 6, l = e & 63;
-        store_quad<BF16>(g, (tile / NT) * 16 + (l & 15), n0 + (tile % NT) * 16 + (l >> 4) * 4, s);
+        for (int w = 1; w < WAVES; ++w) s += part[w][lane];
+        store_quad<BF16>(g, lane & 15, n0 + (lane >> 4) * 4, s);
     }
 }
 
@@ -165,10 +155,22 @@ __device__ __forceinline__ void wait_vmcnt() {
     asm volatile("" ::: "memory");
 }
 
+// Workgroups are dealt to the 8 XCDs in turn; this numbering gives each XCD a run of neighbouring
+// tiles, whose shared operands then stay in its L2.
+__device__ __forceinline__ int tile_of_workgroup(int total) {
+    const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
+    return xcd * (total >> 3) + min(xcd, total & 7) + nth;
+}
+
 // 16 bytes a lane from r at voff + soff to LDS at `to` + 16 * lane, without registers.
 typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ void copy_to_lds(rsrc_t r, i32x4* to, int voff, int soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, voff, soff, 0, 0);
+}
+
+// The same from an address of each lane's own.
+__device__ __forceinline__ void copy_to_lds(const int8_t* from, i32x4* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void*)to, 16, 0, 0);
 }
 
 // Order of issue: MF matrix products with R LDS reads and L copies to LDS spread among them.
@@ -184,7 +186,7 @@ __device__ __forceinline__ void interleave() {
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool DMA, bool BF16>
-__global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, int m_base) {
+__global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) {
     constexpr int NT = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int LA = BM * 8 / NT, LW = BN * 8 / NT;
     static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && TM >= 1 && TN >= 1);
@@ -192,16 +194,13 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    // Workgroups are dealt to the 8 XCDs in turn: give each XCD a run of neighbouring tiles, and
-    // lay a run out 8 tiles high, so that the tiles an XCD works on at a time share operands in
-    // its L2.
-    const int tiles_m = (g.M - m_base + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
-    const int total = tiles_m * tiles_n;
-    const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
-    const int id = xcd * (total >> 3) + min(xcd, total & 7) + nth;
+    // an XCD's run of tiles is laid out 8 tiles high, so that those it works on at a time share
+    // rows of both operands
+    const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
+    const int id = tile_of_workgroup(gridDim.x);
     const int band = id / (8 * tiles_n), in_band = id - band * 8 * tiles_n;
     const int high = min(8, tiles_m - band * 8);
-    const int m0 = m_base + (band * 8 + in_band % high) * BM, n0 = in_band / high * BN;
+    const int m0 = (band * 8 + in_band % high) * BM, n0 = in_band / high * BN;
 
     const int last_m = min(BM, g.M - m0) - 1, last_n = min(BN, g.N - n0) - 1;
     const int8_t* ga = g.a + m0 * g.a_stride;
@@ -341,11 +340,11 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, 
 #pragma unroll
         for (int i = 0; i < LA; ++i)
             lds[s % STAGES][i * NT + tid] =
-                load16(ga + min(row + i * (NT / 8), last_m) * g.a_stride, k + chunk * 16, g.K, true);
+                load16(ga + min(row + i * (NT / 8), last_m) * g.a_stride, k + chunk * 16, g.K);
 #pragma unroll
         for (int i = 0; i < LW; ++i)
             lds[s % STAGES][BM * 8 + i * NT + tid] =
-                load16(gw + min(row + i * (NT / 8), last_n) * g.w_stride, k + chunk * 16, g.K, true);
+                load16(gw + min(row + i * (NT / 8), last_n) * g.w_stride, k + chunk * 16, g.K);
         __syncthreads();
         compute(s);
     }
@@ -421,22 +420,160 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g, 
     }
 }
 
-template <int MT, int NT>
+// ---- small tiles --------------------------------------------------------------------------
+// For products whose 256 x 256 tiles would leave most of the chip idle.  BM x BN outputs for a
+// workgroup; each wave makes a 32 x 32 block, and KG groups of waves share the reduction: a stage
+// is KG * 64 bytes of it, group k takes the k-th 64, and the groups' sums meet in LDS.  What bounds
+// these products is how fast a CU can bring its operands in, so the loop keeps STAGES - 1 stages
+// in flight (DMA), or REGS stages in registers (any alignment).
+template <int BM, int BN, int KG, int STAGES, int REGS, bool DMA, bool BF16>
+__global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_kernel(MatmulArgs g) {
+    constexpr int WN = BN / 32, WAVES = BM / 32 * WN * KG, NT = WAVES * 64;
+    constexpr int BK = KG * 64, CPR = BK / 16, ROWS = BM + BN, LD = ROWS * CPR / NT;
+    static_assert(KG >= 2 && ROWS * CPR % NT == 0 && NT % CPR == 0);
+    constexpr int BUFS = DMA ? STAGES : 2, RED = KG * BM * BN / 4;  // 16-byte places
+    __shared__ __align__(1024) i32x4 lds[BUFS * ROWS * CPR > RED ? BUFS * ROWS * CPR : RED];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // an XCD's tiles share columns of w, the larger operand in these products
+    const int tiles_m = (g.M + BM - 1) / BM;
+    const int id = tile_of_workgroup(gridDim.x);
+    const int m0 = id % tiles_m * BM, n0 = id / tiles_m * BN;
+    const int last_m = min(BM, g.M - m0) - 1, last_n = min(BN, g.N - n0) - 1;
+    const int8_t* ga = g.a + m0 * g.a_stride;
+    const int8_t* gw = g.w + n0 * g.w_stride;
+
+    // A row's CPR chunks of 16 bytes: chunk c of row r sits at place c ^ (r % 8) (CPR >= 8).
+    const int row = tid / CPR, chunk = (tid % CPR) ^ (row & 7);
+    static_assert(NT / CPR % 8 == 0, "rows of one thread's loads agree modulo 8");
+    const int full = g.K / BK;
+    auto source = [&](int i) {  // start of the row that this thread's load i brings a chunk of
+        const int r = row + i * (NT / CPR);
+        return r < BM ? ga + min(r, last_m) * g.a_stride : gw + min(r - BM, last_n) * g.w_stride;
+    };
+    const int8_t* src[LD];
+#pragma unroll
+    for (int i = 0; i < LD; ++i) src[i] = source(i) + chunk * 16;
+
+    i32x4 rest[LD];  // the last partial stage
+    const bool partial = g.K % BK != 0;
+    if (partial) {
+#pragma unroll
+        for (int i = 0; i < LD; ++i) rest[i] = load16(source(i), full * BK + chunk * 16, g.K);
+    }
+    i32x4 acc[2][2] = {};
+    const int kg = wave % KG, block = wave / KG, wm = block / WN, wn = block % WN;
+    const int place = (lane & 15) * CPR + ((kg * 4 + (lane >> 4)) ^ (lane & 7));
+    auto compute = [&](int buf) {
+        const i32x4* A = &lds[buf * ROWS * CPR + wm * 32 * CPR];
+        const i32x4* W = &lds[buf * ROWS * CPR + (BM + wn * 32) * CPR];
+        i32x4 fa[2], fw[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fw[i] = W[i * 16 * CPR + place], fa[i] = A[i * 16 * CPR + place];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8(fw[j], fa[i], acc[i][j]);
+    };
+    if constexpr (DMA) {
+        auto fetch = [&](int s, int buf) {
+#pragma unroll
+            for (int i = 0; i < LD; ++i)
+                copy_to_lds(src[i] + s * BK, &lds[buf * ROWS * CPR + i * NT + wave * 64]);
+        };
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < full) fetch(s, s);
+        int buf = 0;
+        for (int s = 0; s < full; ++s) {
+            if (s + STAGES - 2 < full)
+                wait_vmcnt<(STAGES - 2) * LD>();
+            else
+                wait_vmcnt<0>();
+            lds_barrier();
+            if (s + STAGES - 1 < full) fetch(s + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+            compute(buf);
+            buf = buf + 1 == STAGES ? 0 : buf + 1;
+        }
+    } else {
+        i32x4 hold[REGS][LD];
+        auto load = [&](int s, i32x4(&h)[LD]) {
+#pragma unroll
+            for (int i = 0; i < LD; ++i) __builtin_memcpy(&h[i], src[i] + s * BK, 16);
+        };
+        auto put = [&](const i32x4(&h)[LD], int buf) {
+#pragma unroll
+            for (int i = 0; i < LD; ++i) lds[buf * ROWS * CPR + i * NT + tid] = h[i];
+        };
+        static_assert(REGS % 2 == 0);
+#pragma unroll
+        for (int s = 0; s < REGS; ++s)
+            if (s < full) load(s, hold[s]);
+        if (full > 0) put(hold[0], 0);
+        for (int s = 0; s < full; s += REGS)
+#pragma unroll
+            for (int u = 0; u < REGS; ++u) {
+                if (s + u >= full) break;
+                lds_barrier();
+                if (s + u + REGS < full) load(s + u + REGS, hold[u]);
+                compute(u % 2);
+                if (s + u + 1 < full) put(hold[(u + 1) % REGS], (u + 1) % 2);
+            }
+    }
+    if (partial) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < LD; ++i) lds[i * NT + tid] = rest[i];
+        __syncthreads();
+        compute(0);
+    }
+
+    // Sums of the groups meet in LDS: BM x BN int32 each, a row's places of 4 columns exchanged by
+    // its number.
+    __syncthreads();
+    constexpr int QR = BN / 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = wm * 32 + i * 16 + (lane & 15), q = wn * 8 + j * 4 + (lane >> 4);
+            lds[kg * BM * QR + r * QR + (q ^ (r & 7))] = acc[i][j];
+        }
+    __syncthreads();
+    for (int e = tid; e < BM * QR; e += NT) {
+        const int r = e / QR, q = e % QR;
+        i32x4 sum = lds[r * QR + (q ^ (r & 7))];
+#pragma unroll
+        for (int k = 1; k < KG; ++k) sum += lds[k * BM * QR + r * QR + (q ^ (r & 7))];
+        store_quad<BF16>(g, m0 + r, n0 + q * 4, sum);
+    }
+}
+
 void rows(const MatmulArgs& g) {
-    const dim3 grid((unsigned)((g.N + 16 * NT - 1) / (16 * NT)));
+    const dim3 grid((unsigned)((g.N + 15) / 16));
     if (g.out_bf16)
-        hipLaunchKernelGGL((matmul_rows_kernel<MT, NT, true>), grid, dim3(512), 0, g.stream, g);
+        hipLaunchKernelGGL(matmul_rows_kernel<true>, grid, dim3(512), 0, g.stream, g);
     else
-        hipLaunchKernelGGL((matmul_rows_kernel<MT, NT, false>), grid, dim3(512), 0, g.stream, g);
+        hipLaunchKernelGGL(matmul_rows_kernel<false>, grid, dim3(512), 0, g.stream, g);
+}
+
+template <int BM, int BN, int KG, int STAGES, int REGS, bool DMA>
+void small(const MatmulArgs& g) {
+    const dim3 grid((unsigned)(((int64_t)g.M + BM - 1) / BM * ((g.N + BN - 1) / BN)));
+    constexpr int NT = BM / 32 * (BN / 32) * KG * 64;
+    if (g.out_bf16)
+        hipLaunchKernelGGL((matmul_small_kernel<BM, BN, KG, STAGES, REGS, DMA, true>), grid, dim3(NT), 0, g.stream, g);
+    else
+        hipLaunchKernelGGL((matmul_small_kernel<BM, BN, KG, STAGES, REGS, DMA, false>), grid, dim3(NT), 0, g.stream, g);
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool DMA>
-void tiles(const MatmulArgs& g, int m_base) {
-    const dim3 grid((unsigned)(((int64_t)(g.M - m_base) + BM - 1) / BM * ((g.N + BN - 1) / BN)));
+void tiles(const MatmulArgs& g) {
+    const dim3 grid((unsigned)(((int64_t)g.M + BM - 1) / BM * ((g.N + BN - 1) / BN)));
     if (g.out_bf16)
-        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, true>), grid, dim3(WM * WN * 64), 0, g.stream, g, m_base);
+        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, true>), grid, dim3(WM * WN * 64), 0, g.stream, g);
     else
-        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, false>), grid, dim3(WM * WN * 64), 0, g.stream, g, m_base);
+        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, false>), grid, dim3(WM * WN * 64), 0, g.stream, g);
 }
 
 bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
@@ -444,21 +581,86 @@ bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
            255 * stride + K < (int64_t(1) << 31);
 }
 
+// Form of a product and its expected time.  Up to 2048 tiles' worth of work the time is the number
+// of rounds over the 256 CUs times what a tile takes: a fixed part (filling the pipeline, storing)
+// and a part for each reduction byte, by how fast a CU brings BM + BN rows in (50 to 70 bytes a
+// ns) or, for 256 x 256, multiplies them.  Constants fitted to measurements, M x N x K in us:
+//                        32x64   64x32  128x64  128x128 (4 / 2 stages)  256x256
+//      32 x 12288 x 4096  11.9    12.7    14.5     17.3 /  22.5           42.2
+//     128 x  4096 x 4096   9.8     9.6    13.7     17.1 /  22.9           42.3
+//     512 x  4096 x 4096  24.0    23.9    16.1     19.2 /  24.1           44.5
+//    1024 x  4096 x 4096  48.5    44.9    24.6     21.1 /  26.2           46.1
+//     512 x 12288 x 4096  62.1    62.2    35.6     36.9 /  32.1           50.0
+//    2048 x  4096 x 4096  97.2   146.8    46.6     41.2 /  35.8           50.5
+//    4096 x  4096 x 1024  71.9    70.6    32.5     29.8 /  25.2           23.6
+//    8192 x  2048 x 8192   335     598     192      158 /   142            118
+// Up to 16 rows and 8192 columns (128 tiles of 64 columns, half the CUs) the form without tiles is
+// faster: 1 x 4096 x 4096 6.5 against 8.8 us; 1 x 12288 x 4096 12.6 against 11.1.
+enum class Form { rows, t32x64, t64x32, t128x64, t128x128_deep, t128x128, t256x256 };
+struct Plan {
+    Form form;
+    double us;
+};
+Plan plan(int64_t M, int64_t N, int K) {
+    Plan best{Form::rows, M <= 16 && N <= 8192 ? 1.0 + 1.3e-3 * K : 1e30};
+    if (best.us < 1e30) return best;
+    auto offer = [&](Form f, int bm, int bn, int64_t least, int64_t most, double fixed, double per_k) {
+        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+        if (tiles < least || tiles > most) return;
+        const double rounds = tiles <= 1024 ? (double)((tiles + 255) / 256) : tiles / 256. + .5;
+        const double us = rounds * (fixed + per_k * K * 1e-3);
+        if (us < best.us) best = Plan{f, us};
+    };
+    constexpr int64_t any = int64_t(1) << 62;
+    offer(Form::t32x64, 32, 64, 1, any, 0.8, 1.9);
+    offer(Form::t64x32, 64, 32, 1, any, 0.8, 1.9);
+    offer(Form::t128x64, 128, 64, 1, any, 1.0, 2.8);
+    offer(Form::t128x128_deep, 128, 128, 1, 256, 1.8, 4.2);
+    offer(Form::t128x128, 128, 128, 257, any, 1.8, 3.6);
+    offer(Form::t256x256, 256, 256, 1, any, 9.0, 12.0);
+    return best;
+}
+
+template <bool DMA>
+void start(Form f, const MatmulArgs& g) {
+    switch (f) {
+        case Form::rows: rows(g); break;
+        case Form::t32x64: small<32, 64, 4, 3, 4, DMA>(g); break;
+        case Form::t64x32: small<64, 32, 4, 3, 4, DMA>(g); break;
+        case Form::t128x64: tiles<128, 64, 4, 2, 3, DMA>(g); break;
+        case Form::t128x128_deep: tiles<128, 128, 2, 4, DMA ? 4 : 2, DMA>(g); break;
+        case Form::t128x128: tiles<128, 128, 2, 4, 2, DMA>(g); break;
+        case Form::t256x256: tiles<256, 256, 2, 4, 2, DMA>(g); break;
+    }
+}
+
 }  // namespace
 
 hipError_t launch_matmul_i8(const MatmulArgs& g) {
     if (g.M < 1 || g.N < 1 || g.K < 1 || g.K > GDR_MATMUL_I8_MAX_K) return hipErrorInvalidValue;
     const bool dma = dma_ok(g.a, g.a_stride, g.M, g.K) && dma_ok(g.w, g.w_stride, g.N, g.K);
-    if (g.M <= 16)
-        rows<1, 1>(g);
-    else if (g.M <= 32)
-        rows<2, 1>(g);
-    else if (g.M <= 64)
-        rows<4, 1>(g);
-    else if ((int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256) >= 200)
-        dma ? tiles<256, 256, 2, 4, 2, true>(g, 0) : tiles<256, 256, 2, 4, 2, false>(g, 0);
-    else
-        dma ? tiles<128, 128, 2, 2, 2, true>(g, 0) : tiles<128, 128, 2, 2, 2, false>(g, 0);
+    const Plan whole = plan(g.M, g.N, g.K);
+    // A few rows past a multiple of 256 can cost a round of tiles more: they go into a launch of
+    // their own where that is expected to be faster (4097 x 12288 x 4096: 200 against 218 us).
+    const int rest = g.M % 256, head = g.M - rest;
+    if (head > 0 && rest > 0) {
+        const Plan first = plan(head, g.N, g.K), second = plan(rest, g.N, g.K);
+        if (first.us + second.us + 3.0 < whole.us) {
+            MatmulArgs a = g, b = g;
+            a.M = head;
+            b.M = rest;
+            b.a += head * g.a_stride;
+            b.a_scale += head;
+            for (int i = 0; i < g.out.n; ++i)
+                b.out.ptr[i] = static_cast<char*>(g.out.ptr[i]) + head * g.out.stride[i] * (g.out_bf16 ? 2 : 4);
+            dma ? start<true>(first.form, a) : start<false>(first.form, a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            dma ? start<true>(second.form, b) : start<false>(second.form, b);
+            return hipGetLastError();
+        }
+    }
+    dma ? start<true>(whole.form, g) : start<false>(whole.form, g);
     return hipGetLastError();
 }
 
