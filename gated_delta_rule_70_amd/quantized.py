@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -39,8 +40,18 @@ class MatmulDims(ctypes.Structure):
                 ("w_stride", ctypes.c_int64)]
 
 
+# The same layouts packed into bytes: a fraction of the time of filling a Structure, which counts
+# next to kernels of a few microseconds.
+_NORM = struct.Struct("@6if3q")
+_MATMUL = struct.Struct(f"@4i{MATMUL_I8_MAX_OUT}i{MATMUL_I8_MAX_OUT}q2q")
+_PTRS = struct.Struct(f"@{MATMUL_I8_MAX_OUT}Q")
+assert _NORM.size == ctypes.sizeof(NormDims) and _MATMUL.size == ctypes.sizeof(MatmulDims)
+
 _CODE = {torch.bfloat16: 0, torch.float32: 1}
-_bound = None
+_F32, _I8 = torch.float32, torch.int8
+# the current stream's handle without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_L = None
 
 
 def bind(L):
@@ -54,19 +65,18 @@ def bind(L):
 
 
 def _lib():
-    global _bound
-    if _bound is None:
+    global _L
+    if _L is None:
         import gated_delta_rule_70_amd as gdr
 
-        _bound = gdr.lib()
-    return _bound
+        _L = gdr.lib()
+    return _L
 
 
-def _check(status):
-    if status != 0:
-        import gated_delta_rule_70_amd as gdr
+def _fail(status):
+    import gated_delta_rule_70_amd as gdr
 
-        raise gdr.GdrError(status, _lib().gdr_status_str(status).decode())
+    raise gdr.GdrError(status, _lib().gdr_status_str(status).decode())
 
 
 def _code(t, name):
@@ -76,24 +86,30 @@ def _code(t, name):
     return c
 
 
-def _device(stream, **tensors):
-    """All tensors on the current GPU; returns the stream's handle."""
-    at = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
+def _stream(stream, dev, names, tensors):
+    """The stream's handle, once all tensors are known to be on the current GPU."""
+    for t in tensors:
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            break
+    else:
+        if dev == torch.cuda.current_device():
+            if stream is None:
+                return _raw_stream(dev)
+            return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    for name, t in zip(names, tensors):
+        if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor")
-        if t.get_device() != at:
+    at = torch.cuda.current_device()
+    for name, t in zip(names, tensors):
+        if t is not None and t.get_device() != at:
             raise ValueError(f"{name} is on GPU {t.get_device()}, the current one is {at}")
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t, name, tail=1):
     """Elements from one row to the next of ``t``, whose last ``tail`` dimensions make a row: a
     row's values have to lie next to each other, and the rows evenly apart."""
+    if t.is_contiguous():
+        return math.prod(t.shape[-tail:]) if tail > 1 else t.shape[-1]
     shape, strides = t.shape, t.stride()
     lead = len(shape) - tail
     step = 1
@@ -114,16 +130,12 @@ def _rows(t, name, tail=1):
     return step if row is None or t.numel() == 0 else row
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _out(t, name, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != torch.Size(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -131,7 +143,7 @@ def _out(t, name, shape, dtype, device):
 
 
 def _eps(eps):
-    if not (eps >= 0 and math.isfinite(eps)):
+    if not 0 <= eps <= 3.4028234663852886e38:
         raise ValueError(f"eps must be finite and not negative, got {eps}")
     return eps
 
@@ -146,40 +158,47 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
     (which may be ``x`` or ``residual`` itself), and is None without a residual.  A row of
     zeros has scale 0, a row that holds NaN or infinity scale NaN and q 0.
     """
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"x must be [..., D], got {list(x.shape)}")
-    D = x.shape[-1]
+    shape, dtype = x.shape, x.dtype
+    if not shape or shape[-1] < 1:
+        raise ValueError(f"x must be [..., D], got {list(shape)}")
+    D = shape[-1]
     if D > NORM_MAX_COLS:
         raise ValueError(f"x has {D} values in a row, at most {NORM_MAX_COLS} are supported")
     xc = _code(x, "x")
-    if weight.shape != x.shape[-1:]:
+    if weight.shape != (D,):
         raise ValueError(f"weight must be {[D]}, got {list(weight.shape)}")
-    if weight.dtype != x.dtype and weight.dtype != torch.float32:
-        raise TypeError(f"weight must be {x.dtype} or float32, got {weight.dtype}")
+    wt = weight.dtype
+    if wt is not dtype and wt is not _F32:
+        raise TypeError(f"weight must be {dtype} or float32, got {wt}")
     if not weight.is_contiguous():
         raise ValueError("weight must be contiguous")
+    r_stride = out_stride = 0
     if residual is None:
         if out_residual is not None:
             raise ValueError("out_residual is given without a residual")
-    elif residual.shape != x.shape:
-        raise ValueError(f"residual must be {list(x.shape)}, got {list(residual.shape)}")
-    elif residual.dtype != x.dtype:
-        raise TypeError(f"residual must be {x.dtype}, got {residual.dtype}")
-    if out_residual is not None:
-        if out_residual.shape != x.shape:
-            raise ValueError(f"out_residual must be {list(x.shape)}, got {list(out_residual.shape)}")
-        if out_residual.dtype != x.dtype:
-            raise TypeError(f"out_residual must be {x.dtype}, got {out_residual.dtype}")
-    elif residual is not None:
-        out_residual = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    q = _out(q, "q", x.shape, torch.int8, x.device)
-    scale = _out(scale, "scale", x.shape[:-1], torch.float32, x.device)
-    d = NormDims(scale.numel(), 1, D, xc, 0, _CODE[weight.dtype], _eps(eps), _rows(x, "x"),
-                 0 if residual is None else _rows(residual, "residual"),
-                 0 if out_residual is None else _rows(out_residual, "out_residual"))
-    s = _device(stream, x=x, weight=weight, residual=residual, q=q, scale=scale, out_residual=out_residual)
-    _check(_lib().gdr_add_rmsnorm_i8(ctypes.addressof(d), x.data_ptr(), _ptr(residual), weight.data_ptr(),
-                                     q.data_ptr(), scale.data_ptr(), _ptr(out_residual), s))
+    else:
+        if residual.shape != shape:
+            raise ValueError(f"residual must be {list(shape)}, got {list(residual.shape)}")
+        if residual.dtype is not dtype:
+            raise TypeError(f"residual must be {dtype}, got {residual.dtype}")
+        r_stride = _rows(residual, "residual")
+        if out_residual is None:
+            out_residual = torch.empty(shape, dtype=dtype, device=x.device)
+        if out_residual.shape != shape:
+            raise ValueError(f"out_residual must be {list(shape)}, got {list(out_residual.shape)}")
+        if out_residual.dtype is not dtype:
+            raise TypeError(f"out_residual must be {dtype}, got {out_residual.dtype}")
+        out_stride = _rows(out_residual, "out_residual")
+    q = _out(q, "q", shape, _I8, x.device)
+    scale = _out(scale, "scale", shape[:-1], _F32, x.device)
+    dims = _NORM.pack(scale.numel(), 1, D, xc, 0, _CODE[wt], _eps(eps), _rows(x, "x"), r_stride, out_stride)
+    s = _stream(stream, x.get_device(), ("x", "weight", "residual", "q", "scale", "out_residual"),
+                (x, weight, residual, q, scale, out_residual))
+    status = (_L or _lib()).gdr_add_rmsnorm_i8(
+        dims, x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), q.data_ptr(),
+        scale.data_ptr(), None if out_residual is None else out_residual.data_ptr(), s)
+    if status:
+        _fail(status)
     return q, scale, out_residual
 
 
@@ -190,27 +209,30 @@ def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, str
     ``o`` and ``gate`` are ``[..., HV, dv]`` (bf16 or fp32 each; dv 32, 64 or 128), ``weight``
     ``[dv]`` (bf16 or fp32).  Returns ``q`` (int8, ``[..., HV * dv]``) and ``scale`` (fp32, ``[...]``).
     """
-    if o.dim() < 2:
-        raise ValueError(f"o must be [..., HV, dv], got {list(o.shape)}")
-    H, V = o.shape[-2], o.shape[-1]
+    shape = o.shape
+    if len(shape) < 2:
+        raise ValueError(f"o must be [..., HV, dv], got {list(shape)}")
+    H, V = shape[-2:]
     if V not in (32, 64, 128):
         raise ValueError(f"dv must be 32, 64 or 128, got {V}")
     if H < 1 or H * V > NORM_MAX_COLS:
         raise ValueError(f"HV * dv must be in 1 .. {NORM_MAX_COLS}, got {H * V}")
-    if gate.shape != o.shape:
-        raise ValueError(f"gate must be {list(o.shape)}, got {list(gate.shape)}")
-    if weight.shape != o.shape[-1:]:
+    if gate.shape != shape:
+        raise ValueError(f"gate must be {list(shape)}, got {list(gate.shape)}")
+    if weight.shape != (V,):
         raise ValueError(f"weight must be {[V]}, got {list(weight.shape)}")
-    codes = _code(o, "o"), _code(gate, "gate"), _code(weight, "weight")
+    oc, gc, wc = _code(o, "o"), _code(gate, "gate"), _code(weight, "weight")
     if not weight.is_contiguous():
         raise ValueError("weight must be contiguous")
-    lead = o.shape[:-2]
-    q = _out(q, "q", (*lead, H * V), torch.int8, o.device)
-    scale = _out(scale, "scale", lead, torch.float32, o.device)
-    d = NormDims(scale.numel(), H, V, *codes, _eps(eps), _rows(o, "o", 2), _rows(gate, "gate", 2), 0)
-    s = _device(stream, o=o, gate=gate, weight=weight, q=q, scale=scale)
-    _check(_lib().gdr_gated_rmsnorm_i8(ctypes.addressof(d), o.data_ptr(), gate.data_ptr(), weight.data_ptr(),
-                                       q.data_ptr(), scale.data_ptr(), s))
+    lead = shape[:-2]
+    q = _out(q, "q", (*lead, H * V), _I8, o.device)
+    scale = _out(scale, "scale", lead, _F32, o.device)
+    dims = _NORM.pack(scale.numel(), H, V, oc, gc, wc, _eps(eps), _rows(o, "o", 2), _rows(gate, "gate", 2), 0)
+    s = _stream(stream, o.get_device(), ("o", "gate", "weight", "q", "scale"), (o, gate, weight, q, scale))
+    status = (_L or _lib()).gdr_gated_rmsnorm_i8(dims, o.data_ptr(), gate.data_ptr(), weight.data_ptr(),
+                                                 q.data_ptr(), scale.data_ptr(), s)
+    if status:
+        _fail(status)
     return q, scale
 
 
@@ -224,50 +246,64 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     output, a sequence of column counts for that many new tensors, or a sequence of tensors (of
     one type; their rows may be strided).  Returns a tensor, or a tuple for a sequence.
     """
-    if a.dim() < 1 or w.dim() != 2 or a.shape[-1] != w.shape[1]:
-        raise ValueError(f"a must be [..., K] and w [N, K], got {list(a.shape)} and {list(w.shape)}")
-    lead, (N, K) = a.shape[:-1], w.shape
+    shape, wshape = a.shape, w.shape
+    if not shape or len(wshape) != 2 or shape[-1] != wshape[1]:
+        raise ValueError(f"a must be [..., K] and w [N, K], got {list(shape)} and {list(wshape)}")
+    lead, (N, K) = shape[:-1], wshape
     if N < 1 or not 1 <= K <= MATMUL_I8_MAX_K:
         raise ValueError(f"N must be at least 1 and K in 1 .. {MATMUL_I8_MAX_K}, got N={N} K={K}")
-    for t, name in ((a, "a"), (w, "w")):
-        if t.dtype != torch.int8:
-            raise TypeError(f"{name} must be int8, got {t.dtype}")
-    for t, name, shape in ((a_scale, "a_scale", lead), (w_scale, "w_scale", (N,)), (bias, "bias", (N,))):
-        if t is None:
-            if name == "bias":
-                continue
-            raise TypeError(f"{name} is required")
-        if t.shape != torch.Size(shape):
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    if a.dtype is not _I8:
+        raise TypeError(f"a must be int8, got {a.dtype}")
+    if w.dtype is not _I8:
+        raise TypeError(f"w must be int8, got {w.dtype}")
+    _vector(a_scale, "a_scale", lead)
+    _vector(w_scale, "w_scale", (N,))
+    if bias is not None:
+        _vector(bias, "bias", (N,))
     single = out is None or isinstance(out, torch.Tensor)
-    outs = (N,) if out is None else (out,) if single else tuple(out)
-    if not 1 <= len(outs) <= MATMUL_I8_MAX_OUT:
-        raise ValueError(f"1 to {MATMUL_I8_MAX_OUT} outputs are supported, got {len(outs)}")
-    cols = [t.shape[-1] if isinstance(t, torch.Tensor) and t.dim() else t for t in outs]
-    if not all(isinstance(c, int) and c >= 1 for c in cols) or sum(cols) != N:
+    outs = [N] if out is None else [out] if single else list(out)
+    n = len(outs)
+    if not 1 <= n <= MATMUL_I8_MAX_OUT:
+        raise ValueError(f"1 to {MATMUL_I8_MAX_OUT} outputs are supported, got {n}")
+    cols = [t if isinstance(t, int) else t.shape[-1] if t.dim() else 0 for t in outs]
+    if min(cols) < 1 or sum(cols) != N:
         raise ValueError(f"the outputs' columns {cols} must be positive and add up to {N}")
-    outs = tuple(t if isinstance(t, torch.Tensor) else torch.empty(*lead, t, dtype=out_dtype, device=a.device)
-                 for t in outs)
-    oc = _code(outs[0], "out")
-    d = MatmulDims(a_scale.numel(), K, len(outs), oc)
     for i, t in enumerate(outs):
+        if isinstance(t, int):
+            outs[i] = torch.empty(*lead, t, dtype=out_dtype, device=a.device)
+    dtype = outs[0].dtype
+    oc = _code(outs[0], "out")
+    strides, ptrs = [], []
+    for t in outs:
         if t.shape[:-1] != lead:
-            raise ValueError(f"out must be {[*lead, cols[i]]}, got {list(t.shape)}")
-        if t.dtype != outs[0].dtype:
-            raise TypeError(f"outputs must be of one type, got {outs[0].dtype} and {t.dtype}")
-        d.out_cols[i] = cols[i]
-        d.out_stride[i] = _rows(t, "out")
-    d.a_stride, d.w_stride = _rows(a, "a"), _rows(w, "w")
-    s = _device(stream, a=a, a_scale=a_scale, w=w, w_scale=w_scale, bias=bias,
-                **{f"out[{i}]": t for i, t in enumerate(outs)})
-    ptrs = (_VP * len(outs))(*[t.data_ptr() for t in outs])
-    _check(_lib().gdr_matmul_i8(ctypes.addressof(d), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
-                                w_scale.data_ptr(), _ptr(bias), ctypes.addressof(ptrs), s))
-    return outs[0] if single else outs
+            raise ValueError(f"out must be {[*lead, t.shape[-1]]}, got {list(t.shape)}")
+        if t.dtype is not dtype:
+            raise TypeError(f"outputs must be of one type, got {dtype} and {t.dtype}")
+        strides.append(_rows(t, "out"))
+        ptrs.append(t.data_ptr())
+    none = _NONE[n:]
+    dims = _MATMUL.pack(a_scale.numel(), K, n, oc, *cols, *none, *strides, *none, _rows(a, "a"), _rows(w, "w"))
+    s = _stream(stream, a.get_device(), _MATMUL_NAMES, (a, a_scale, w, w_scale, bias, *outs))
+    status = (_L or _lib()).gdr_matmul_i8(dims, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                                          None if bias is None else bias.data_ptr(), _PTRS.pack(*ptrs, *none), s)
+    if status:
+        _fail(status)
+    return outs[0] if single else tuple(outs)
+
+
+_NONE = (0,) * MATMUL_I8_MAX_OUT
+_MATMUL_NAMES = ("a", "a_scale", "w", "w_scale", "bias") + ("out",) * MATMUL_I8_MAX_OUT
+
+
+def _vector(t, name, shape):
+    if t is None:
+        raise TypeError(f"{name} is required")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype is not _F32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def quantize_rows_i8(w):
