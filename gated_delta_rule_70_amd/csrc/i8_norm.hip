@@ -17,11 +17,14 @@ namespace {
 
 constexpr float kFltMax = 3.402823466e38f;
 
-// Eight consecutive values as fp32.  WIDE: the address takes 16-byte loads.
-template <bool WIDE>
-__device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
-    if constexpr (WIDE) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>(p);
+// Values 0 .. 7 at p as fp32, zeros from n on.  Vector loads at any alignment of the elements: the
+// hardware takes them unaligned, so only a row's last group of fewer than 8 (PART: there may be
+// one) goes value by value.
+template <bool PART>
+__device__ __forceinline__ void load8(const bf16_t* p, int n, float (&v)[8]) {
+    if (!PART || n >= 8) {
+        u32x4 u;
+        __builtin_memcpy(&u, p, 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             v[2 * j] = __uint_as_float(u[j] << 16);
@@ -29,40 +32,91 @@ __device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = to_f32(p[j]);
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f32(p[j]) : 0.f;
     }
 }
-template <bool WIDE>
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    if constexpr (WIDE) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+template <bool PART>
+__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
+    if (!PART || n >= 8) {
+        __builtin_memcpy(v, p, 32);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = p[j];
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.f;
     }
 }
 __device__ __forceinline__ float round_to(float x, const float*) { return x; }
 __device__ __forceinline__ float round_to(float x, const bf16_t*) {
     return static_cast<float>(static_cast<__bf16>(x));
 }
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store1(bf16_t* p, float x) { *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(x); }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+template <bool PART>
+__device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
+    if (!PART || n >= 8) {
+        __builtin_memcpy(p, v, 32);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = v[j];
+    }
 }
-__device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
+template <bool PART>
+__device__ __forceinline__ void store8(bf16_t* p, int n, const float (&v)[8]) {
     const u32x2 a = bf16x4_bits(f32x4{v[0], v[1], v[2], v[3]}), b = bf16x4_bits(f32x4{v[4], v[5], v[6], v[7]});
-    *reinterpret_cast<u32x4*>(p) = u32x4{a[0], a[1], b[0], b[1]};
+    const u32x4 u = {a[0], a[1], b[0], b[1]};
+    if (!PART || n >= 8) {
+        __builtin_memcpy(p, &u, 16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j].bits = (uint16_t)(u[j / 2] >> (j % 2 * 16));
+    }
 }
-__device__ __forceinline__ u32x2 pack8(const int (&c)[8]) {
+
+// Rounding to whole numbers, ties to even, by one addition: x + kRound (|x| < 2^22) has the whole
+// number's low bits at its end.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+// The low bytes of eight such sums, or zeros.
+__device__ __forceinline__ u32x2 pack8(const float (&y)[8], bool zero) {
     u32x2 r;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        r[j] = (c[4 * j] & 0xFF) | (c[4 * j + 1] & 0xFF) << 8 | (c[4 * j + 2] & 0xFF) << 16 | (uint32_t)c[4 * j + 3] << 24;
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t a = __builtin_amdgcn_perm(__float_as_uint(y[4 * j + 1]), __float_as_uint(y[4 * j]), 0x0C0C0400);
+        const uint32_t b = __builtin_amdgcn_perm(__float_as_uint(y[4 * j + 3]), __float_as_uint(y[4 * j + 2]), 0x04000C0C);
+        r[j] = zero ? 0u : a | b;
+    }
     return r;
+}
+template <bool PART>
+__device__ __forceinline__ void store_codes(int8_t* q, int n, u32x2 c) {
+    if (!PART || n >= 8) {
+        __builtin_memcpy(q, &c, 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) q[j] = (int8_t)(c[j / 4] >> (j % 4 * 8));
+    }
+}
+
+// Sum over the V / 8 neighbouring lanes (4, 8 or 16) that hold a head's V values, in all of them.
+template <int CTRL>
+__device__ __forceinline__ double dpp_mov64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum_head(double x, int V) {
+    x += dpp_mov64<0xB1>(x);               // quad_perm [1,0,3,2]
+    x += dpp_mov64<0x4E>(x);               // quad_perm [2,3,0,1]
+    if (V > 32) x += dpp_mov64<0x141>(x);  // row_half_mirror: the other quad of 8 lanes
+    if (V > 64) x += dpp_mov64<0x140>(x);  // row_mirror: the other half of 16 lanes
+    return x;
+}
+
+// 1 / sqrt(m) in fp64: the hardware's estimate and one Newton step.  Zero for m = 0.
+__device__ __forceinline__ double rsqrt64(double m) {
+    const double r = __builtin_amdgcn_rsq(m);
+    const double e = __builtin_fma(-m * r, r, 1.0);
+    return m == 0. ? 0. : __builtin_fma(r * 0.5, e, r);
 }
 
 // Sum and maximum of TPR consecutive threads (64, or the whole workgroup), in all of them.
@@ -93,15 +147,14 @@ __device__ __forceinline__ void reduce_row(double& sum, T& top, int& bad) {
     }
 }
 
-// Residual addition, norm and codes.  TPR threads for each row, NV groups of 8 values in each
-// thread: WIDE groups are 8 consecutive values, otherwise values TPR apart (so that single
-// loads of neighbouring threads are neighbours).
+// Residual addition, norm and codes.  TPR threads for each row, NV groups of 8 consecutive values
+// in each thread.
 //
 // T holds t: fp32 where s and weight are bf16 (a product of two 8-bit significands is exact),
 // fp64 otherwise (exact again), so A is exact too.  127 t / A is taken in fp32 first: its error
 // is below 4 * 2^-24 relative, 2^-15 absolute; within 2^-14 of a border between codes (one value
 // in 8000) it is taken again in fp64.
-template <typename TX, typename TW, typename T, int TPR, int NV, bool WIDE>
+template <typename TX, typename TW, typename T, int TPR, int NV, bool PART>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(NormArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     const int tid = TPR < 256 ? threadIdx.x % TPR : threadIdx.x;
@@ -118,37 +171,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
     double sum = 0.;
     T top = T(0);
     int bad = 0;
-    auto at = [&](int i, int j) { return WIDE ? (i * TPR + tid) * 8 + j : (i * 8 + j) * TPR + tid; };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float s[8], wv[8];
-        if constexpr (WIDE) {
-            if (at(i, 0) < D) {
-                load8<true>(x + at(i, 0), s);
-                load8<true>(w + at(i, 0), wv);
-                if (r) {
-                    float rv[8];
-                    load8<true>(r + at(i, 0), rv);
+        const int e = (i * TPR + tid) * 8, n = D - e;
+        float s[8] = {}, wv[8] = {};
+        if (n > 0) {
+            load8<PART>(x + e, n, s);
+            load8<PART>(w + e, n, wv);
+            if (r) {
+                float rv[8];
+                load8<PART>(r + e, n, rv);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[j] = round_to(s[j] + rv[j], x);
-                }
-                if (out) store8(out + at(i, 0), s);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = wv[j] = 0.f;
+                for (int j = 0; j < 8; ++j) s[j] = round_to(s[j] + rv[j], x);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = at(i, j);
-                s[j] = wv[j] = 0.f;
-                if (e < D) {
-                    s[j] = to_f32(x[e]);
-                    wv[j] = to_f32(w[e]);
-                    if (r) s[j] = round_to(s[j] + to_f32(r[e]), x);
-                    if (out) store1(out + e, s[j]);
-                }
-            }
+            if (out) store8<PART>(out + e, n, s);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -161,8 +197,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
     }
     reduce_row<TPR>(sum, top, bad);
 
-    const double rho = 1.0 / sqrt(sum / D + (double)a.eps);
     if (tid == 0) {
+        const double rho = 1.0 / sqrt(sum / D + (double)a.eps);
         double sc = (double)top * rho / 127.0;
         if (top == T(0)) sc = 0.;  // also with eps = 0, where rho is infinite
         a.scale[row] = bad ? __builtin_nanf("") : (float)sc;
@@ -173,36 +209,26 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
     const float inv = zero || tiny ? 0.f : 127.f / (float)top;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        int c[8];
+        float y[8];
         float worst = tiny ? 1.f : 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float v = (float)t[i][j] * inv, n = __builtin_rintf(v);
-            c[j] = (int)n;
-            worst = fmaxf(worst, fabsf(v - n));
+            y[j] = __builtin_fmaf((float)t[i][j], inv, kRound);
+            worst = fmaxf(worst, fabsf(__builtin_fmaf((float)t[i][j], inv, kRound - y[j])));
         }
         if (worst > 0.5f - 0x1p-14f) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = zero ? 0 : (int)rint((double)t[i][j] * 127.0 / (double)top);
+            for (int j = 0; j < 8; ++j) y[j] = (float)rint((double)t[i][j] * 127.0 / (double)top) + kRound;
         }
-        if (zero) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = 0;
-        }
-        if constexpr (WIDE) {
-            if (at(i, 0) < D) *reinterpret_cast<u32x2*>(q + at(i, 0)) = pack8(c);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (at(i, j) < D) q[at(i, j)] = (int8_t)c[j];
-        }
+        const int e = (i * TPR + tid) * 8;
+        if (e < D) store_codes<PART>(q + e, D - e, pack8(y, zero));
     }
 }
 
 // exp(-z) to about 1 ulp: the product with log2(e) is taken in two parts, so that the error of
 // the exponent does not grow with |z|.  Beyond |z| = 200 the result stays infinity or zero.
 __device__ __forceinline__ float exp_neg(float z) {
-    z = fminf(fmaxf(z, -200.f), 200.f);
+    z = __builtin_amdgcn_fmed3f(z, -200.f, 200.f);
     constexpr float kL = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;  // log2(e), high and low
     const float p = -z * kL;
     const float e = __builtin_fmaf(-z, kL, -p) + -z * kLo;
@@ -211,7 +237,7 @@ __device__ __forceinline__ float exp_neg(float z) {
 
 // Norm per value head (V values, V/8 neighbouring threads), times weight and silu(gate), and
 // codes over the whole token.
-template <typename TO, typename TG, typename TW, int TPR, int NV, bool WIDE>
+template <typename TO, typename TG, typename TW, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_rmsnorm_kernel(NormArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     const int tid = TPR < 256 ? threadIdx.x % TPR : threadIdx.x;
@@ -223,16 +249,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_rmsnorm_kernel(No
     const TW* w = static_cast<const TW*>(a.w);
     int8_t* q = a.q + (int64_t)row * D;
 
+    const double per_v = V == 32 ? 1. / 32 : V == 64 ? 1. / 64 : 1. / 128;
     float n[NV][8];
     uint32_t top = 0;  // |n| as ordered bits: NaN above infinity above every number
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = (i * TPR + tid) * 8;
         float zv[8], wv[8];
-        if (e < D) {
-            load8<WIDE>(o + e, n[i]);
-            load8<WIDE>(z + e, zv);
-            load8<WIDE>(w + e % V, wv);
+        if (e < D) {  // D is a multiple of 8
+            load8<false>(o + e, 8, n[i]);
+            load8<false>(z + e, 8, zv);
+            load8<false>(w + (e & (V - 1)), 8, wv);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) n[i][j] = zv[j] = wv[j] = 0.f;
@@ -240,13 +267,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_rmsnorm_kernel(No
         double ss = 0.;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)n[i][j], (double)n[i][j], ss);
-        for (int m = V / 16; m >= 1; m >>= 1) ss += __shfl_xor(ss, m);
-        const float rho = (float)(1.0 / sqrt(ss / V + (double)a.eps));
+        ss = sum_head(ss, V);
+        const float rho = (float)rsqrt64(__builtin_fma(ss, per_v, (double)a.eps));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // a zero head stays zero also where eps = 0 makes rho infinite
-            const float x = n[i][j] == 0.f ? 0.f : n[i][j] * rho;
-            n[i][j] = x * wv[j] * (zv[j] / (1.f + exp_neg(zv[j])));
+            const float silu = zv[j] * __builtin_amdgcn_rcpf(1.f + exp_neg(zv[j]));
+            n[i][j] = n[i][j] * rho * (wv[j] * silu);
             const uint32_t b = __float_as_uint(n[i][j]) & 0x7FFFFFFFu;
             top = b > top ? b : top;
         }
@@ -257,27 +283,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_rmsnorm_kernel(No
     const float A = __uint_as_float(top);
     const bool zero = bad || top == 0;
     if (tid == 0) a.scale[row] = bad ? __builtin_nanf("") : A / 127.f;
-    // a power of two that keeps 127 / A finite
-    const float up = A < 0x1p-100f ? 0x1p100f : 1.f;
-    const float inv = zero ? 0.f : 127.f / (A * up);
+    if (A < 0x1p-100f) {  // a power of two that keeps 127 / A finite
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n[i][j] *= 0x1p100f;
+    }
+    const float inv = zero ? 0.f : 127.f / (A < 0x1p-100f ? A * 0x1p100f : A);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = (i * TPR + tid) * 8;
-        int c[8];
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = zero ? 0 : (int)__builtin_rintf(n[i][j] * up * inv);
-        if (e < D) {
-            if constexpr (WIDE)
-                *reinterpret_cast<u32x2*>(q + e) = pack8(c);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) q[e + j] = (int8_t)c[j];
-        }
+        for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(n[i][j], inv, kRound);
+        if (e < D) store_codes<false>(q + e, 8, pack8(y, zero));
     }
-}
-
-bool wide(const void* p, int64_t stride, int rows, int elt) {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows == 1 || stride * elt % 16 == 0));
 }
 
 template <int TPR>
@@ -286,18 +306,28 @@ dim3 grid_of(int rows) {
     return dim3((unsigned)((rows + (int64_t)RPB - 1) / RPB));
 }
 
-template <typename TX, typename TW, typename T, bool WIDE>
-void add_rmsnorm_sized(const NormArgs& a) {
+// Threads for a row and groups for a thread: as many threads as the row fills with one or two groups
+// each, since a row is read and written once and what counts is loads in flight.  A row of up to
+// 2048 values by one wave (no barrier) pays once there are rows enough to fill the chip with them.
+// At 4097 rows of 4096 bf16: 256 threads with two groups 25.8 us, one wave with eight 45.6; in the
+// gated norm 512 threads with one group 20.1 us, 256 with two 21.4, one wave 39.9.
+template <typename TX, typename TW, typename T>
+void add_rmsnorm_typed(const NormArgs& a) {
     auto go = [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-        hipLaunchKernelGGL((add_rmsnorm_kernel<TX, TW, T, TPR, NV, WIDE>), grid_of<TPR>(a.rows),
-                           dim3(TPR < 256 ? 256 : TPR), 0, a.stream, a);
+        const dim3 threads(TPR < 256 ? 256 : TPR);
+        if (a.cols % 8 == 0)
+            hipLaunchKernelGGL((add_rmsnorm_kernel<TX, TW, T, TPR, NV, false>), grid_of<TPR>(a.rows), threads, 0, a.stream, a);
+        else
+            hipLaunchKernelGGL((add_rmsnorm_kernel<TX, TW, T, TPR, NV, true>), grid_of<TPR>(a.rows), threads, 0, a.stream, a);
     };
     using std::integral_constant;
     if (a.cols <= 512)
         go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (a.cols <= 2048)
+    else if (a.cols <= 2048 && a.rows > 4096)
         go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    else if (a.cols <= 2048)
+        go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (a.cols <= 4096)
         go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     else if (a.cols <= 8192)
@@ -306,38 +336,27 @@ void add_rmsnorm_sized(const NormArgs& a) {
         go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
-template <typename TX, typename TW, typename T>
-void add_rmsnorm_typed(const NormArgs& a) {
-    const bool v = a.cols % 8 == 0 && wide(a.x, a.x_stride, a.rows, sizeof(TX)) &&
-                   wide(a.r, a.r_stride, a.rows, sizeof(TX)) && wide(a.out, a.out_stride, a.rows, sizeof(TX)) &&
-                   wide(a.w, 0, 1, sizeof(TW)) && wide(a.q, a.cols, 1, 1);
-    v ? add_rmsnorm_sized<TX, TW, T, true>(a) : add_rmsnorm_sized<TX, TW, T, false>(a);
-}
-
-template <typename TO, typename TG, typename TW, bool WIDE>
-void gated_sized(const NormArgs& a) {
+template <typename TO, typename TG, typename TW>
+void gated_typed(const NormArgs& a) {
     auto go = [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-        hipLaunchKernelGGL((gated_rmsnorm_kernel<TO, TG, TW, TPR, NV, WIDE>), grid_of<TPR>(a.rows),
+        hipLaunchKernelGGL((gated_rmsnorm_kernel<TO, TG, TW, TPR, NV>), grid_of<TPR>(a.rows),
                            dim3(TPR < 256 ? 256 : TPR), 0, a.stream, a);
     };
     using std::integral_constant;
     const int D = a.heads * a.cols;
     if (D <= 512)
         go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (D <= 1024 && a.rows > 2048)
+        go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (D <= 2048)
+        go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (D <= 4096)
-        go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+        go(integral_constant<int, 512>{}, integral_constant<int, 1>{});
     else if (D <= 8192)
-        go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+        go(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
     else
         go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
-}
-
-template <typename TO, typename TG, typename TW>
-void gated_typed(const NormArgs& a) {
-    const bool v = wide(a.x, a.x_stride, a.rows, sizeof(TO)) && wide(a.r, a.r_stride, a.rows, sizeof(TG)) &&
-                   wide(a.w, 0, 1, sizeof(TW)) && wide(a.q, a.heads * a.cols, 1, 1);
-    v ? gated_sized<TO, TG, TW, true>(a) : gated_sized<TO, TG, TW, false>(a);
 }
 
 }  // namespace
