@@ -577,8 +577,8 @@ void tiles(const MatmulArgs& g) {
 }
 
 bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows == 1 || stride % 16 == 0) &&
-           255 * stride + K < (int64_t(1) << 31);
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 &&
+           (rows == 1 || (stride % 16 == 0 && stride <= (INT32_MAX - K) / 255));
 }
 
 // Form of a product and its expected time.  Up to 2048 tiles' worth of work the time is the number

@@ -8,6 +8,10 @@
 
 Activations and weights are int8 codes with an fp32 scale for each token and each output
 channel; residual stream, gate and outputs are bf16 or fp32.  Forward only.
+
+Work is enqueued on the current stream, or on ``stream`` (a torch stream or a handle), which the
+caller orders after whatever made the inputs; memory used there is not reused before it is done.
+Calls allocate nothing but the outputs that are not given, and can be captured into graphs.
 """
 from __future__ import annotations
 
@@ -93,9 +97,16 @@ def _stream(stream, dev, names, tensors):
             break
     else:
         if dev == torch.cuda.current_device():
+            here = _raw_stream(dev)
             if stream is None:
-                return _raw_stream(dev)
-            return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+                return here
+            there = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            if there != here:  # the allocator must not hand the memory on before that stream is done
+                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(there)
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(s)
+            return there
     for name, t in zip(names, tensors):
         if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor")

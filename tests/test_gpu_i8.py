@@ -361,6 +361,24 @@ def test_repeatable_and_on_another_stream(M):
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_stream_argument():
+    """Calls given another stream than the current one, whose inputs are dropped at once."""
+    side = torch.cuda.Stream()
+    want = chain(*chain_inputs(60, 10))
+    for stream in (side, side.cuda_stream):
+        x, res, nw, w1, s1, w2, s2, hw = chain_inputs(60, 10)
+        side.wait_stream(torch.cuda.current_stream())
+        q8, sc, h = gdr.add_rmsnorm_i8(x, nw, residual=res, stream=stream)
+        o, z = gdr.matmul_i8(q8, sc, w1, s1, out=(256, 256), stream=stream)
+        q8, sc2 = gdr.gated_rmsnorm_i8(o.view(-1, 4, 64), z.view(-1, 4, 64), hw, stream=stream)
+        y = gdr.matmul_i8(q8, sc2, w2, s2, stream=stream)
+        del x, res, nw, w1, s1, q8, o, z
+        for _ in range(8):
+            torch.full((60, 512), 99.0, device="cuda")
+        side.synchronize()
+        assert torch.equal(y, want[3]) and torch.equal(h, want[0])
+
+
 @pytest.mark.parametrize("M", [1, 50, 500])
 def test_graph_replays(M):
     x = chain_inputs(M, 20)
