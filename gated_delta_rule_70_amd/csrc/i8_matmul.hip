@@ -173,18 +173,6 @@ __device__ __forceinline__ void copy_to_lds(const int8_t* from, i32x4* to) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void*)to, 16, 0, 0);
 }
 
-// Order of issue: MF matrix products with R LDS reads and L copies to LDS spread among them.
-template <int MF, int R, int L, int I = 0>
-__device__ __forceinline__ void interleave() {
-    if constexpr (I < R) {
-        constexpr int mf = (I + 1) * MF / R - I * MF / R, ld = (I + 1) * L / R - I * L / R;
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, mf, 0);
-        if constexpr (ld > 0) __builtin_amdgcn_sched_group_barrier(0x020, ld, 0);
-        interleave<MF, R, L, I + 1>();
-    }
-}
-
 template <int BM, int BN, int WM, int WN, int STAGES, bool DMA, bool BF16>
 __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) {
     constexpr int NT = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -281,29 +269,49 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
     if constexpr (DMA) {
         // Two sets of fragments: while one half of a stage is multiplied the next half is read
         // from LDS, also across stages: the barrier that frees stage s (everyone has read it) and
-        // opens stage s + 1 stands between the halves of stage s.
-        constexpr int L = LA + LW, MF = TM * TN, RD = TM + TN;
+        // opens stage s + 1 stands between the halves of stage s.  The order is written out, a
+        // row of products at a time: LDS reads go with the first rows (two each, so that the last
+        // are back before the next half needs them), copies to LDS one or two with each row, since
+        // a run of copies holds a wave up while the address unit takes 64 lanes' worth each.
+        constexpr int L = LA + LW, RD = TM + TN, PR = (RD + TM - 1) / TM + 1, PL = (L + TM - 1) / TM;
         Frags f0, f1;
+        auto half = [&](const Frags& use, Frags& next, int rs, int rh, auto reads, int fs, auto copies) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                if constexpr (decltype(reads)::value) {
+#pragma unroll
+                    for (int r = i * PR; r < (i + 1) * PR && r < RD; ++r) {
+                        if (r < TN)
+                            next.w[r] = lds[rs % STAGES][BM * 8 + wn * (TN * 128) + r * 128 + (place ^ (rh * 4))];
+                        else
+                            next.a[r - TN] = lds[rs % STAGES][wm * (TM * 128) + (r - TN) * 128 + (place ^ (rh * 4))];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma_i8(use.w[j], use.a[i], acc[i][j]);
+                if constexpr (decltype(copies)::value) {
+#pragma unroll
+                    for (int c = i * PL; c < (i + 1) * PL && c < L; ++c) {
+                        i32x4* to = &lds[fs % STAGES][wave * 64];
+                        if (c < LA)
+                            copy_to_lds(ra, to + c * NT, va[c], fs * kBK);
+                        else
+                            copy_to_lds(rw, to + BM * 8 + (c - LA) * NT, vw[c - LA], fs * kBK);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
         auto step = [&](int s, auto more, auto next) {
-            read(s, 1, f1);
-            multiply(f0);
-            interleave<MF, RD, 0>();
-            __builtin_amdgcn_sched_barrier(0);
+            half(f0, f1, s, 1, std::true_type{}, 0, std::false_type{});
             if constexpr (decltype(next)::value) {
                 if constexpr (decltype(more)::value)
                     wait_vmcnt<(STAGES - 2) * L>();
                 else
                     wait_vmcnt<0>();
                 lds_barrier();
-                if constexpr (decltype(more)::value) fetch(s + STAGES);
-                read(s + 1, 0, f0);
             }
-            multiply(f1);
-            if constexpr (decltype(more)::value)
-                interleave<MF, RD, L>();
-            else if constexpr (decltype(next)::value)
-                interleave<MF, RD, 0>();
-            __builtin_amdgcn_sched_barrier(0);
+            half(f1, f0, s + 1, 0, next, s + STAGES, more);
         };
         using yes = std::true_type;
         using no = std::false_type;
