@@ -38,7 +38,7 @@ int64_t elt_of(int32_t t) { return t == GDR_F32 ? 4 : 2; }
 // The checks that both norms share, on dims alone.
 int validate_norm(const gdr_norm_dims* d) {
     if (!d) return GDR_ERR_NULL;
-    if (d->rows < 0 || d->heads < 1 || d->cols < 1) return GDR_ERR_SHAPE;
+    if (d->rows < 0 || d->rows > GDR_I8_MAX_ROWS || d->heads < 1 || d->cols < 1) return GDR_ERR_SHAPE;
     if ((int64_t)d->heads * d->cols > GDR_NORM_MAX_COLS) return GDR_ERR_SHAPE;
     if (!known_dtype(d->x_dtype) || !known_dtype(d->weight_dtype)) return GDR_ERR_UNSUPPORTED;
     if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return GDR_ERR_UNSUPPORTED;
@@ -100,7 +100,8 @@ int gdr_add_rmsnorm_i8(const gdr_norm_dims* dims, const void* x, const void* res
     if (overlap(ro, rx) && !(out_residual == x && (d.rows == 1 || d.out_stride == d.x_stride))) return GDR_ERR_ALIAS;
     if (overlap(ro, rr) && !(out_residual == residual && (d.rows == 1 || d.out_stride == d.r_stride)))
         return GDR_ERR_ALIAS;
-    const gdr::NormArgs a = norm_args(dims, x, residual, weight, q, scale, out_residual, stream);
+    gdr::NormArgs a = norm_args(dims, x, residual, weight, q, scale, out_residual, stream);
+    a.heads = 0;
     return gdr::launch_add_rmsnorm_i8(a) == hipSuccess ? GDR_OK : GDR_ERR_HIP;
 }
 
@@ -133,7 +134,7 @@ int gdr_matmul_i8(const gdr_matmul_i8_dims* dims, const int8_t* a, const float* 
                   const float* w_scale, const float* bias, void* const* outs, void* stream) {
     if (!dims) return GDR_ERR_NULL;
     const gdr_matmul_i8_dims& d = *dims;
-    if (d.M < 0 || d.K < 1 || d.K > GDR_MATMUL_I8_MAX_K || d.n_out < 1 || d.n_out > GDR_MATMUL_I8_MAX_OUT ||
+    if (d.M < 0 || d.M > GDR_I8_MAX_ROWS || d.K < 1 || d.K > GDR_MATMUL_I8_MAX_K || d.n_out < 1 || d.n_out > GDR_MATMUL_I8_MAX_OUT ||
         d.a_stride < 0 || d.w_stride < 0)
         return GDR_ERR_SHAPE;
     if (!known_dtype(d.out_dtype)) return GDR_ERR_UNSUPPORTED;
@@ -152,8 +153,8 @@ int gdr_matmul_i8(const gdr_matmul_i8_dims* dims, const int8_t* a, const float* 
         if (N > (1 << 30)) return GDR_ERR_SHAPE;
     }
     for (int i = d.n_out; i <= GDR_MATMUL_I8_MAX_OUT; ++i) g.out.begin[i] = (int)N;
-    // the smallest tile has 16 rows or columns; a grid has at most 2^31 - 1 workgroups
-    if ((d.M + 15LL) / 16 * ((N + 15) / 16) >= (1LL << 31)) return GDR_ERR_SHAPE;
+    // a launch has fewer than 2^32 threads: 2^23 tiles of 256 x 256 with 512 each
+    if ((d.M + 255LL) / 256 * ((N + 255) / 256) >= (1LL << 23)) return GDR_ERR_SHAPE;
     if (d.M == 0) return GDR_OK;
     if (!a || !a_scale || !w || !w_scale || !outs) return GDR_ERR_NULL;
     for (int i = 0; i < d.n_out; ++i)

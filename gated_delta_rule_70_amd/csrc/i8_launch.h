@@ -10,7 +10,7 @@
 namespace gdr {
 
 struct NormArgs {
-    int rows, heads, cols;
+    int rows, heads, cols;  // heads: 0 for the residual norm
     bool x_bf16, gate_bf16, w_bf16;
     float eps;
     int64_t x_stride, r_stride, out_stride;

@@ -619,7 +619,7 @@ Plan plan(int64_t M, int64_t N, int K) {
         const double us = rounds * (fixed + per_k * K * 1e-3);
         if (us < best.us) best = Plan{f, us};
     };
-    constexpr int64_t any = int64_t(1) << 62;
+    constexpr int64_t any = (1 << 23) - 1;  // a launch has fewer than 2^32 threads, 512 for each tile
     offer(Form::t32x64, 32, 64, 1, any, 0.8, 1.9);
     offer(Form::t64x32, 64, 32, 1, any, 0.8, 1.9);
     offer(Form::t128x64, 128, 64, 1, any, 1.0, 2.8);
@@ -645,7 +645,7 @@ void start(Form f, const MatmulArgs& g) {
 }  // namespace
 
 hipError_t launch_matmul_i8(const MatmulArgs& g) {
-    if (g.M < 1 || g.N < 1 || g.K < 1 || g.K > GDR_MATMUL_I8_MAX_K) return hipErrorInvalidValue;
+    if (g.M < 1 || g.M > GDR_I8_MAX_ROWS || g.N < 1 || g.K < 1 || g.K > GDR_MATMUL_I8_MAX_K) return hipErrorInvalidValue;
     const bool dma = dma_ok(g.a, g.a_stride, g.M, g.K) && dma_ok(g.w, g.w_stride, g.N, g.K);
     const Plan whole = plan(g.M, g.N, g.K);
     // A few rows past a multiple of 256 can cost a round of tiles more: they go into a launch of

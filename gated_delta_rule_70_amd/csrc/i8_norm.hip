@@ -361,26 +361,50 @@ void gated_typed(const NormArgs& a) {
 
 }  // namespace
 
-hipError_t launch_add_rmsnorm_i8(const NormArgs& a) {
-    if (a.rows < 1 || a.cols < 1 || a.cols > GDR_NORM_MAX_COLS) return hipErrorInvalidValue;
-    if (!a.x_bf16)
-        add_rmsnorm_typed<float, float, double>(a);
-    else if (a.w_bf16)
-        add_rmsnorm_typed<bf16_t, bf16_t, float>(a);
-    else
-        add_rmsnorm_typed<bf16_t, float, double>(a);
-    return hipGetLastError();
+// A launch has fewer than 2^32 threads: rows go in slices of 2^20, at most 1024 threads each.
+template <typename F>
+static hipError_t by_slices(const NormArgs& all, int64_t q_cols, F launch) {
+    constexpr int kSlice = 1 << 20;
+    const int64_t ex = all.x_bf16 ? 2 : 4, er = all.heads ? (all.gate_bf16 ? 2 : 4) : ex;
+    for (int r0 = 0; r0 < all.rows; r0 += kSlice) {
+        NormArgs a = all;
+        a.rows = all.rows - r0 < kSlice ? all.rows - r0 : kSlice;
+        a.x = static_cast<const char*>(all.x) + r0 * all.x_stride * ex;
+        if (all.r) a.r = static_cast<const char*>(all.r) + r0 * all.r_stride * er;
+        if (all.out) a.out = static_cast<char*>(all.out) + r0 * all.out_stride * ex;
+        a.q += r0 * q_cols;
+        a.scale += r0;
+        launch(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
-hipError_t launch_gated_rmsnorm_i8(const NormArgs& a) {
-    if (a.rows < 1 || a.heads * a.cols > GDR_NORM_MAX_COLS || a.cols % 32 != 0 || a.cols > 128)
+hipError_t launch_add_rmsnorm_i8(const NormArgs& all) {
+    if (all.rows < 1 || all.rows > GDR_I8_MAX_ROWS || all.cols < 1 || all.cols > GDR_NORM_MAX_COLS)
         return hipErrorInvalidValue;
-    auto w = [&](auto o, auto g) {
-        a.w_bf16 ? gated_typed<decltype(o), decltype(g), bf16_t>(a) : gated_typed<decltype(o), decltype(g), float>(a);
-    };
-    auto g = [&](auto o) { a.gate_bf16 ? w(o, bf16_t{}) : w(o, float{}); };
-    a.x_bf16 ? g(bf16_t{}) : g(float{});
-    return hipGetLastError();
+    return by_slices(all, all.cols, [](const NormArgs& a) {
+        if (!a.x_bf16)
+            add_rmsnorm_typed<float, float, double>(a);
+        else if (a.w_bf16)
+            add_rmsnorm_typed<bf16_t, bf16_t, float>(a);
+        else
+            add_rmsnorm_typed<bf16_t, float, double>(a);
+    });
+}
+
+hipError_t launch_gated_rmsnorm_i8(const NormArgs& all) {
+    if (all.rows < 1 || all.rows > GDR_I8_MAX_ROWS || all.heads < 1 || all.heads * all.cols > GDR_NORM_MAX_COLS ||
+        (all.cols != 32 && all.cols != 64 && all.cols != 128))
+        return hipErrorInvalidValue;
+    return by_slices(all, all.heads * all.cols, [](const NormArgs& a) {
+        auto w = [&](auto o, auto g) {
+            a.w_bf16 ? gated_typed<decltype(o), decltype(g), bf16_t>(a) : gated_typed<decltype(o), decltype(g), float>(a);
+        };
+        auto g = [&](auto o) { a.gate_bf16 ? w(o, bf16_t{}) : w(o, float{}); };
+        a.x_bf16 ? g(bf16_t{}) : g(float{});
+    });
 }
 
 }  // namespace gdr

@@ -55,6 +55,7 @@ _CODE = {torch.bfloat16: 0, torch.float32: 1}
 _F32, _I8 = torch.float32, torch.int8
 # the current stream's handle without building a Stream object
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _L = None
 
 
@@ -92,11 +93,11 @@ def _code(t, name):
 
 def _stream(stream, dev, names, tensors):
     """The stream's handle, once all tensors are known to be on the current GPU."""
-    for t in tensors:
-        if t is not None and (dev < 0 or t.get_device() != dev):
-            break
-    else:
-        if dev == torch.cuda.current_device():
+    if dev >= 0 and dev == _current_device():
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
             here = _raw_stream(dev)
             if stream is None:
                 return here

@@ -20,7 +20,7 @@
  * nothing; statuses are gdr_status; results are bitwise reproducible (no atomics).  rows == 0
  * is a valid call that does nothing (pointers may then be NULL).  Strides are in elements,
  * between rows; within a row values are contiguous.  Pointers need only their element type's
- * alignment; 16-byte aligned pointers and row strides take the wide-load kernels.
+ * alignment; the product is faster where a, w and their row strides are multiples of 16 bytes.
  */
 #ifndef GDR_I8_H
 #define GDR_I8_H
@@ -31,13 +31,14 @@
 extern "C" {
 #endif
 
+#define GDR_I8_MAX_ROWS (1 << 30)    /* most rows (tokens) of one call                       */
 #define GDR_NORM_MAX_COLS 32768      /* most values in one row (heads * cols) of the norms    */
 #define GDR_MATMUL_I8_MAX_K 131071   /* longest reduction: 128 * 128 * K stays below 2^31     */
 #define GDR_MATMUL_I8_MAX_OUT 8      /* most separate outputs of one product                  */
 
 /* Dims of the two norms. */
 typedef struct {
-    int32_t rows;         /* tokens, >= 0                                                     */
+    int32_t rows;         /* tokens, 0 .. GDR_I8_MAX_ROWS                                   */
     int32_t heads;        /* gdr_gated_rmsnorm_i8: value heads; gdr_add_rmsnorm_i8: 1         */
     int32_t cols;         /* values per row, or per head (then 32, 64 or 128)                 */
     int32_t x_dtype;      /* x, residual and out_residual, or o (gdr_dtype)                   */
@@ -80,11 +81,12 @@ int gdr_gated_rmsnorm_i8(const gdr_norm_dims* dims, const void* o, const void* g
 
 /* Dims of the product. */
 typedef struct {
-    int32_t M;            /* rows of a (tokens), >= 0                                         */
+    int32_t M;            /* rows of a (tokens), 0 .. GDR_I8_MAX_ROWS                         */
     int32_t K;            /* 1 .. GDR_MATMUL_I8_MAX_K                                         */
     int32_t n_out;        /* separate outputs, 1 .. GDR_MATMUL_I8_MAX_OUT                     */
     int32_t out_dtype;    /* gdr_dtype of every output                                        */
-    int32_t out_cols[GDR_MATMUL_I8_MAX_OUT];  /* columns of each, >= 1; their sum is N        */
+    int32_t out_cols[GDR_MATMUL_I8_MAX_OUT];  /* columns of each, >= 1; their sum is N, at most
+                             2^30, and M / 256 * N / 256 (each rounded up) below 2^23         */
     int64_t out_stride[GDR_MATMUL_I8_MAX_OUT];/* elements between rows of each, >= its columns*/
     int64_t a_stride;     /* bytes from one row of a to the next, >= 0                        */
     int64_t w_stride;     /* bytes from one row of w to the next, >= 0                        */

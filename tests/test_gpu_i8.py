@@ -104,6 +104,21 @@ def test_add_rmsnorm_special_rows(D, dtype):
     check_norm(x, w, None)
 
 
+def test_more_rows_than_one_launch_takes():
+    M = (1 << 20) + 5
+    x, r, w = (torch.randn(M, 8, device="cuda", dtype=BF) for _ in range(3))
+    s, q_ref, scale_ref = norm_reference(x, w[0], r, 1e-6)
+    note(f"{M} rows")
+    q, scale, out = gdr.add_rmsnorm_i8(x, w[0], r)
+    assert torch.equal(out, s) and torch.equal(q.double(), q_ref)
+    assert bool(((scale - scale_ref).abs() <= 1.01 * U * scale_ref).all())
+    o, z = x.view(M, 8).repeat(1, 4).view(M, 1, 32), r.repeat(1, 4).view(M, 1, 32)
+    q, scale = gdr.gated_rmsnorm_i8(o, z, torch.ones(32, device="cuda"))
+    tail = slice(M - 40, M)
+    q2, scale2 = gdr.gated_rmsnorm_i8(o[tail].contiguous(), z[tail].contiguous(), torch.ones(32, device="cuda"))
+    assert torch.equal(q[tail], q2) and torch.equal(scale[tail], scale2)
+
+
 def test_add_rmsnorm_strides_and_in_place():
     base = rand(6, 5, 200, dtype=BF, seed=4)
     r, w = rand(6, 5, 96, dtype=BF, seed=5), rand(96, dtype=BF, seed=6)

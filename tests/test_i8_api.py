@@ -65,7 +65,7 @@ def test_norm_refusals(L, entry):
     assert fn(*[None] * (8 if entry == "add" else 7)) == ENULL
     for name in ("x", "w", "q", "scale") + (("r",) if entry == "gated" else ()):
         assert norm(L, entry, **{name: None}) == ENULL, name
-    for kw in (dict(rows=-1), dict(heads=0), dict(cols=0), dict(x_stride=-1), dict(r_stride=-1),
+    for kw in (dict(rows=-1), dict(rows=(1 << 30) + 1), dict(heads=0), dict(cols=0), dict(x_stride=-1), dict(r_stride=-1),
                dict(cols=32768 + 1) if entry == "add" else dict(heads=1025, cols=32),
                dict(rows=1 << 30, x_stride=1 << 40)):
         assert norm(L, entry, **kw) == ESHAPE, kw
@@ -119,7 +119,7 @@ def test_matmul_refusals(L):
     for kw in (dict(M=-1), dict(K=0), dict(K=131072, a_stride=131072, w_stride=131072), dict(n_out=0), dict(n_out=9),
                dict(a_stride=-1), dict(w_stride=-1), dict(out_cols=(0, 16)), dict(out_stride=(31, 16)),
                dict(out_cols=((1 << 30), 16)), dict(M=2147483647, out_cols=(1 << 20, 1 << 20)),
-               dict(M=1 << 30, a_stride=1 << 40)):
+               dict(M=1 << 30, a_stride=1 << 40), dict(M=(1 << 30) + 1)):
         assert product(L, **kw) == ESHAPE, kw
     assert product(L, out_dtype=2) == EUNSUP
     for kw in (dict(a_scale=addr(1, 2)), dict(w_scale=addr(6, 1)), dict(bias=addr(3, 2)), dict(outs=(addr(4, 1), 5)),
