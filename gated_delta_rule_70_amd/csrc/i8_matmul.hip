@@ -21,26 +21,33 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// 16 bytes at p + k of a row of K bytes, zeros from K on.  Any alignment.  A last partial chunk of
-// a row of at least 16 bytes is the row's last 16, shifted.
-__device__ __forceinline__ i32x4 load16(const int8_t* p, int k, int K) {
-    const int past = k + 16 - K;  // bytes of the chunk that lie behind the row
-    uint64_t lo = 0, hi = 0;
-    if (past <= 0) {
-        __builtin_memcpy(&lo, p + k, 8);
-        __builtin_memcpy(&hi, p + k + 8, 8);
-    } else if (past < 16 && K >= 16) {
-        __builtin_memcpy(&lo, p + (K - 16), 8);
-        __builtin_memcpy(&hi, p + (K - 8), 8);
-        const int sh = past * 8;
-        lo = sh < 64 ? lo >> sh | hi << (64 - sh) : hi >> (sh - 64);
-        hi = sh < 64 ? hi >> sh : 0;
-    } else if (past < 16) {
+// v[i] = 16 bytes at p[i] + k[i] of a row of K bytes, zeros from K on.  Any alignment.  A chunk that
+// passes the row's end is cut from the row's last 16 bytes, so that all loads are under way before
+// one is waited for (only rows of fewer than 16 bytes go byte by byte).
+template <int N>
+__device__ __forceinline__ void load_cut(const int8_t* const (&p)[N], const int (&k)[N], int K, i32x4 (&v)[N]) {
+    if (K >= 16) {
 #pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (i < K) (i < 8 ? lo : hi) |= static_cast<uint64_t>(static_cast<uint8_t>(p[i])) << (i % 8 * 8);
+        for (int i = 0; i < N; ++i) __builtin_memcpy(&v[i], p[i] + min(k[i], K - 16), 16);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int sh = (k[i] - min(k[i], K - 16)) * 8;  // bits to drop at the low end
+            const uint64_t lo = (uint32_t)v[i][0] | (uint64_t)(uint32_t)v[i][1] << 32;
+            const uint64_t hi = (uint32_t)v[i][2] | (uint64_t)(uint32_t)v[i][3] << 32;
+            const uint64_t low = sh < 64 ? lo >> (sh & 63) | hi << 1 << (63 - (sh & 63)) : sh < 128 ? hi >> (sh & 63) : 0;
+            const uint64_t high = sh < 64 ? hi >> (sh & 63) : 0;
+            v[i] = i32x4{(int)low, (int)(low >> 32), (int)high, (int)(high >> 32)};
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 15; ++j)
+                if (k[i] == 0 && j < K) u[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i][j])) << (j % 4 * 8);
+            v[i] = i32x4{(int)u[0], (int)u[1], (int)u[2], (int)u[3]};
+        }
     }
-    return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
 }
 
 // Where the outputs of columns n .. n+3 go: for each column its output's first value of row 0
@@ -96,8 +103,15 @@ __device__ __forceinline__ void store_quad(const MatmulArgs& g, int m, int n, i3
         }
 }
 
-// ---- up to 16 rows --------------------------------------------------------------------------
-// One workgroup makes 16 columns.  Its 8 waves share the reduction, 256 bytes in turn, each
+// Workgroups are dealt to the 8 XCDs in turn; this numbering gives each XCD a run of neighbouring
+// tiles, whose shared operands then stay in its L2.
+__device__ __forceinline__ int tile_of_workgroup(int total) {
+    const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
+    return xcd * (total >> 3) + min(xcd, total & 7) + nth;
+}
+
+// ---- few outputs ----------------------------------------------------------------------------
+// One workgroup makes 16 columns of 16 rows.  Its 8 waves share the reduction, 256 bytes in turn, each
 // straight from memory to registers to the matrix cores: every weight is read once and used at
 // once, so nothing is gained by LDS; the sums meet there at the end.
 template <bool BF16>
@@ -105,9 +119,10 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
     constexpr int WAVES = 8, U = 4, STEP = 64 * U;
     __shared__ i32x4 part[WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n0 = blockIdx.x * 16, kq = (lane >> 4) * 16;
+    const int tiles_m = (g.M + 15) / 16, id = tile_of_workgroup(gridDim.x);
+    const int m0 = id % tiles_m * 16, n0 = id / tiles_m * 16, kq = (lane >> 4) * 16;
     const int8_t* pw = g.w + min(n0 + (lane & 15), g.N - 1) * g.w_stride;
-    const int8_t* pa = g.a + min(lane & 15, g.M - 1) * g.a_stride;
+    const int8_t* pa = g.a + min(m0 + (lane & 15), g.M - 1) * g.a_stride;
     i32x4 acc = {};
     for (int k0 = wave * STEP; k0 < g.K; k0 += WAVES * STEP) {
         i32x4 fw[U], fa[U];
@@ -118,11 +133,14 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
                 __builtin_memcpy(&fa[u], pa + k0 + u * 64 + kq, 16);
             }
         } else {
+            const int8_t* p[2 * U];
+            int k[2 * U];
+            i32x4 v[2 * U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                fw[u] = load16(pw, k0 + u * 64 + kq, g.K);
-                fa[u] = load16(pa, k0 + u * 64 + kq, g.K);
-            }
+            for (int u = 0; u < 2 * U; ++u) p[u] = u < U ? pw : pa, k[u] = k0 + u % U * 64 + kq;
+            load_cut(p, k, g.K, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u) fw[u] = v[u], fa[u] = v[U + u];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) acc = mfma_i8(fw[u], fa[u], acc);
@@ -133,7 +151,7 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
         i32x4 s = part[0][lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) s += part[w][lane];
-        store_quad<BF16>(g, lane & 15, n0 + (lane >> 4) * 4, s);
+        store_quad<BF16>(g, m0 + (lane & 15), n0 + (lane >> 4) * 4, s);
     }
 }
 
@@ -153,13 +171,6 @@ __device__ __forceinline__ void wait_vmcnt() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
     asm volatile("" ::: "memory");
-}
-
-// Workgroups are dealt to the 8 XCDs in turn; this numbering gives each XCD a run of neighbouring
-// tiles, whose shared operands then stay in its L2.
-__device__ __forceinline__ int tile_of_workgroup(int total) {
-    const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
-    return xcd * (total >> 3) + min(xcd, total & 7) + nth;
 }
 
 // 16 bytes a lane from r at voff + soff to LDS at `to` + 16 * lane, without registers.
@@ -343,16 +354,20 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
         }
     }
     if (g.K % kBK != 0) {
-        const int s = full, k = full * kBK;
+        const int s = full;
+        const int8_t* p[LA + LW];
+        int k[LA + LW];
+        i32x4 v[LA + LW];
+#pragma unroll
+        for (int i = 0; i < LA + LW; ++i) {
+            k[i] = full * kBK + chunk * 16;
+            p[i] = i < LA ? ga + min(row + i * (NT / 8), last_m) * g.a_stride
+                          : gw + min(row + (i - LA) * (NT / 8), last_n) * g.w_stride;
+        }
+        load_cut(p, k, g.K, v);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < LA; ++i)
-            lds[s % STAGES][i * NT + tid] =
-                load16(ga + min(row + i * (NT / 8), last_m) * g.a_stride, k + chunk * 16, g.K);
-#pragma unroll
-        for (int i = 0; i < LW; ++i)
-            lds[s % STAGES][BM * 8 + i * NT + tid] =
-                load16(gw + min(row + i * (NT / 8), last_n) * g.w_stride, k + chunk * 16, g.K);
+        for (int i = 0; i < LA + LW; ++i) lds[s % STAGES][(i < LA ? i * NT : BM * 8 + (i - LA) * NT) + tid] = v[i];
         __syncthreads();
         compute(s);
     }
@@ -466,8 +481,11 @@ __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_ke
     i32x4 rest[LD];  // the last partial stage
     const bool partial = g.K % BK != 0;
     if (partial) {
+        const int8_t* p[LD];
+        int k[LD];
 #pragma unroll
-        for (int i = 0; i < LD; ++i) rest[i] = load16(source(i), full * BK + chunk * 16, g.K);
+        for (int i = 0; i < LD; ++i) p[i] = source(i), k[i] = full * BK + chunk * 16;
+        load_cut(p, k, g.K, rest);
     }
     i32x4 acc[2][2] = {};
     const int kg = wave % KG, block = wave / KG, wm = block / WN, wn = block % WN;
@@ -558,7 +576,7 @@ __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_ke
 }
 
 void rows(const MatmulArgs& g) {
-    const dim3 grid((unsigned)((g.N + 15) / 16));
+    const dim3 grid((unsigned)(((int64_t)g.M + 15) / 16 * ((g.N + 15) / 16)));
     if (g.out_bf16)
         hipLaunchKernelGGL(matmul_rows_kernel<true>, grid, dim3(512), 0, g.stream, g);
     else
@@ -602,16 +620,18 @@ bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
 //    2048 x  4096 x 4096  97.2   146.8    46.6     41.2 /  35.8           50.5
 //    4096 x  4096 x 1024  71.9    70.6    32.5     29.8 /  25.2           23.6
 //    8192 x  2048 x 8192   335     598     192      158 /   142            118
-// Up to 16 rows and 8192 columns (128 tiles of 64 columns, half the CUs) the form without tiles is
-// faster: 1 x 4096 x 4096 6.5 against 8.8 us; 1 x 12288 x 4096 12.6 against 11.1.
+// The form without tiles is faster where 16 x 16 outputs do not make more than one workgroup for
+// each CU (51 x 256 x 8100 8.6 against 17.3 us; at 64 x 2048 x 1024, twice that, 5.3 against 5.1)
+// and up to 16 rows and 8192 columns (1 x 4096 x 4096 6.5 against 8.8 us; 1 x 12288 x 4096 12.6
+// against 11.1).
 enum class Form { rows, t32x64, t64x32, t128x64, t128x128_deep, t128x128, t256x256 };
 struct Plan {
     Form form;
     double us;
 };
 Plan plan(int64_t M, int64_t N, int K) {
-    Plan best{Form::rows, M <= 16 && N <= 8192 ? 1.0 + 1.3e-3 * K : 1e30};
-    if (best.us < 1e30) return best;
+    if ((M <= 16 && N <= 8192) || (M + 15) / 16 * ((N + 15) / 16) <= 256) return Plan{Form::rows, 1.0 + 1.3e-3 * K};
+    Plan best{Form::t32x64, 1e30};
     auto offer = [&](Form f, int bm, int bn, int64_t least, int64_t most, double fixed, double per_k) {
         const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
         if (tiles < least || tiles > most) return;
