@@ -21,19 +21,58 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// v[i] = 16 bytes at p[i] + k[i] of a row of K bytes, zeros from K on.  Any alignment.  A chunk that
-// passes the row's end is cut from the row's last 16 bytes, so that all loads are under way before
-// one is waited for (only rows of fewer than 16 bytes go byte by byte).
-template <int N>
-__device__ __forceinline__ void load_cut(const int8_t* const (&p)[N], const int (&k)[N], int K, i32x4 (&v)[N]) {
-    if (K >= 16) {
+// Bytes at any address.  A load of 16 bytes from an address that is no multiple of 4 is served
+// many times slower than one that is (20 x 680 x 3344: 11.7 against 5.7 us), so 16 bytes at p are
+// taken from a window of 20 that begins at the multiple of 4 before p, and moved into place.  The
+// window is kept inside the operand (`first` to 20 bytes before its end, `last`), so that nothing
+// outside it is read; at its two ends the window then begins elsewhere, up to 4 bytes before p.
+struct Extent {
+    const int8_t *first, *last;
+};
+__device__ __forceinline__ Extent extent_of(const int8_t* p, int64_t rows, int64_t stride, int K) {
+    return Extent{p, p + (rows - 1) * stride + K - 20};
+}
+struct Window {
+    i32x4 v;
+    int v4;
+    int drop;  // bytes before p, 0 .. 4
+};
+__device__ __forceinline__ Window load_window(const int8_t* p, Extent e) {
+    const int8_t* w = p - (reinterpret_cast<uintptr_t>(p) & 3u);
+    w = w < e.first ? e.first : w;
+    w = w > e.last ? e.last : w;
+    Window r;
+    __builtin_memcpy(&r.v, w, 16);
+    __builtin_memcpy(&r.v4, w + 16, 4);
+    r.drop = (int)(p - w);
+    return r;
+}
+__device__ __forceinline__ i32x4 bytes_of(const Window& w) {
+    const bool b = w.drop == 4;
+    const uint32_t d[5] = {(uint32_t)(b ? w.v[1] : w.v[0]), (uint32_t)(b ? w.v[2] : w.v[1]), (uint32_t)(b ? w.v[3] : w.v[2]),
+                           (uint32_t)(b ? w.v4 : w.v[3]), (uint32_t)w.v4};
+    i32x4 r;
 #pragma unroll
-        for (int i = 0; i < N; ++i) __builtin_memcpy(&v[i], p[i] + min(k[i], K - 16), 16);
+    for (int i = 0; i < 4; ++i) r[i] = (int)__builtin_amdgcn_alignbyte(d[i + 1], d[i], (uint32_t)w.drop & 3u);
+    return r;
+}
+
+// v[i] = 16 bytes at p[i] + k[i] of a row of K bytes, zeros from K on.  A chunk that passes the row's
+// end is cut from the row's last 16 bytes, so that all loads are under way before one is waited for
+// (only rows of fewer than 20 bytes go byte by byte).  e[i]: the operand that p[i] is a row of.
+template <int N>
+__device__ __forceinline__ void load_cut(const int8_t* const (&p)[N], const int (&k)[N], int K, const Extent (&e)[N],
+                                         i32x4 (&v)[N]) {
+    if (K >= 20) {
+        Window w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = load_window(p[i] + min(k[i], K - 16), e[i]);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            const i32x4 u = bytes_of(w[i]);
             const int sh = (k[i] - min(k[i], K - 16)) * 8;  // bits to drop at the low end
-            const uint64_t lo = (uint32_t)v[i][0] | (uint64_t)(uint32_t)v[i][1] << 32;
-            const uint64_t hi = (uint32_t)v[i][2] | (uint64_t)(uint32_t)v[i][3] << 32;
+            const uint64_t lo = (uint32_t)u[0] | (uint64_t)(uint32_t)u[1] << 32;
+            const uint64_t hi = (uint32_t)u[2] | (uint64_t)(uint32_t)u[3] << 32;
             const uint64_t low = sh < 64 ? lo >> (sh & 63) | hi << 1 << (63 - (sh & 63)) : sh < 128 ? hi >> (sh & 63) : 0;
             const uint64_t high = sh < 64 ? hi >> (sh & 63) : 0;
             v[i] = i32x4{(int)low, (int)(low >> 32), (int)high, (int)(high >> 32)};
@@ -43,8 +82,8 @@ __device__ __forceinline__ void load_cut(const int8_t* const (&p)[N], const int 
         for (int i = 0; i < N; ++i) {
             uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < 15; ++j)
-                if (k[i] == 0 && j < K) u[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i][j])) << (j % 4 * 8);
+            for (int j = 0; j < 16; ++j)
+                if (k[i] + j < K) u[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i][k[i] + j])) << (j % 4 * 8);
             v[i] = i32x4{(int)u[0], (int)u[1], (int)u[2], (int)u[3]};
         }
     }
@@ -114,7 +153,9 @@ __device__ __forceinline__ int tile_of_workgroup(int total) {
 // One workgroup makes 16 columns of 16 rows.  Its 8 waves share the reduction, 256 bytes in turn, each
 // straight from memory to registers to the matrix cores: every weight is read once and used at
 // once, so nothing is gained by LDS; the sums meet there at the end.
-template <bool BF16>
+// ALIGN: pointers and row strides are multiples of 4 and K is one of 16 (16: chunks are whole), are
+// multiples of 4 (4), or anything (1).
+template <int ALIGN, bool BF16>
 __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
     constexpr int WAVES = 8, U = 4, STEP = 64 * U;
     __shared__ i32x4 part[WAVES][64];
@@ -123,22 +164,41 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
     const int m0 = id % tiles_m * 16, n0 = id / tiles_m * 16, kq = (lane >> 4) * 16;
     const int8_t* pw = g.w + min(n0 + (lane & 15), g.N - 1) * g.w_stride;
     const int8_t* pa = g.a + min(m0 + (lane & 15), g.M - 1) * g.a_stride;
+    const Extent ea = extent_of(g.a, g.M, g.a_stride, g.K), ew = extent_of(g.w, g.N, g.w_stride, g.K);
     i32x4 acc = {};
     for (int k0 = wave * STEP; k0 < g.K; k0 += WAVES * STEP) {
         i32x4 fw[U], fa[U];
-        if (k0 + STEP <= g.K) {
+        if constexpr (ALIGN == 16) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * 64 + kq, from = k < g.K ? k : 0;
+                __builtin_memcpy(&fw[u], pw + from, 16);
+                __builtin_memcpy(&fa[u], pa + from, 16);
+                if (k >= g.K) fw[u] = i32x4{0, 0, 0, 0};
+            }
+        } else if (ALIGN == 4 && k0 + STEP <= g.K) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 __builtin_memcpy(&fw[u], pw + k0 + u * 64 + kq, 16);
                 __builtin_memcpy(&fa[u], pa + k0 + u * 64 + kq, 16);
             }
+        } else if (k0 + STEP <= g.K) {
+            Window w[U], a[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                w[u] = load_window(pw + k0 + u * 64 + kq, ew);
+                a[u] = load_window(pa + k0 + u * 64 + kq, ea);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) fw[u] = bytes_of(w[u]), fa[u] = bytes_of(a[u]);
         } else {
             const int8_t* p[2 * U];
             int k[2 * U];
+            Extent e[2 * U];
             i32x4 v[2 * U];
 #pragma unroll
-            for (int u = 0; u < 2 * U; ++u) p[u] = u < U ? pw : pa, k[u] = k0 + u % U * 64 + kq;
-            load_cut(p, k, g.K, v);
+            for (int u = 0; u < 2 * U; ++u) p[u] = u < U ? pw : pa, e[u] = u < U ? ew : ea, k[u] = k0 + u % U * 64 + kq;
+            load_cut(p, k, g.K, e, v);
 #pragma unroll
             for (int u = 0; u < U; ++u) fw[u] = v[u], fa[u] = v[U + u];
         }
@@ -219,6 +279,7 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
 #pragma unroll
         for (int i = 0; i < LW; ++i) vw[i] = min(row + i * (NT / 8), last_n) * (int)g.w_stride + chunk * 16;
     }
+    const Extent ea = extent_of(g.a, g.M, g.a_stride, g.K), ew = extent_of(g.w, g.N, g.w_stride, g.K);
     i32x4 hold[DMA ? 1 : LA + LW];
     auto fetch = [&](int s) {
         const int k = s * kBK;
@@ -357,14 +418,16 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
         const int s = full;
         const int8_t* p[LA + LW];
         int k[LA + LW];
+        Extent e[LA + LW];
         i32x4 v[LA + LW];
 #pragma unroll
         for (int i = 0; i < LA + LW; ++i) {
             k[i] = full * kBK + chunk * 16;
+            e[i] = i < LA ? ea : ew;
             p[i] = i < LA ? ga + min(row + i * (NT / 8), last_m) * g.a_stride
                           : gw + min(row + (i - LA) * (NT / 8), last_n) * g.w_stride;
         }
-        load_cut(p, k, g.K, v);
+        load_cut(p, k, g.K, e, v);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < LA + LW; ++i) lds[s % STAGES][(i < LA ? i * NT : BM * 8 + (i - LA) * NT) + tid] = v[i];
@@ -470,6 +533,8 @@ __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_ke
     const int row = tid / CPR, chunk = (tid % CPR) ^ (row & 7);
     static_assert(NT / CPR % 8 == 0, "rows of one thread's loads agree modulo 8");
     const int full = g.K / BK;
+    const Extent ea = extent_of(g.a, g.M, g.a_stride, g.K), ew = extent_of(g.w, g.N, g.w_stride, g.K);
+    auto extent = [&](int i) { return row + i * (NT / CPR) < BM ? ea : ew; };
     auto source = [&](int i) {  // start of the row that this thread's load i brings a chunk of
         const int r = row + i * (NT / CPR);
         return r < BM ? ga + min(r, last_m) * g.a_stride : gw + min(r - BM, last_n) * g.w_stride;
@@ -483,9 +548,10 @@ __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_ke
     if (partial) {
         const int8_t* p[LD];
         int k[LD];
+        Extent e[LD];
 #pragma unroll
-        for (int i = 0; i < LD; ++i) p[i] = source(i), k[i] = full * BK + chunk * 16;
-        load_cut(p, k, g.K, rest);
+        for (int i = 0; i < LD; ++i) p[i] = source(i), k[i] = full * BK + chunk * 16, e[i] = extent(i);
+        load_cut(p, k, g.K, e, rest);
     }
     i32x4 acc[2][2] = {};
     const int kg = wave % KG, block = wave / KG, wm = block / WN, wn = block % WN;
@@ -575,12 +641,13 @@ __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_ke
     }
 }
 
+template <int ALIGN>
 void rows(const MatmulArgs& g) {
     const dim3 grid((unsigned)(((int64_t)g.M + 15) / 16 * ((g.N + 15) / 16)));
     if (g.out_bf16)
-        hipLaunchKernelGGL(matmul_rows_kernel<true>, grid, dim3(512), 0, g.stream, g);
+        hipLaunchKernelGGL((matmul_rows_kernel<ALIGN, true>), grid, dim3(512), 0, g.stream, g);
     else
-        hipLaunchKernelGGL(matmul_rows_kernel<false>, grid, dim3(512), 0, g.stream, g);
+        hipLaunchKernelGGL((matmul_rows_kernel<ALIGN, false>), grid, dim3(512), 0, g.stream, g);
 }
 
 template <int BM, int BN, int KG, int STAGES, int REGS, bool DMA>
@@ -600,6 +667,11 @@ void tiles(const MatmulArgs& g) {
         hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, true>), grid, dim3(WM * WN * 64), 0, g.stream, g);
     else
         hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, false>), grid, dim3(WM * WN * 64), 0, g.stream, g);
+}
+
+bool words_ok(const MatmulArgs& g) {
+    return ((reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.w)) & 3u) == 0 &&
+           (g.M == 1 || g.a_stride % 4 == 0) && (g.N == 1 || g.w_stride % 4 == 0);
 }
 
 bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
@@ -652,7 +724,7 @@ Plan plan(int64_t M, int64_t N, int K) {
 template <bool DMA>
 void start(Form f, const MatmulArgs& g) {
     switch (f) {
-        case Form::rows: rows(g); break;
+        case Form::rows: words_ok(g) ? g.K % 16 == 0 ? rows<16>(g) : rows<4>(g) : rows<1>(g); break;
         case Form::t32x64: small<32, 64, 4, 3, 4, DMA>(g); break;
         case Form::t64x32: small<64, 32, 4, 3, 4, DMA>(g); break;
         case Form::t128x64: tiles<128, 64, 4, 2, 3, DMA>(g); break;
