@@ -92,7 +92,8 @@ def _code(t, name):
 
 
 def _stream(stream, dev, names, tensors):
-    """The stream's handle, once all tensors are known to be on the current GPU."""
+    """The stream's handle, once all tensors are known to be on the current GPU (``dev``: that of
+    one of them)."""
     if dev >= 0 and dev == _current_device():
         for t in tensors:
             if t is not None and t.get_device() != dev:
@@ -120,8 +121,6 @@ def _stream(stream, dev, names, tensors):
 def _rows(t, name, tail=1):
     """Elements from one row to the next of ``t``, whose last ``tail`` dimensions make a row: a
     row's values have to lie next to each other, and the rows evenly apart."""
-    if t.is_contiguous():
-        return math.prod(t.shape[-tail:]) if tail > 1 else t.shape[-1]
     shape, strides = t.shape, t.stride()
     lead = len(shape) - tail
     step = 1
@@ -155,9 +154,12 @@ def _out(t, name, shape, dtype, device):
 
 
 def _eps(eps):
-    if not 0 <= eps <= 3.4028234663852886e38:
-        raise ValueError(f"eps must be finite and not negative, got {eps}")
-    return eps
+    raise ValueError(f"eps must be finite in fp32 and not negative, got {eps}")
+
+
+_F32_MAX = 3.4028234663852886e38
+_NORM_NAMES = ("weight", "residual", "q", "scale", "out_residual", "x")
+_GATED_NAMES = ("gate", "weight", "q", "scale", "o")
 
 
 def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=None, out_residual=None, stream=None):
@@ -193,19 +195,22 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
             raise ValueError(f"residual must be {list(shape)}, got {list(residual.shape)}")
         if residual.dtype is not dtype:
             raise TypeError(f"residual must be {dtype}, got {residual.dtype}")
-        r_stride = _rows(residual, "residual")
+        r_stride = D if residual.is_contiguous() else _rows(residual, "residual")
         if out_residual is None:
             out_residual = torch.empty(shape, dtype=dtype, device=x.device)
         if out_residual.shape != shape:
             raise ValueError(f"out_residual must be {list(shape)}, got {list(out_residual.shape)}")
         if out_residual.dtype is not dtype:
             raise TypeError(f"out_residual must be {dtype}, got {out_residual.dtype}")
-        out_stride = _rows(out_residual, "out_residual")
-    q = _out(q, "q", shape, _I8, x.device)
-    scale = _out(scale, "scale", shape[:-1], _F32, x.device)
-    dims = _NORM.pack(scale.numel(), 1, D, xc, 0, _CODE[wt], _eps(eps), _rows(x, "x"), r_stride, out_stride)
-    s = _stream(stream, x.get_device(), ("x", "weight", "residual", "q", "scale", "out_residual"),
-                (x, weight, residual, q, scale, out_residual))
+        out_stride = D if out_residual.is_contiguous() else _rows(out_residual, "out_residual")
+    lead = shape[:-1]
+    if q is None or q.shape != shape or q.dtype is not _I8 or not q.is_contiguous():
+        q = _out(q, "q", shape, _I8, x.device)
+    if scale is None or scale.shape != lead or scale.dtype is not _F32 or not scale.is_contiguous():
+        scale = _out(scale, "scale", lead, _F32, x.device)
+    dims = _NORM.pack(scale.numel(), 1, D, xc, 0, _CODE[wt], eps if 0 <= eps <= _F32_MAX else _eps(eps),
+                      D if x.is_contiguous() else _rows(x, "x"), r_stride, out_stride)
+    s = _stream(stream, x.get_device(), _NORM_NAMES, (weight, residual, q, scale, out_residual, x))
     status = (_L or _lib()).gdr_add_rmsnorm_i8(
         dims, x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), q.data_ptr(),
         scale.data_ptr(), None if out_residual is None else out_residual.data_ptr(), s)
@@ -237,10 +242,16 @@ def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, str
     if not weight.is_contiguous():
         raise ValueError("weight must be contiguous")
     lead = shape[:-2]
-    q = _out(q, "q", (*lead, H * V), _I8, o.device)
-    scale = _out(scale, "scale", lead, _F32, o.device)
-    dims = _NORM.pack(scale.numel(), H, V, oc, gc, wc, _eps(eps), _rows(o, "o", 2), _rows(gate, "gate", 2), 0)
-    s = _stream(stream, o.get_device(), ("o", "gate", "weight", "q", "scale"), (o, gate, weight, q, scale))
+    D = H * V
+    qshape = (*lead, D)
+    if q is None or q.shape != qshape or q.dtype is not _I8 or not q.is_contiguous():
+        q = _out(q, "q", qshape, _I8, o.device)
+    if scale is None or scale.shape != lead or scale.dtype is not _F32 or not scale.is_contiguous():
+        scale = _out(scale, "scale", lead, _F32, o.device)
+    dims = _NORM.pack(scale.numel(), H, V, oc, gc, wc, eps if 0 <= eps <= _F32_MAX else _eps(eps),
+                      D if o.is_contiguous() else _rows(o, "o", 2),
+                      D if gate.is_contiguous() else _rows(gate, "gate", 2), 0)
+    s = _stream(stream, o.get_device(), _GATED_NAMES, (gate, weight, q, scale, o))
     status = (_L or _lib()).gdr_gated_rmsnorm_i8(dims, o.data_ptr(), gate.data_ptr(), weight.data_ptr(),
                                                  q.data_ptr(), scale.data_ptr(), s)
     if status:
@@ -268,8 +279,10 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
         raise TypeError(f"a must be int8, got {a.dtype}")
     if w.dtype is not _I8:
         raise TypeError(f"w must be int8, got {w.dtype}")
-    _vector(a_scale, "a_scale", lead)
-    _vector(w_scale, "w_scale", (N,))
+    if a_scale is None or a_scale.shape != lead or a_scale.dtype is not _F32 or not a_scale.is_contiguous():
+        _vector(a_scale, "a_scale", lead)
+    if w_scale is None or w_scale.shape != (N,) or w_scale.dtype is not _F32 or not w_scale.is_contiguous():
+        _vector(w_scale, "w_scale", (N,))
     if bias is not None:
         _vector(bias, "bias", (N,))
     single = out is None or isinstance(out, torch.Tensor)
@@ -277,24 +290,30 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     n = len(outs)
     if not 1 <= n <= MATMUL_I8_MAX_OUT:
         raise ValueError(f"1 to {MATMUL_I8_MAX_OUT} outputs are supported, got {n}")
-    cols = [t if isinstance(t, int) else t.shape[-1] if t.dim() else 0 for t in outs]
-    if min(cols) < 1 or sum(cols) != N:
-        raise ValueError(f"the outputs' columns {cols} must be positive and add up to {N}")
     for i, t in enumerate(outs):
-        if isinstance(t, int):
+        if isinstance(t, int) and t > 0:
             outs[i] = torch.empty(*lead, t, dtype=out_dtype, device=a.device)
-    dtype = outs[0].dtype
-    oc = _code(outs[0], "out")
-    strides, ptrs = [], []
+    matrix = len(lead) == 1
+    dtype, cols, strides, ptrs = None, [], [], []
     for t in outs:
-        if t.shape[:-1] != lead:
-            raise ValueError(f"out must be {[*lead, t.shape[-1]]}, got {list(t.shape)}")
-        if t.dtype is not dtype:
+        oshape = t.shape if isinstance(t, torch.Tensor) else ()
+        if not oshape or oshape[-1] < 1:
+            cols = [u.shape[-1] if isinstance(u, torch.Tensor) and u.dim() else u for u in outs]
+            raise ValueError(f"the outputs' columns {cols} must be positive and add up to {N}")
+        if (len(oshape) != 2 or oshape[0] != lead[0]) if matrix else oshape[:-1] != lead:
+            raise ValueError(f"out must be {[*lead, oshape[-1]]}, got {list(oshape)}")
+        if dtype is None:
+            dtype, oc = t.dtype, _code(t, "out")
+        elif t.dtype is not dtype:
             raise TypeError(f"outputs must be of one type, got {dtype} and {t.dtype}")
-        strides.append(_rows(t, "out"))
+        cols.append(oshape[-1])
+        strides.append(oshape[-1] if t.is_contiguous() else _rows(t, "out"))
         ptrs.append(t.data_ptr())
+    if sum(cols) != N:
+        raise ValueError(f"the outputs' columns {cols} must be positive and add up to {N}")
     none = _NONE[n:]
-    dims = _MATMUL.pack(a_scale.numel(), K, n, oc, *cols, *none, *strides, *none, _rows(a, "a"), _rows(w, "w"))
+    dims = _MATMUL.pack(a_scale.numel(), K, n, oc, *cols, *none, *strides, *none,
+                        K if a.is_contiguous() else _rows(a, "a"), K if w.is_contiguous() else _rows(w, "w"))
     s = _stream(stream, a.get_device(), _MATMUL_NAMES, (a, a_scale, w, w_scale, bias, *outs))
     status = (_L or _lib()).gdr_matmul_i8(dims, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
                                           None if bias is None else bias.data_ptr(), _PTRS.pack(*ptrs, *none), s)
