@@ -1,6 +1,13 @@
 // int8 matrix product with a scale for each row of a and of w:
 //   out[m][n] = (sum_k a[m][k] w[n][k]) * a_scale[m] * w_scale[n] + bias[n]
-// Sums are int32 in the matrix cores (v_mfma_i32_16x16x64_i8), exact for K <= 131071.
+// Sums are int32 in the matrix cores (v_mfma_i32_16x16x64_i8), exact for K <= 131071.  Scales and
+// bias are applied in fp32; a bf16 output is rounded once, as it is stored.
+//
+// Forms, by how many outputs there are (see plan()): 16 x 16 outputs by 8 waves that share the
+// reduction, without LDS staging; small tiles whose waves share the reduction; 128-wide tiles;
+// 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 10.4 us, 4.8 TB/s,
+// the rate of a large copy being 5.1.  At 32768 x 4096 x 4096 the chip is limited by power: 447 us,
+// 2460 TOP/s (the library's int8 product reaches 2070 on 8192^3).
 #include "i8_launch.h"
 
 #include <type_traits>
@@ -222,6 +229,12 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
 //   DMA   memory to LDS without registers (16 bytes a lane): pointers and row strides are
 //         multiples of 16 and a tile's rows lie within 2^31 bytes;
 //   else  through registers, at any alignment, a stage ahead.
+// What bounds the 256 x 256 form: at 8192^3 the matrix cores are busy 74 % of the time at a clock of
+// 1.83 GHz; an order of issue with 68 % busy ran at 1.94 GHz and took the same time, so it is the
+// power that a product costs.  Tried and dropped (8192^3, 430 us): 32x32x32 products, 457;
+// four waves of 128 x 128 each, a third fewer LDS reads but nothing to cover a wait, 477; 64-byte
+// stages, five deep, 621 (half lines cost as many requests as whole ones); touching lines two
+// stages ahead to have them in L2, 515; higher wave priority around the products, 519.
 // Rows past the end repeat the last one (their results are dropped); the reduction's last
 // partial 128 bytes go through registers, with zeros behind them.
 constexpr int kBK = 128;
@@ -511,7 +524,8 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
 // workgroup; each wave makes a 32 x 32 block, and KG groups of waves share the reduction: a stage
 // is KG * 64 bytes of it, group k takes the k-th 64, and the groups' sums meet in LDS.  What bounds
 // these products is how fast a CU can bring its operands in, so the loop keeps STAGES - 1 stages
-// in flight (DMA), or REGS stages in registers (any alignment).
+// in flight (DMA), or REGS stages in registers (any alignment).  32 x 12288 x 4096: 10.7 us, 4.8
+// TB/s; 128 x 4096 x 4096: 9.7 us, where each CU brings 393 KB in at 50 bytes a ns.
 template <int BM, int BN, int KG, int STAGES, int REGS, bool DMA, bool BF16>
 __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_kernel(MatmulArgs g) {
     constexpr int WN = BN / 32, WAVES = BM / 32 * WN * KG, NT = WAVES * 64;
