@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["gdr_api.cpp", "decode.hip", "chunk_prep.hip", "chunk_prep_split.hip", "chunk_carry.hip",
            "chunk_carry_wide.hip", "tree_verify.hip", "varlen_plan.hip", "i8_api.cpp", "i8_norm.hip",
@@ -53,10 +55,31 @@ def _compile(src: str) -> str:
     return out
 
 
+def _compile_binding() -> None:
+    """The Python extension of the 8-bit operators (csrc/binding.cpp), host code against PyTorch's
+    headers."""
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    paths = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f for p in paths for f in ("-isystem", p)],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{res.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)

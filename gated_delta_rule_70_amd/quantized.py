@@ -16,7 +16,8 @@ Calls allocate nothing but the outputs that are not given, and can be captured i
 from __future__ import annotations
 
 import ctypes
-import math
+import importlib.util
+import os
 import struct
 
 import torch
@@ -44,8 +45,7 @@ class MatmulDims(ctypes.Structure):
                 ("w_stride", ctypes.c_int64)]
 
 
-# The same layouts packed into bytes: a fraction of the time of filling a Structure, which counts
-# next to kernels of a few microseconds.
+# The same layouts packed into bytes, which takes a fraction of the time of filling a Structure.
 _NORM = struct.Struct("@6if3q")
 _MATMUL = struct.Struct(f"@4i{MATMUL_I8_MAX_OUT}i{MATMUL_I8_MAX_OUT}q2q")
 _PTRS = struct.Struct(f"@{MATMUL_I8_MAX_OUT}Q")
@@ -76,6 +76,26 @@ def _lib():
 
         _L = gdr.lib()
     return _L
+
+
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+_B = None
+
+
+def _binding():
+    """The extension that takes ordinary calls straight to the library (csrc/binding.cpp)."""
+    global _B
+    if _B is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is not built; run `python -m gated_delta_rule_70_amd.build`")
+        L = _lib()
+        spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(f, _VP).value for f in (L.gdr_add_rmsnorm_i8, L.gdr_gated_rmsnorm_i8, L.gdr_matmul_i8)),
+               _current_device, _raw_stream)
+        _B = m
+    return _B
 
 
 def _fail(status):
@@ -172,6 +192,8 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
     (which may be ``x`` or ``residual`` itself), and is None without a residual.  A row of
     zeros has scale 0, a row that holds NaN or infinity scale NaN and q 0.
     """
+    if stream is None and (_B or _binding()).add_rmsnorm(x, weight, residual, eps, q, scale, out_residual):
+        return q, scale, out_residual
     shape, dtype = x.shape, x.dtype
     if not shape or shape[-1] < 1:
         raise ValueError(f"x must be [..., D], got {list(shape)}")
@@ -226,6 +248,8 @@ def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, str
     ``o`` and ``gate`` are ``[..., HV, dv]`` (bf16 or fp32 each; dv 32, 64 or 128), ``weight``
     ``[dv]`` (bf16 or fp32).  Returns ``q`` (int8, ``[..., HV * dv]``) and ``scale`` (fp32, ``[...]``).
     """
+    if stream is None and (_B or _binding()).gated_rmsnorm(o, gate, weight, eps, q, scale):
+        return q, scale
     shape = o.shape
     if len(shape) < 2:
         raise ValueError(f"o must be [..., HV, dv], got {list(shape)}")
@@ -269,6 +293,8 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     output, a sequence of column counts for that many new tensors, or a sequence of tensors (of
     one type; their rows may be strided).  Returns a tensor, or a tuple for a sequence.
     """
+    if stream is None and (_B or _binding()).matmul(a, a_scale, w, w_scale, bias, out):
+        return out if isinstance(out, torch.Tensor) else tuple(out)
     shape, wshape = a.shape, w.shape
     if not shape or len(wshape) != 2 or shape[-1] != wshape[1]:
         raise ValueError(f"a must be [..., K] and w [N, K], got {list(shape)} and {list(wshape)}")

@@ -376,6 +376,47 @@ def test_repeatable_and_on_another_stream(M):
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("M", [1, 70])
+def test_both_ways_into_the_library(M, monkeypatch):
+    """Calls with every tensor given go through the extension, others through Python: the same
+    results, and each is the way taken."""
+    x, res, nw, w1, s1, w2, s2, hw = chain_inputs(M, 30)
+    q8, sc, h = torch.empty(M, 512, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"), torch.empty_like(x)
+    o, z = (torch.empty(M, 256, dtype=BF, device="cuda") for _ in range(2))
+    g8, sc2, y = torch.empty(M, 256, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"), torch.empty_like(x)
+
+    def given():
+        gdr.add_rmsnorm_i8(x, nw, residual=res, q=q8, scale=sc, out_residual=h)
+        assert gdr.matmul_i8(q8, sc, w1, s1, out=[o, z]) == (o, z)
+        gdr.gated_rmsnorm_i8(o.view(-1, 4, 64), z.view(-1, 4, 64), hw, q=g8, scale=sc2)
+        assert gdr.matmul_i8(g8, sc2, w2, s2, out=y) is y
+        return [t.clone() for t in (h, sc, sc2, y)]
+
+    python = chain(x, res, nw, w1, s1, w2, s2, hw)
+    with monkeypatch.context() as m:
+        m.setattr(gdr.quantized, "_stream", None)      # the way through Python would raise
+        native = given()
+    with monkeypatch.context() as m:
+        class Never:
+            add_rmsnorm = gated_rmsnorm = matmul = staticmethod(lambda *a: None)
+        m.setattr(gdr.quantized, "_B", Never)
+        slow = given()
+    for a, b, c in zip(python, native, slow):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    # bias, and no residual
+    b = torch.ones(512, device="cuda")
+    assert torch.equal(gdr.matmul_i8(g8, sc2, w2, s2, bias=b, out=y).clone(), gdr.matmul_i8(g8, sc2, w2, s2, bias=b))
+    gdr.add_rmsnorm_i8(x, nw, q=q8, scale=sc)
+    q_ref, sc_ref, none = gdr.add_rmsnorm_i8(x, nw)
+    assert none is None and torch.equal(q8, q_ref) and torch.equal(sc, sc_ref)
+    # an error status comes back as the exception: the codes over the input
+    with pytest.raises(gdr.GdrError) as e:
+        gdr.add_rmsnorm_i8(x, nw, q=x.view(-1).view(torch.int8)[:M * 512].view(M, 512), scale=sc)
+    assert e.value.status == 5
+    with pytest.raises(ValueError, match="scale must be"):
+        gdr.add_rmsnorm_i8(x, nw, q=q8, scale=torch.empty(M + 1, device="cuda"))
+
+
 def test_stream_argument():
     """Calls given another stream than the current one, whose inputs are dropped at once."""
     side = torch.cuda.Stream()
