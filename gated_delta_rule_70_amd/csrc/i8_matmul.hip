@@ -697,20 +697,21 @@ bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
 // of rounds over the 256 CUs times what a tile takes: a fixed part (filling the pipeline, storing)
 // and a part for each reduction byte, by how fast a CU brings BM + BN rows in (50 to 70 bytes a
 // ns) or, for 256 x 256, multiplies them.  Constants fitted to measurements, M x N x K in us:
-//                        32x64   64x32  128x64  128x128 (4 / 2 stages)  256x256
-//      32 x 12288 x 4096  11.9    12.7    14.5     17.3 /  22.5           42.2
-//     128 x  4096 x 4096   9.8     9.6    13.7     17.1 /  22.9           42.3
-//     512 x  4096 x 4096  24.0    23.9    16.1     19.2 /  24.1           44.5
-//    1024 x  4096 x 4096  48.5    44.9    24.6     21.1 /  26.2           46.1
-//     512 x 12288 x 4096  62.1    62.2    35.6     36.9 /  32.1           50.0
-//    2048 x  4096 x 4096  97.2   146.8    46.6     41.2 /  35.8           50.5
-//    4096 x  4096 x 1024  71.9    70.6    32.5     29.8 /  25.2           23.6
-//    8192 x  2048 x 8192   335     598     192      158 /   142            118
+//                        32x64  128x64  128x128 (4 / 2 stages)  256x256
+//      32 x 12288 x 4096  11.9    14.5     17.3 /  22.5           42.2
+//     128 x  4096 x 4096   9.8    13.7     17.1 /  22.9           42.3
+//     512 x  4096 x 4096  24.0    16.1     19.2 /  24.1           44.5
+//    1024 x  4096 x 4096  48.5    24.6     21.1 /  26.2           46.1
+//     512 x 12288 x 4096  62.1    35.6     36.9 /  32.1           50.0
+//    2048 x  4096 x 4096  97.2    46.6     41.2 /  35.8           50.5
+//    4096 x  4096 x 1024  71.9    32.5     29.8 /  25.2           23.6
+//    8192 x  2048 x 8192   335     192      158 /   142            118
+// (64 x 32 tiles take what 32 x 64 take.)
 // The form without tiles is faster where 16 x 16 outputs do not make more than one workgroup for
 // each CU (51 x 256 x 8100 8.6 against 17.3 us; at 64 x 2048 x 1024, twice that, 5.3 against 5.1)
 // and up to 16 rows and 8192 columns (1 x 4096 x 4096 6.5 against 8.8 us; 1 x 12288 x 4096 12.6
 // against 11.1).
-enum class Form { rows, t32x64, t64x32, t128x64, t128x128_deep, t128x128, t256x256 };
+enum class Form { rows, t32x64, t128x64, t128x128_deep, t128x128, t256x256 };
 struct Plan {
     Form form;
     double us;
@@ -727,7 +728,6 @@ Plan plan(int64_t M, int64_t N, int K) {
     };
     constexpr int64_t any = (1 << 23) - 1;  // a launch has fewer than 2^32 threads, 512 for each tile
     offer(Form::t32x64, 32, 64, 1, any, 0.8, 1.9);
-    offer(Form::t64x32, 64, 32, 1, any, 0.8, 1.9);
     offer(Form::t128x64, 128, 64, 1, any, 1.0, 2.8);
     offer(Form::t128x128_deep, 128, 128, 1, 256, 1.8, 4.2);
     offer(Form::t128x128, 128, 128, 257, any, 1.8, 3.6);
@@ -740,7 +740,6 @@ void start(Form f, const MatmulArgs& g) {
     switch (f) {
         case Form::rows: words_ok(g) ? g.K % 16 == 0 ? rows<16>(g) : rows<4>(g) : rows<1>(g); break;
         case Form::t32x64: small<32, 64, 4, 3, 4, DMA>(g); break;
-        case Form::t64x32: small<64, 32, 4, 3, 4, DMA>(g); break;
         case Form::t128x64: tiles<128, 64, 4, 2, 3, DMA>(g); break;
         case Form::t128x128_deep: tiles<128, 128, 2, 4, DMA ? 4 : 2, DMA>(g); break;
         case Form::t128x128: tiles<128, 128, 2, 4, 2, DMA>(g); break;

@@ -146,6 +146,53 @@ def test_add_rmsnorm_strides_and_in_place():
     assert torch.equal(q3.cpu().double(), norm_reference(x, w, None, 1e-6)[1])
 
 
+def test_single_vectors():
+    x, w = rand(96, dtype=BF, seed=1), rand(96, dtype=BF, seed=2)
+    q, scale, none = gdr.add_rmsnorm_i8(x.cuda(), w.cuda())
+    s, q_ref, scale_ref = norm_reference(x, w, None, 1e-6)
+    assert q.shape == (96,) and scale.shape == () and none is None and torch.equal(q.cpu().double(), q_ref)
+    wq, ws = gdr.quantize_rows_i8(rand(10, 96, seed=3).cuda())
+    y = gdr.matmul_i8(q, scale, wq, ws, out_dtype=F32)
+    two = gdr.matmul_i8(q, scale, wq, ws, out_dtype=F32, out=(3, 7))
+    assert y.shape == (10,) and torch.equal(torch.cat(two), y)
+    assert torch.equal(gdr.matmul_i8(q[None], scale[None], wq, ws, out_dtype=F32)[0], y)
+    o, z = rand(3, 32, seed=4), rand(3, 32, seed=5)
+    g, gs = gdr.gated_rmsnorm_i8(o.cuda(), z.cuda(), torch.ones(32, device="cuda"))
+    assert g.shape == (96,) and gs.shape == ()
+    g2, gs2 = gdr.gated_rmsnorm_i8(o[None].cuda(), z[None].cuda(), torch.ones(32, device="cuda"))
+    assert torch.equal(g, g2[0]) and torch.equal(gs, gs2[0])
+
+
+@pytest.mark.parametrize("N,K", [(32776, 32), (32776, 1000)])
+def test_outputs_past_four_gigabytes(N, K):
+    M = 66000
+    a, w = torch.randint(-128, 128, (M, K), device="cuda", dtype=torch.int8), codes(N, K, seed=2)
+    sa, sw = torch.rand(M, device="cuda") + 0.1, rand(N, seed=3).abs()
+    note(f"outputs past 4 GiB, K={K}")
+    y = gdr.matmul_i8(a, sa, w.cuda(), sw.cuda())
+    for at in (0, 32768, 65533, M - 70):
+        rows = slice(at, min(at + 70, M))
+        size, ref = product_reference(a[rows].cpu(), sa[rows].cpu(), w, sw, None)
+        tol = 3 * U * size + U * (ref.abs() + 4 * U * size)
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+        assert bool(((y[rows].cpu().double() - ref).abs() <= tol).all())
+
+
+def test_norm_rows_past_four_gigabytes():
+    M, D = 560000, 4096
+    x = torch.randn(M, D, device="cuda", dtype=BF)
+    note("norm of rows past 4 GiB")
+    w = rand(D, dtype=BF, seed=1)
+    q, scale, s = gdr.add_rmsnorm_i8(x, w.cuda(), residual=x)
+    g, gs = gdr.gated_rmsnorm_i8(x.view(M, 32, 128), x.view(M, 32, 128), torch.ones(128, device="cuda"))
+    for at in (0, 262144, 524288, M - 9):
+        rows = slice(at, at + 9)
+        s_ref, q_ref, _ = norm_reference(x[rows].cpu(), w, x[rows].cpu(), 1e-6)
+        assert torch.equal(s[rows].cpu(), s_ref) and torch.equal(q[rows].cpu().double(), q_ref)
+        g2, gs2 = gdr.gated_rmsnorm_i8(x[rows].view(9, 32, 128), x[rows].view(9, 32, 128), torch.ones(128, device="cuda"))
+        assert torch.equal(g[rows], g2) and torch.equal(gs[rows], gs2)
+
+
 def test_no_rows():
     q, s, out = gdr.add_rmsnorm_i8(torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda"), torch.empty(0, 64, device="cuda"))
     assert q.shape == (0, 64) and s.shape == (0,) and out.shape == (0, 64)
@@ -271,6 +318,38 @@ def test_product_columns(N):
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_product_larger(M, N, K, dtype):
     check_product(M, N, K, dtype=dtype, bias=dtype == F32, seed=M)
+
+
+# Sizes that each form of the product takes, with operands that can and cannot be copied straight
+# to LDS (K a multiple of 16 or not), whole and partial reductions, and rows and columns that end
+# inside a tile.
+FORMS = {
+    "16x16": [(3, 4100, 4096), (50, 250, 1044), (45, 300, 1001)],
+    "32x64": [(33, 2048, 2048), (17, 9000, 1040), (250, 700, 999)],
+    "128x64": [(640, 1024, 1024), (650, 1000, 784), (600, 1003, 1001)],
+    "128x128, four stages": [(2048, 2048, 512), (1025, 2050, 528), (1500, 2050, 903)],
+    "128x128": [(1024, 8192, 1024), (1000, 8190, 1040), (2100, 4097, 1001)],
+    "256x256": [(4096, 4096, 1024), (4096, 4000, 1568), (4096, 4001, 1553)],
+    "256x256 and a launch for the last rows": [(4101, 4000, 1536), (4097, 12288, 2064)],
+}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_product_forms(form, dtype):
+    for M, N, K in FORMS[form]:
+        a, w = codes(M, K, seed=1).cuda(), codes(N, K, seed=2).cuda()
+        sa, sw = rand(M, seed=3).abs().cuda() + 0.1, rand(N, seed=4).abs().cuda() * K ** -0.5
+        b = rand(N, seed=5).cuda() if dtype == F32 else None
+        size, ref = product_reference(a, sa, w, sw, b)   # on the GPU, in fp64
+        room = torch.full((M + 2, N), 7.0, dtype=dtype, device="cuda")
+        note(f"{form}: M={M} N={N} K={K} {dtype}")
+        gdr.matmul_i8(a, sa, w, sw, bias=b, out=room[1:M + 1])
+        tol = 3 * U * size + U * (ref.abs() + 4 * U * size)
+        if dtype == BF:
+            tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+        assert bool(((room[1:M + 1].double() - ref).abs() <= tol).all()), (M, N, K)
+        assert bool((room[0] == 7.0).all()) and bool((room[M + 1] == 7.0).all())
 
 
 @pytest.mark.parametrize("out", [(100, 156), (4, 8, 244), (1, 255), (3, 5, 7, 11, 13, 17, 19, 181), (128, 128), (64, 60, 132)])
