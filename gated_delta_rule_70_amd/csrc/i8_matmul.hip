@@ -10,6 +10,7 @@
 // 2460 TOP/s (the library's int8 product reaches 2070 on 8192^3).
 #include "i8_launch.h"
 
+#include <algorithm>
 #include <type_traits>
 
 #include "gdr_device.h"
@@ -693,8 +694,8 @@ bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
            (rows == 1 || (stride % 16 == 0 && stride <= (INT32_MAX - K) / 255));
 }
 
-// Form of a product and its expected time.  Up to 2048 tiles' worth of work the time is the number
-// of rounds over the 256 CUs times what a tile takes: a fixed part (filling the pipeline, storing)
+// Form of a product and its expected time: the number of rounds over the 256 CUs (whole ones up to
+// 1024 tiles, where they stay in step) times what a tile takes: a fixed part (filling the pipeline, storing)
 // and a part for each reduction byte, by how fast a CU brings BM + BN rows in (50 to 70 bytes a
 // ns) or, for 256 x 256, multiplies them.  Constants fitted to measurements, M x N x K in us:
 //                        32x64  128x64  128x128 (4 / 2 stages)  256x256
@@ -705,6 +706,8 @@ bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
 //     512 x 12288 x 4096  62.1    35.6     36.9 /  32.1           50.0
 //    2048 x  4096 x 4096  97.2    46.6     41.2 /  35.8           50.5
 //    4096 x  4096 x 1024  71.9    32.5     29.8 /  25.2           23.6
+//    8192 x  8192 x  512         107.7    114.8 /  85.5           77.1
+//    3000 x  4096 x 4096          68.4     57.6 /  59.9           50.3
 //    8192 x  2048 x 8192   335     192      158 /   142            118
 // (64 x 32 tiles take what 32 x 64 take.)
 // The form without tiles is faster where 16 x 16 outputs do not make more than one workgroup for
@@ -731,7 +734,9 @@ Plan plan(int64_t M, int64_t N, int K) {
     offer(Form::t128x64, 128, 64, 1, any, 1.0, 2.8);
     offer(Form::t128x128_deep, 128, 128, 1, 256, 1.8, 4.2);
     offer(Form::t128x128, 128, 128, 257, any, 1.8, 3.6);
-    offer(Form::t256x256, 256, 256, 1, any, 9.0, 12.0);
+    // up to one tile for each CU, a tile takes longer the more of them draw on memory and power
+    const double fill = std::min(1.0, ((M + 255) / 256) * ((N + 255) / 256) / 256.0);
+    offer(Form::t256x256, 256, 256, 1, any, 8.0, 8.0 + 3.5 * fill * fill);
     return best;
 }
 
