@@ -142,13 +142,9 @@ int gdr_matmul_i8(const gdr_matmul_i8_dims* dims, const int8_t* a, const float* 
     gdr::MatmulArgs g{};
     int64_t N = 0;
     g.out.n = d.n_out;
-    g.out.quad = g.out.wide = 1;
-    const int64_t per = 16 / eo;
     for (int i = 0; i < d.n_out; ++i) {
         if (d.out_cols[i] < 1 || (d.M > 1 && d.out_stride[i] < d.out_cols[i])) return GDR_ERR_SHAPE;
         g.out.begin[i] = (int)N;
-        if (N % 4 != 0 || (d.M > 1 && d.out_stride[i] % 4 != 0)) g.out.quad = 0;
-        if (d.out_cols[i] % per != 0 || (d.M > 1 && d.out_stride[i] % per != 0)) g.out.wide = 0;
         N += d.out_cols[i];
         if (N > (1 << 30)) return GDR_ERR_SHAPE;
     }
@@ -167,8 +163,6 @@ int gdr_matmul_i8(const gdr_matmul_i8_dims* dims, const int8_t* a, const float* 
         return GDR_ERR_SHAPE;
     for (int i = 0; i < d.n_out; ++i) {
         if (!aligned(outs[i], eo)) return GDR_ERR_ALIGN;
-        if (!aligned(outs[i], 4 * eo)) g.out.quad = 0;
-        if (!aligned(outs[i], 16)) g.out.wide = 0;
         if (!range_of(outs[i], d.M, d.out_cols[i], d.out_stride[i], eo, &out[i])) return GDR_ERR_SHAPE;
         for (const Range& r : in)
             if (overlap(out[i], r)) return GDR_ERR_ALIAS;

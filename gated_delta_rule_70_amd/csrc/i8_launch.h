@@ -26,8 +26,6 @@ struct MatmulOut {
     int begin[GDR_MATMUL_I8_MAX_OUT + 1];  // first column of each; begin[n] = N
     void* ptr[GDR_MATMUL_I8_MAX_OUT];
     int64_t stride[GDR_MATMUL_I8_MAX_OUT];
-    int quad;  // every group of 4 columns 4i .. 4i+3 lies in one output, at an address that takes one store
-    int wide;  // the same for groups of 16 bytes
 };
 
 struct MatmulArgs {

@@ -11,6 +11,7 @@
 #include "i8_launch.h"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "gdr_device.h"
@@ -97,20 +98,20 @@ __device__ __forceinline__ void load_cut(const int8_t* const (&p)[N], const int 
     }
 }
 
-// Where the outputs of columns n .. n+3 go: for each column its output's first value of row 0
-// and the distance between rows.  Columns of one output share both.
+// Where column n goes.
 struct Where {
-    char* p;  // address of column n in row 0
+    char* p;  // its address in row 0
     int64_t stride;
+    int left;  // columns of the same output from n on
 };
 __device__ __forceinline__ Where where(const MatmulOut& o, int n, int elt) {
     char* p = static_cast<char*>(o.ptr[0]);
     int64_t stride = o.stride[0];
-    int begin = 0;
+    int begin = 0, end = o.begin[1];
 #pragma unroll
     for (int i = 1; i < GDR_MATMUL_I8_MAX_OUT; ++i)
-        if (i < o.n && n >= o.begin[i]) p = static_cast<char*>(o.ptr[i]), stride = o.stride[i], begin = o.begin[i];
-    return Where{p + (int64_t)(n - begin) * elt, stride};
+        if (i < o.n && n >= o.begin[i]) p = static_cast<char*>(o.ptr[i]), stride = o.stride[i], begin = o.begin[i], end = o.begin[i + 1];
+    return Where{p + (int64_t)(n - begin) * elt, stride, end - n};
 }
 
 template <bool BF16>
@@ -119,6 +120,14 @@ __device__ __forceinline__ void store_value(char* p, float x) {
         *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(x);
     else
         *reinterpret_cast<float*>(p) = x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_bits(char* p, const char* from) {
+    if constexpr (BF16)
+        *reinterpret_cast<uint16_t*>(p) = *reinterpret_cast<const uint16_t*>(from);
+    else
+        *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(from);
 }
 
 // Columns n .. n+3 of output row m from their sums.
@@ -133,13 +142,15 @@ __device__ __forceinline__ void store_quad(const MatmulArgs& g, int m, int n, i3
         const int c = min(n + j, g.N - 1);
         v[j] = (float)acc[j] * sa * g.w_scale[c] + (g.bias ? g.bias[c] : 0.f);
     }
-    if (g.out.quad && n + 4 <= g.N) {
-        const Where to = where(g.out, n, E);
+    const Where to = where(g.out, n, E);
+    if (to.left >= 4) {  // one store, at any alignment
         char* p = to.p + m * to.stride * E;
-        if constexpr (BF16)
-            *reinterpret_cast<u32x2*>(p) = bf16x4_bits(f32x4{v[0], v[1], v[2], v[3]});
-        else
-            *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+        if constexpr (BF16) {
+            const u32x2 b = bf16x4_bits(f32x4{v[0], v[1], v[2], v[3]});
+            __builtin_memcpy(p, &b, 8);
+        } else {
+            __builtin_memcpy(p, v, 16);
+        }
         return;
     }
 #pragma unroll
@@ -227,9 +238,11 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
 // One workgroup of WM x WN waves makes BM x BN outputs, 128 reduction bytes at a time through
 // STAGES buffers in LDS.  A row's 128 bytes are 8 chunks of 16; chunk c of row r sits at place
 // c ^ (r % 8), which spreads the 16 rows that a fragment reads over all banks.
-//   DMA   memory to LDS without registers (16 bytes a lane): pointers and row strides are
-//         multiples of 16 and a tile's rows lie within 2^31 bytes;
-//   else  through registers, at any alignment, a stage ahead.
+// Operands go from memory to LDS without registers, 16 bytes a lane; a tile's rows lie within 2^31
+// bytes.  Copies need addresses that are multiples of 4.  Where rows begin elsewhere (SHIFT) each is
+// copied from the aligned word that its first byte lies in, with one more word behind each stage's
+// 128 bytes, and a fragment is moved into place, by 0 to 3 bytes, as it is read from LDS.  Words
+// are read whole: the first and the last may begin before the operand or end behind it.
 // What bounds the 256 x 256 form: at 8192^3 the matrix cores are busy 74 % of the time at a clock of
 // 1.83 GHz; an order of issue with 68 % busy ran at 1.94 GHz and took the same time, so it is the
 // power that a product costs.  Tried and dropped (8192^3, 430 us): 32x32x32 products, 457;
@@ -247,23 +260,47 @@ __device__ __forceinline__ void wait_vmcnt() {
     asm volatile("" ::: "memory");
 }
 
-// 16 bytes a lane from r at voff + soff to LDS at `to` + 16 * lane, without registers.
+// 16 bytes a lane from r at voff + soff to LDS at `to` + 16 * lane, without registers; one word the
+// same way.
 typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ void copy_to_lds(rsrc_t r, i32x4* to, int voff, int soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ void copy_word_to_lds(rsrc_t r, int* to, int voff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, voff, 0, 0, 0);
 }
 
 // The same from an address of each lane's own.
 __device__ __forceinline__ void copy_to_lds(const int8_t* from, i32x4* to) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void*)to, 16, 0, 0);
 }
+__device__ __forceinline__ void copy_word_to_lds(const int8_t* from, int* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void*)to, 4, 0, 0);
+}
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool DMA, bool BF16>
+// Bytes by .. by + 15 of v and the word behind it.
+__device__ __forceinline__ i32x4 moved(i32x4 v, int next, uint32_t by) {
+    const uint32_t d[5] = {(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3], (uint32_t)next};
+    i32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = (int)__builtin_amdgcn_alignbyte(d[j + 1], d[j], by);
+    return r;
+}
+__device__ __forceinline__ const int8_t* word_of(const int8_t* p) { return p - (reinterpret_cast<uintptr_t>(p) & 3u); }
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool SHIFT, bool BF16>
 __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) {
     constexpr int NT = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int LA = BM * 8 / NT, LW = BN * 8 / NT;
     static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && TM >= 1 && TN >= 1);
-    __shared__ __align__(1024) i32x4 lds[STAGES][(BM + BN) * 8];
+    constexpr int ROWS = BM + BN;
+    // Stages and, with SHIFT, the word behind each row's 128 bytes.  One array: with several the
+    // compiler takes every copy under way to be waited for before any of them is read.
+    __shared__ __align__(1024) i32x4 room[STAGES * ROWS * 8 + (SHIFT ? STAGES * ROWS / 4 : 0)];
+    i32x4(*const lds)[ROWS * 8] = reinterpret_cast<i32x4(*)[ROWS * 8]>(room);
+    int* const words = reinterpret_cast<int*>(room);
+    constexpr int BEHIND = STAGES * ROWS * 32;  // words before the words behind
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -283,41 +320,49 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
     static_assert(NT % 64 == 0);
 
     const int full = g.K / kBK;
+    // Offsets of this thread's chunks from the first byte of the tile's first row or, with SHIFT,
+    // from the word that it lies in.
+    const int lead_a = SHIFT ? (int)(reinterpret_cast<uintptr_t>(ga) & 3u) : 0;
+    const int lead_w = SHIFT ? (int)(reinterpret_cast<uintptr_t>(gw) & 3u) : 0;
+    const int bytes_a = lead_a + last_m * (int)g.a_stride + g.K, bytes_w = lead_w + last_n * (int)g.w_stride + g.K;
+    const rsrc_t ra = make_rsrc(ga - lead_a, SHIFT ? (uint32_t)(bytes_a + 3) & ~3u : (uint32_t)bytes_a);
+    const rsrc_t rw = make_rsrc(gw - lead_w, SHIFT ? (uint32_t)(bytes_w + 3) & ~3u : (uint32_t)bytes_w);
+    auto start_a = [&](int r) {
+        const int at = min(r, last_m) * (int)g.a_stride + lead_a;
+        return SHIFT ? at & ~3 : at;
+    };
+    auto start_w = [&](int r) {
+        const int at = min(r, last_n) * (int)g.w_stride + lead_w;
+        return SHIFT ? at & ~3 : at;
+    };
     int va[LA], vw[LW];
-    rsrc_t ra, rw;
-    if constexpr (DMA) {
-        ra = make_rsrc(ga, (uint32_t)(last_m * g.a_stride + g.K));
-        rw = make_rsrc(gw, (uint32_t)(last_n * g.w_stride + g.K));
 #pragma unroll
-        for (int i = 0; i < LA; ++i) va[i] = min(row + i * (NT / 8), last_m) * (int)g.a_stride + chunk * 16;
+    for (int i = 0; i < LA; ++i) va[i] = start_a(row + i * (NT / 8)) + chunk * 16;
 #pragma unroll
-        for (int i = 0; i < LW; ++i) vw[i] = min(row + i * (NT / 8), last_n) * (int)g.w_stride + chunk * 16;
-    }
+    for (int i = 0; i < LW; ++i) vw[i] = start_w(row + i * (NT / 8)) + chunk * 16;
+    // Each wave copies the words behind 64 rows.  A word past the operand's last one would belong
+    // to a row that begins at a whole word, which needs none: the last one is read in its place.
+    static_assert(!SHIFT || (BM % 64 == 0 && BN % 64 == 0 && ROWS / 64 <= WM * WN));
+    const int group = wave % (ROWS / 64) * 64;
+    const bool group_a = group < BM;
+    const int vb = group_a ? start_a(group + lane) : start_w(group - BM + lane);
+    const int last_word = ((group_a ? bytes_a : bytes_w) - 1) & ~3;
+    constexpr int L = LA + LW + (SHIFT ? 1 : 0);  // copies of a stage
     const Extent ea = extent_of(g.a, g.M, g.a_stride, g.K), ew = extent_of(g.w, g.N, g.w_stride, g.K);
-    i32x4 hold[DMA ? 1 : LA + LW];
     auto fetch = [&](int s) {
         const int k = s * kBK;
-        if constexpr (DMA) {
-            i32x4* to = &lds[s % STAGES][wave * 64];
+        i32x4* to = &lds[s % STAGES][wave * 64];
 #pragma unroll
-            for (int i = 0; i < LA; ++i) copy_to_lds(ra, to + i * NT, va[i], k);
+        for (int i = 0; i < LA; ++i) copy_to_lds(ra, to + i * NT, va[i], k);
 #pragma unroll
-            for (int i = 0; i < LW; ++i) copy_to_lds(rw, to + BM * 8 + i * NT, vw[i], k);
-        } else {
-#pragma unroll
-            for (int i = 0; i < LA; ++i)
-                __builtin_memcpy(&hold[i], ga + min(row + i * (NT / 8), last_m) * g.a_stride + (k + chunk * 16), 16);
-#pragma unroll
-            for (int i = 0; i < LW; ++i)
-                __builtin_memcpy(&hold[LA + i], gw + min(row + i * (NT / 8), last_n) * g.w_stride + (k + chunk * 16), 16);
-        }
-    };
-    auto put = [&](int s) {
-        if constexpr (!DMA) {
-#pragma unroll
-            for (int i = 0; i < LA; ++i) lds[s % STAGES][i * NT + tid] = hold[i];
-#pragma unroll
-            for (int i = 0; i < LW; ++i) lds[s % STAGES][BM * 8 + i * NT + tid] = hold[LA + i];
+        for (int i = 0; i < LW; ++i) copy_to_lds(rw, to + BM * 8 + i * NT, vw[i], k);
+        if constexpr (SHIFT) {
+            int* word = &words[BEHIND + s % STAGES * ROWS + group];
+            const int v = min(vb + k + kBK, last_word);
+            if (group_a)
+                copy_word_to_lds(ra, word, v);
+            else
+                copy_word_to_lds(rw, word, v);
         }
     };
 
@@ -337,6 +382,33 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
 #pragma unroll
         for (int i = 0; i < TM; ++i) f.a[i] = A[i * 128 + (place ^ (h * 4))];
     };
+    // The same, moved into place.  Rows 16 apart begin alike in a word (those past the end may not;
+    // their results are dropped).  Behind chunk 7 is the word from `behind`.
+    const int quarter = lane >> 4;
+    const uint32_t by_a = ((uint32_t)lead_a + (uint32_t)(wm * TM * 16 + (lane & 15)) * (uint32_t)g.a_stride) & 3u;
+    const uint32_t by_w = ((uint32_t)lead_w + (uint32_t)(wn * TN * 16 + (lane & 15)) * (uint32_t)g.w_stride) & 3u;
+    const bool past = quarter == 3;  // in a stage's second half
+    const int next0 = (lane & 15) * 32 + ((quarter + 1) ^ (lane & 7)) * 4;
+    const int next1 = past ? BEHIND + wm * (TM * 16) + (lane & 15) : wm * (TM * 512) + (lane & 15) * 32 + ((quarter + 5) ^ (lane & 7)) * 4;
+    const int next2 = past ? BEHIND + BM + wn * (TN * 16) + (lane & 15)
+                           : BM * 32 + wn * (TN * 512) + (lane & 15) * 32 + ((quarter + 5) ^ (lane & 7)) * 4;
+    const int apart1 = past ? 16 : 512, stage1 = past ? ROWS : ROWS * 32;
+    auto read_moved = [&](int s, int h, Frags& f) {
+        const int b = s % STAGES;
+        read(s, h, f);
+        const int* A = words + (h ? next1 + b * stage1 : b * (ROWS * 32) + wm * (TM * 512) + next0);
+        const int* W = words + (h ? next2 + b * stage1 : b * (ROWS * 32) + BM * 32 + wn * (TN * 512) + next0);
+        const int apart = h ? apart1 : 512;
+        int na[TM], nw[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) nw[j] = W[j * apart];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) na[i] = A[i * apart];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) f.w[j] = moved(f.w[j], nw[j], by_w);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) f.a[i] = moved(f.a[i], na[i], by_a);
+    };
     auto multiply = [&](const Frags& f) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -352,14 +424,22 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
         }
     };
 
-    if constexpr (DMA) {
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s)
+        if (s < full) fetch(s);
+    if (full >= STAGES)
+        wait_vmcnt<(STAGES - 1) * L>();
+    else
+        wait_vmcnt<0>();
+    lds_barrier();
+    if constexpr (!SHIFT) {
         // Two sets of fragments: while one half of a stage is multiplied the next half is read
         // from LDS, also across stages: the barrier that frees stage s (everyone has read it) and
         // opens stage s + 1 stands between the halves of stage s.  The order is written out, a
         // row of products at a time: LDS reads go with the first rows (two each, so that the last
         // are back before the next half needs them), copies to LDS one or two with each row, since
         // a run of copies holds a wave up while the address unit takes 64 lanes' worth each.
-        constexpr int L = LA + LW, RD = TM + TN, PR = (RD + TM - 1) / TM + 1, PL = (L + TM - 1) / TM;
+        constexpr int RD = TM + TN, PR = (RD + TM - 1) / TM + 1, PL = (L + TM - 1) / TM;
         Frags f0, f1;
         auto half = [&](const Frags& use, Frags& next, int rs, int rh, auto reads, int fs, auto copies) {
 #pragma unroll
@@ -401,14 +481,6 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
         };
         using yes = std::true_type;
         using no = std::false_type;
-#pragma unroll
-        for (int s = 0; s < STAGES; ++s)
-            if (s < full) fetch(s);
-        if (full >= STAGES)
-            wait_vmcnt<(STAGES - 1) * L>();
-        else
-            wait_vmcnt<0>();
-        lds_barrier();
         if (full > 0) {
             read(0, 0, f0);
             int s = 0;
@@ -417,15 +489,22 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
             step(s, no{}, no{});
         }
     } else {
-        if (full > 0) {
-            fetch(0);
-            put(0);
-        }
+        // One set: the barrier that frees stage s and opens the next stands where all of its
+        // fragments have been read and half of them are multiplied.
         for (int s = 0; s < full; ++s) {
-            lds_barrier();
-            if (s + 1 < full) fetch(s + 1);
-            compute(s);
-            if (s + 1 < full) put(s + 1);
+            Frags f;
+            read_moved(s, 0, f);
+            multiply(f);
+            read_moved(s, 1, f);
+            if (s + 1 < full) {
+                if (s + STAGES - 1 < full)
+                    wait_vmcnt<(STAGES - 2) * L>();
+                else
+                    wait_vmcnt<0>();
+                lds_barrier();
+                if (s + STAGES < full) fetch(s + STAGES);
+            }
+            multiply(f);
         }
     }
     if (g.K % kBK != 0) {
@@ -469,12 +548,15 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
             sw[j][c] = g.w_scale[n];
             bias[j][c] = g.bias ? g.bias[n] : 0.f;
         }
-    const bool wide = g.out.wide;
-    const int col = wide ? lane % CH * PER : lane % CW;          // of this lane's stores
-    const int first = wide ? lane / CH : lane / CW;              // and its first row
-    const int step_r = wide ? 64 / CH : 64 / CW;
+    const int col = lane % CH * PER, first = lane / CH;  // 16 bytes of columns and the first row of this lane's stores
+    constexpr int step_r = 64 / CH;
     const bool on = nw + col < g.N;
+    // they go to one output or two; columns from `both` on, of a third one and more, one by one
     const Where to = where(g.out, min(nw + col, g.N - 1), E);
+    const int own = min(to.left, PER), all = min(PER, g.N - nw - col);
+    Where then = to;
+    if (own < all) then = where(g.out, nw + col + own, E);
+    const int both = min(own + then.left, all);
     char* mine = reinterpret_cast<char*>(&lds[0][0]) + wave * SPACE;
     lds_barrier();
 #pragma unroll
@@ -503,18 +585,21 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
         char* p = to.p + (int64_t)(mw + pass * RP + first) * to.stride * E;
         for (int r = first; r < rows; r += step_r, p += step_r * to.stride * E) {
             const char* at = mine + r * EB + (col / PER ^ (r & (CH - 1))) * 16;
-            if (wide) {
+            if (to.left >= PER) {  // one store, at any alignment
                 u32x4 x;
                 __builtin_memcpy(&x, __builtin_assume_aligned(at, 16), 16);
-                *reinterpret_cast<u32x4*>(p) = x;
-            } else if constexpr (BF16) {
-                uint16_t x;
-                __builtin_memcpy(&x, __builtin_assume_aligned(at + col % PER * E, 2), 2);
-                *reinterpret_cast<uint16_t*>(p) = x;
+                __builtin_memcpy(p, &x, 16);
             } else {
-                float x;
-                __builtin_memcpy(&x, __builtin_assume_aligned(at + col % PER * E, 4), 4);
-                *reinterpret_cast<float*>(p) = x;
+                const int64_t m = mw + pass * RP + r;
+                char* p2 = then.p + m * then.stride * E;
+#pragma unroll
+                for (int c = 0; c < PER; ++c)
+                    if (c < both) store_bits<BF16>(c < own ? p + c * E : p2 + (c - own) * E, at + c * E);
+#pragma unroll 1
+                for (int c = both; c < all; ++c) {
+                    const Where one = where(g.out, nw + col + c, E);
+                    store_bits<BF16>(one.p + m * one.stride * E, at + c * E);
+                }
             }
         }
     }
@@ -525,15 +610,19 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
 // workgroup; each wave makes a 32 x 32 block, and KG groups of waves share the reduction: a stage
 // is KG * 64 bytes of it, group k takes the k-th 64, and the groups' sums meet in LDS.  What bounds
 // these products is how fast a CU can bring its operands in, so the loop keeps STAGES - 1 stages
-// in flight (DMA), or REGS stages in registers (any alignment).  32 x 12288 x 4096: 10.7 us, 4.8
+// in flight.  32 x 12288 x 4096: 10.7 us, 4.8
 // TB/s; 128 x 4096 x 4096: 9.7 us, where each CU brings 393 KB in at 50 bytes a ns.
-template <int BM, int BN, int KG, int STAGES, int REGS, bool DMA, bool BF16>
+template <int BM, int BN, int KG, int STAGES, bool SHIFT, bool BF16>
 __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_kernel(MatmulArgs g) {
     constexpr int WN = BN / 32, WAVES = BM / 32 * WN * KG, NT = WAVES * 64;
     constexpr int BK = KG * 64, CPR = BK / 16, ROWS = BM + BN, LD = ROWS * CPR / NT;
     static_assert(KG >= 2 && ROWS * CPR % NT == 0 && NT % CPR == 0);
-    constexpr int BUFS = DMA ? STAGES : 2, RED = KG * BM * BN / 4;  // 16-byte places
-    __shared__ __align__(1024) i32x4 lds[BUFS * ROWS * CPR > RED ? BUFS * ROWS * CPR : RED];
+    constexpr int RED = KG * BM * BN / 4;  // 16-byte places
+    constexpr int GROUPS = (ROWS + 63) / 64, L = LD + (SHIFT ? 1 : 0);
+    constexpr int STAGED = STAGES * ROWS * CPR + (SHIFT ? STAGES * GROUPS * 16 : 0);
+    __shared__ __align__(1024) i32x4 lds[STAGED > RED ? STAGED : RED];
+    int* const words = reinterpret_cast<int*>(lds);
+    constexpr int BEHIND = STAGES * ROWS * CPR * 4;  // the words behind each row's BK bytes
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // an XCD's tiles share columns of w, the larger operand in these products
@@ -556,7 +645,13 @@ __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_ke
     };
     const int8_t* src[LD];
 #pragma unroll
-    for (int i = 0; i < LD; ++i) src[i] = source(i) + chunk * 16;
+    for (int i = 0; i < LD; ++i) src[i] = (SHIFT ? word_of(source(i)) : source(i)) + chunk * 16;
+    // each wave copies the words behind 64 rows (as in the tile kernel)
+    static_assert(GROUPS <= WAVES);
+    const int group = wave % GROUPS * 64, brow = min(group + lane, ROWS - 1);
+    const bool in_a = brow < BM;
+    const int8_t* bsrc = word_of(in_a ? ga + min(brow, last_m) * g.a_stride : gw + min(brow - BM, last_n) * g.w_stride);
+    const int8_t* blast = word_of(in_a ? ga + last_m * g.a_stride + g.K - 1 : gw + last_n * g.w_stride + g.K - 1);
 
     i32x4 rest[LD];  // the last partial stage
     const bool partial = g.K % BK != 0;
@@ -571,68 +666,58 @@ __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_ke
     i32x4 acc[2][2] = {};
     const int kg = wave % KG, block = wave / KG, wm = block / WN, wn = block % WN;
     const int place = (lane & 15) * CPR + ((kg * 4 + (lane >> 4)) ^ (lane & 7));
-    auto compute = [&](int buf) {
+    const int quarter = kg * 4 + (lane >> 4);  // this lane's chunk
+    const uint32_t by_a = (uint32_t)(reinterpret_cast<uintptr_t>(ga) + (wm * 32 + (lane & 15)) * g.a_stride) & 3u;
+    const uint32_t by_w = (uint32_t)(reinterpret_cast<uintptr_t>(gw) + (wn * 32 + (lane & 15)) * g.w_stride) & 3u;
+    auto compute = [&](int buf, auto move) {
         const i32x4* A = &lds[buf * ROWS * CPR + wm * 32 * CPR];
         const i32x4* W = &lds[buf * ROWS * CPR + (BM + wn * 32) * CPR];
         i32x4 fa[2], fw[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) fw[i] = W[i * 16 * CPR + place], fa[i] = A[i * 16 * CPR + place];
+        if constexpr (decltype(move)::value) {
+            const bool past = quarter == CPR - 1;
+            const int next = (buf * ROWS * CPR + (lane & 15) * CPR + ((quarter + 1) ^ (lane & 7))) * 4;
+            const int behind = BEHIND + buf * GROUPS * 64 + (lane & 15), apart = past ? 16 : 16 * CPR * 4;
+            const int* nA = words + (past ? behind + wm * 32 : next + wm * 32 * CPR * 4);
+            const int* nW = words + (past ? behind + BM + wn * 32 : next + (BM + wn * 32) * CPR * 4);
+            const int n[4] = {nA[0], nA[apart], nW[0], nW[apart]};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fa[i] = moved(fa[i], n[i], by_a), fw[i] = moved(fw[i], n[2 + i], by_w);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8(fw[j], fa[i], acc[i][j]);
     };
-    if constexpr (DMA) {
-        auto fetch = [&](int s, int buf) {
+    auto fetch = [&](int s, int buf) {
 #pragma unroll
-            for (int i = 0; i < LD; ++i)
-                copy_to_lds(src[i] + s * BK, &lds[buf * ROWS * CPR + i * NT + wave * 64]);
-        };
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
-            if (s < full) fetch(s, s);
-        int buf = 0;
-        for (int s = 0; s < full; ++s) {
-            if (s + STAGES - 2 < full)
-                wait_vmcnt<(STAGES - 2) * LD>();
-            else
-                wait_vmcnt<0>();
-            lds_barrier();
-            if (s + STAGES - 1 < full) fetch(s + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
-            compute(buf);
-            buf = buf + 1 == STAGES ? 0 : buf + 1;
+        for (int i = 0; i < LD; ++i) copy_to_lds(src[i] + s * BK, &lds[buf * ROWS * CPR + i * NT + wave * 64]);
+        if constexpr (SHIFT) {
+            const int8_t* from = bsrc + (s + 1) * BK;
+            copy_word_to_lds(from < blast ? from : blast, &words[BEHIND + buf * GROUPS * 64 + group]);
         }
-    } else {
-        i32x4 hold[REGS][LD];
-        auto load = [&](int s, i32x4(&h)[LD]) {
+    };
 #pragma unroll
-            for (int i = 0; i < LD; ++i) __builtin_memcpy(&h[i], src[i] + s * BK, 16);
-        };
-        auto put = [&](const i32x4(&h)[LD], int buf) {
-#pragma unroll
-            for (int i = 0; i < LD; ++i) lds[buf * ROWS * CPR + i * NT + tid] = h[i];
-        };
-        static_assert(REGS % 2 == 0);
-#pragma unroll
-        for (int s = 0; s < REGS; ++s)
-            if (s < full) load(s, hold[s]);
-        if (full > 0) put(hold[0], 0);
-        for (int s = 0; s < full; s += REGS)
-#pragma unroll
-            for (int u = 0; u < REGS; ++u) {
-                if (s + u >= full) break;
-                lds_barrier();
-                if (s + u + REGS < full) load(s + u + REGS, hold[u]);
-                compute(u % 2);
-                if (s + u + 1 < full) put(hold[(u + 1) % REGS], (u + 1) % 2);
-            }
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < full) fetch(s, s);
+    int buf = 0;
+    for (int s = 0; s < full; ++s) {
+        if (s + STAGES - 2 < full)
+            wait_vmcnt<(STAGES - 2) * L>();
+        else
+            wait_vmcnt<0>();
+        lds_barrier();
+        if (s + STAGES - 1 < full) fetch(s + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+        compute(buf, std::integral_constant<bool, SHIFT>{});
+        buf = buf + 1 == STAGES ? 0 : buf + 1;
     }
     if (partial) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < LD; ++i) lds[i * NT + tid] = rest[i];
         __syncthreads();
-        compute(0);
+        compute(0, std::false_type{});
     }
 
     // Sums of the groups meet in LDS: BM x BN int32 each, a row's places of 4 columns exchanged by
@@ -665,121 +750,160 @@ void rows(const MatmulArgs& g) {
         hipLaunchKernelGGL((matmul_rows_kernel<ALIGN, false>), grid, dim3(512), 0, g.stream, g);
 }
 
-template <int BM, int BN, int KG, int STAGES, int REGS, bool DMA>
+template <int BM, int BN, int KG, int STAGES, bool SHIFT>
 void small(const MatmulArgs& g) {
     const dim3 grid((unsigned)(((int64_t)g.M + BM - 1) / BM * ((g.N + BN - 1) / BN)));
     constexpr int NT = BM / 32 * (BN / 32) * KG * 64;
     if (g.out_bf16)
-        hipLaunchKernelGGL((matmul_small_kernel<BM, BN, KG, STAGES, REGS, DMA, true>), grid, dim3(NT), 0, g.stream, g);
+        hipLaunchKernelGGL((matmul_small_kernel<BM, BN, KG, STAGES, SHIFT, true>), grid, dim3(NT), 0, g.stream, g);
     else
-        hipLaunchKernelGGL((matmul_small_kernel<BM, BN, KG, STAGES, REGS, DMA, false>), grid, dim3(NT), 0, g.stream, g);
+        hipLaunchKernelGGL((matmul_small_kernel<BM, BN, KG, STAGES, SHIFT, false>), grid, dim3(NT), 0, g.stream, g);
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool DMA>
+template <int BM, int BN, int WM, int WN, int STAGES, bool SHIFT>
 void tiles(const MatmulArgs& g) {
     const dim3 grid((unsigned)(((int64_t)g.M + BM - 1) / BM * ((g.N + BN - 1) / BN)));
     if (g.out_bf16)
-        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, true>), grid, dim3(WM * WN * 64), 0, g.stream, g);
+        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, SHIFT, true>), grid, dim3(WM * WN * 64), 0, g.stream, g);
     else
-        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, DMA, false>), grid, dim3(WM * WN * 64), 0, g.stream, g);
+        hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, SHIFT, false>), grid, dim3(WM * WN * 64), 0, g.stream, g);
 }
 
-bool words_ok(const MatmulArgs& g) {
-    return ((reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.w)) & 3u) == 0 &&
-           (g.M == 1 || g.a_stride % 4 == 0) && (g.N == 1 || g.w_stride % 4 == 0);
+// Where rows of a and w begin: all at whole lines of 128 bytes (0), at multiples of 16 (1), at
+// whole words (2), or anywhere (3).
+int places_of(const MatmulArgs& g) {
+    const uint64_t all = reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.w) |
+                         (g.M > 1 ? (uint64_t)g.a_stride : 0) | (g.N > 1 ? (uint64_t)g.w_stride : 0);
+    return all % 128 == 0 ? 0 : all % 16 == 0 ? 1 : all % 4 == 0 ? 2 : 3;
 }
 
-bool dma_ok(const int8_t* p, int64_t stride, int rows, int K) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 &&
-           (rows == 1 || (stride % 16 == 0 && stride <= (INT32_MAX - K) / 255));
-}
+// A tile's rows lie within 2^31 bytes.
+bool near(int64_t stride, int rows, int K) { return rows == 1 || stride <= (INT32_MAX - K - 8) / 255; }
 
-// Form of a product and its expected time: the number of rounds over the 256 CUs (whole ones up to
-// 1024 tiles, where they stay in step) times what a tile takes: a fixed part (filling the pipeline, storing)
-// and a part for each reduction byte, by how fast a CU brings BM + BN rows in (50 to 70 bytes a
-// ns) or, for 256 x 256, multiplies them.  Constants fitted to measurements, M x N x K in us:
-//                        32x64  128x64  128x128 (4 / 2 stages)  256x256
-//      32 x 12288 x 4096  11.9    14.5     17.3 /  22.5           42.2
-//     128 x  4096 x 4096   9.8    13.7     17.1 /  22.9           42.3
-//     512 x  4096 x 4096  24.0    16.1     19.2 /  24.1           44.5
-//    1024 x  4096 x 4096  48.5    24.6     21.1 /  26.2           46.1
-//     512 x 12288 x 4096  62.1    35.6     36.9 /  32.1           50.0
-//    2048 x  4096 x 4096  97.2    46.6     41.2 /  35.8           50.5
-//    4096 x  4096 x 1024  71.9    32.5     29.8 /  25.2           23.6
-//    8192 x  8192 x  512         107.7    114.8 /  85.5           77.1
-//    3000 x  4096 x 4096          68.4     57.6 /  59.9           50.3
-//    8192 x  2048 x 8192   335     192      158 /   142            118
-// (64 x 32 tiles take what 32 x 64 take.)
-// The form without tiles is faster where 16 x 16 outputs do not make more than one workgroup for
-// each CU (51 x 256 x 8100 8.6 against 17.3 us; at 64 x 2048 x 1024, twice that, 5.3 against 5.1)
-// and up to 16 rows and 8192 columns (1 x 4096 x 4096 6.5 against 8.8 us; 1 x 12288 x 4096 12.6
-// against 11.1).
-enum class Form { rows, t32x64, t128x64, t128x128_deep, t128x128, t256x256 };
+// Form of a product and its expected time, from how many tiles a CU of the 256 gets (past four of
+// them the CUs no longer keep step, and a fraction counts) and what a tile takes: a fixed part
+// (filling the pipeline, storing) and a part for each reduction byte.  Forms of which two
+// workgroups fit a CU overlap their fixed parts; the others slow down as more CUs draw on memory
+// and power.  Where rows do not begin at whole lines, the 128 bytes of a stage lie in two lines and
+// all forms but those that read 256 in a row take longer; fragments that have to be moved into
+// place cost more again.  The constants were fitted to 11000 random sizes (17 to 32768 rows, 128 to
+// 12288 columns, reductions of 256 to 8192); the form so chosen takes 0.6 % longer than the fastest
+// on average, 14 % at the 99th percentile.
+// M x N x K in us, rows beginning at whole lines:
+//                        32x64  128x64  128x128 (4 / 2 stages)  192x256  256x256
+//      32 x 12288 x 4096  14.2    18.6     20.0 /  30.9           40.8     47.3
+//     128 x  4096 x 4096   8.5    12.3     15.5 /  21.9           32.4     38.1
+//     512 x  4096 x 4096  22.6    13.7     16.2 /  22.4           33.2     39.6
+//    1024 x  4096 x 4096  47.0    23.0     20.0 /  25.1           34.4     40.2
+//     512 x 12288 x 4096  77.3    43.6     44.2 /  40.3           46.6     53.3
+//    2048 x  4096 x 4096  99.1    50.4     43.0 /  38.3           47.2     50.7
+//    4096 x  4096 x 1024  73.3    32.4          /  26.0           28.9     21.8
+//    8192 x  8192 x  512          99.8          /  77.9           64.0     68.6
+//    1691 x  5760 x 4096 108.6    61.7          /  63.3           47.0     51.7
+//    3000 x  4096 x 4096 133.3    69.6          /  61.3           50.5     56.0
+//    8192 x  2048 x 8192 334.1   185.9          / 137.1          148.3    111.0
+// The form without tiles is also taken up to 16 rows and 8192 columns (1 x 4096 x 4096 6.5 against
+// 8.8 us; 1 x 12288 x 4096 12.6 against 11.1).
+constexpr int64_t kMostTiles = (1 << 23) - 1;  // a launch has fewer than 2^32 threads, 512 for each tile
+enum class Form { rows, t32x64, t128x64, t128x128_deep, t128x128, t192x256, t256x256 };
 struct Plan {
     Form form;
     double us;
 };
-Plan plan(int64_t M, int64_t N, int K) {
-    if ((M <= 16 && N <= 8192) || (M + 15) / 16 * ((N + 15) / 16) <= 256) return Plan{Form::rows, 1.0 + 1.3e-3 * K};
-    Plan best{Form::t32x64, 1e30};
-    auto offer = [&](Form f, int bm, int bn, int64_t least, int64_t most, double fixed, double per_k) {
-        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
-        if (tiles < least || tiles > most) return;
-        const double rounds = tiles <= 1024 ? (double)((tiles + 255) / 256) : tiles / 256. + .5;
-        const double us = rounds * (fixed + per_k * K * 1e-3);
-        if (us < best.us) best = Plan{f, us};
-    };
-    constexpr int64_t any = (1 << 23) - 1;  // a launch has fewer than 2^32 threads, 512 for each tile
-    offer(Form::t32x64, 32, 64, 1, any, 0.8, 1.9);
-    offer(Form::t128x64, 128, 64, 1, any, 1.0, 2.8);
-    offer(Form::t128x128_deep, 128, 128, 1, 256, 1.8, 4.2);
-    offer(Form::t128x128, 128, 128, 257, any, 1.8, 3.6);
-    // up to one tile for each CU, a tile takes longer the more of them draw on memory and power
-    const double fill = std::min(1.0, ((M + 255) / 256) * ((N + 255) / 256) / 256.0);
-    offer(Form::t256x256, 256, 256, 1, any, 8.0, 8.0 + 3.5 * fill * fill);
+struct Cost {
+    int rows, cols, a_cu;     // of a tile; workgroups that fit a CU
+    double fixed, per_k;      // us for a tile, and for 1000 reduction bytes of it
+    double more;              // added to per_k: for a CU's first tile (two a CU), once every CU has one (one a CU)
+    double places[4];         // per_k for each of places_of(), in relation to the first
+};
+constexpr Cost kCosts[] = {{16, 16, 0, 1.05, 1.43, 0, {1, .65, .75, 1.27}},
+                           {32, 64, 2, 2.6, 1.25, 0, {1, 1.02, 1.11, 1.54}},
+                           {128, 64, 2, 2.7, 2.34, 0, {1, 1.51, 1.57, 2.50}},
+                           {128, 128, 1, 3.5, 2.5, .9, {1, 1.60, 1.72, 0}},  // four stages: not where fragments are moved
+                           {128, 128, 2, 4.4, 3.3, .5, {1, 1.41, 1.49, 2.05}},
+                           {192, 256, 1, 7.3, 7.3, 1.2, {1, 1.32, 1.37, 1.90}},
+                           {256, 256, 1, 9.9, 8.1, 1.6, {1, 1.38, 1.35, 1.95}}};
+Plan plan(int64_t M, int64_t N, int K, int places) {
+    Plan best{Form::rows, 1e30};
+    for (int f = 0; f < 7; ++f) {
+        const Cost& c = kCosts[f];
+        const int64_t tiles = ((M + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
+        if (tiles > kMostTiles || (f == (int)Form::t128x128_deep && (tiles > 256 || places == 3))) continue;
+        const double k = K * 1e-3 * c.places[places];
+        const double n = tiles <= 1024 ? (double)((tiles + 255) / 256) : tiles / 256. + .5;
+        const double fill = std::min(1.0, tiles / 256.0);
+        const double us = c.a_cu == 0   ? std::max(1.0, .5 + tiles / 512.) * (c.fixed + c.per_k * k)
+                          : c.a_cu == 2 ? c.fixed * std::ceil(n / 2) + k * (c.per_k * n + c.more)
+                                        : n * (c.fixed + k * (c.per_k + c.more * fill * fill));
+        if (2.0 + us < best.us) best = Plan{(Form)f, 2.0 + us};  // 2: a launch
+        if (f == 0 && M <= 16 && N <= 8192) break;
+    }
     return best;
 }
 
-template <bool DMA>
+template <bool SHIFT>
 void start(Form f, const MatmulArgs& g) {
     switch (f) {
-        case Form::rows: words_ok(g) ? g.K % 16 == 0 ? rows<16>(g) : rows<4>(g) : rows<1>(g); break;
-        case Form::t32x64: small<32, 64, 4, 3, 4, DMA>(g); break;
-        case Form::t128x64: tiles<128, 64, 4, 2, 3, DMA>(g); break;
-        case Form::t128x128_deep: tiles<128, 128, 2, 4, DMA ? 4 : 2, DMA>(g); break;
-        case Form::t128x128: tiles<128, 128, 2, 4, 2, DMA>(g); break;
-        case Form::t256x256: tiles<256, 256, 2, 4, 2, DMA>(g); break;
+        case Form::rows: SHIFT ? rows<1>(g) : g.K % 16 == 0 ? rows<16>(g) : rows<4>(g); break;
+        case Form::t32x64: small<32, 64, 4, 3, SHIFT>(g); break;
+        case Form::t128x64: tiles<128, 64, 4, 2, 3, SHIFT>(g); break;
+        case Form::t128x128_deep: tiles<128, 128, 2, 4, 4, false>(g); break;  // of whole words only
+        case Form::t128x128: tiles<128, 128, 2, 4, 2, SHIFT>(g); break;
+        case Form::t192x256: tiles<192, 256, 2, 4, 2, SHIFT>(g); break;
+        case Form::t256x256: tiles<256, 256, 2, 4, 2, SHIFT>(g); break;
     }
+}
+
+MatmulArgs rows_of(const MatmulArgs& g, int first, int count) {
+    MatmulArgs r = g;
+    r.M = count;
+    r.a += first * g.a_stride;
+    r.a_scale += first;
+    for (int i = 0; i < g.out.n; ++i)
+        r.out.ptr[i] = static_cast<char*>(g.out.ptr[i]) + first * g.out.stride[i] * (g.out_bf16 ? 2 : 4);
+    return r;
+}
+
+hipError_t launch(Form f, const MatmulArgs& g) {
+    places_of(g) < 3 ? start<false>(f, g) : start<true>(f, g);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_matmul_i8(const MatmulArgs& g) {
     if (g.M < 1 || g.M > GDR_I8_MAX_ROWS || g.N < 1 || g.K < 1 || g.K > GDR_MATMUL_I8_MAX_K) return hipErrorInvalidValue;
-    const bool dma = dma_ok(g.a, g.a_stride, g.M, g.K) && dma_ok(g.w, g.w_stride, g.N, g.K);
-    const Plan whole = plan(g.M, g.N, g.K);
-    // A few rows past a multiple of 256 can cost a round of tiles more: they go into a launch of
-    // their own where that is expected to be faster (4097 x 12288 x 4096: 200 against 218 us).
-    const int rest = g.M % 256, head = g.M - rest;
-    if (head > 0 && rest > 0) {
-        const Plan first = plan(head, g.N, g.K), second = plan(rest, g.N, g.K);
-        if (first.us + second.us + 3.0 < whole.us) {
-            MatmulArgs a = g, b = g;
-            a.M = head;
-            b.M = rest;
-            b.a += head * g.a_stride;
-            b.a_scale += head;
-            for (int i = 0; i < g.out.n; ++i)
-                b.out.ptr[i] = static_cast<char*>(g.out.ptr[i]) + head * g.out.stride[i] * (g.out_bf16 ? 2 : 4);
-            dma ? start<true>(first.form, a) : start<false>(first.form, a);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-            dma ? start<true>(second.form, b) : start<false>(second.form, b);
-            return hipGetLastError();
+    const int places = places_of(g);
+    if (!near(g.a_stride, g.M, g.K) || !near(g.w_stride, g.N, g.K)) {
+        // rows this far apart: the forms that address each row by itself
+        if ((g.M + 31LL) / 32 * ((g.N + 63LL) / 64) > kMostTiles) {
+            const int half = g.M / 2;
+            const hipError_t e = launch_matmul_i8(rows_of(g, 0, half));
+            return e == hipSuccess ? launch_matmul_i8(rows_of(g, half, g.M - half)) : e;
         }
+        const Form f = plan(g.M, g.N, g.K, places).form;
+        return launch(f == Form::rows ? f : Form::t32x64, g);
     }
-    dma ? start<true>(whole.form, g) : start<false>(whole.form, g);
-    return hipGetLastError();
+    const Plan whole = plan(g.M, g.N, g.K, places);
+    // Rows that would cost a round of large tiles of their own go into a second launch, of smaller
+    // ones: those past a multiple of 256 (4097 x 12288 x 4096: 189 against 207 us), or past the last
+    // round in which every CU has a tile (6023 x 2692 x 7008: 134 against 185).  Where less than a
+    // seventh is expected to be saved the two launches were as often slower.
+    const int high = g.M / 256, wide = (g.N + 255) / 256;
+    const int heads[2] = {high * 256, (int)((int64_t)high * wide / 256 * 256 / wide * 256)};
+    Plan first{}, second{};
+    int head = 0;
+    double least = .85 * whole.us;
+    for (int h : heads) {
+        if (h < 1 || h >= g.M) continue;
+        const Plan a = plan(h, g.N, g.K, places), b = plan(g.M - h, g.N, g.K, places);
+        if (a.us + b.us < least) least = a.us + b.us, head = h, first = a, second = b;
+    }
+    if (head > 0) {
+        const hipError_t e = launch(first.form, rows_of(g, 0, head));
+        return e == hipSuccess ? launch(second.form, rows_of(g, head, g.M - head)) : e;
+    }
+    return launch(whole.form, g);
 }
 
 }  // namespace gdr

@@ -352,6 +352,84 @@ def test_product_forms(form, dtype):
         assert bool((room[0] == 7.0).all()) and bool((room[M + 1] == 7.0).all())
 
 
+# The same where rows begin at whole lines, at multiples of 16, at whole words and anywhere: fragments
+# are read in place in the first three, and moved by 0 to 3 bytes in the last.
+PLACES = [(33, 2048, (2048, 2064, 2068, 2049)), (250, 700, (512, 528, 532, 515, 510)), (640, 1024, (1024, 1040, 1044, 1001)),
+          (1000, 2050, (2048, 2064, 2068, 2049, 514)), (1024, 8192, (1024, 1040, 1044, 1001)), (1486, 7920, (2048, 2064, 2068, 2326)),
+          (3000, 4001, (1024, 1040, 1044, 1001, 1003)), (4096, 4001, (2048, 2064, 2068, 2049)),
+          (4097, 12288, (4096, 2064, 2068, 2049)), (6023, 2690, (2064, 2068, 2049))]
+
+
+@pytest.mark.parametrize("M,N,Ks", PLACES, ids=[f"{m}x{n}" for m, n, _ in PLACES])
+def test_product_places(M, N, Ks):
+    for K in Ks:
+        a, w = codes(M, K, seed=1).cuda(), codes(N, K, seed=2).cuda()
+        sa, sw = rand(M, seed=3).abs().cuda() + 0.1, rand(N, seed=4).abs().cuda() * K ** -0.5
+        size, ref = product_reference(a, sa, w, sw, None)
+        note(f"M={M} N={N} K={K}")
+        y = gdr.matmul_i8(a, sa, w, sw, out_dtype=F32)
+        assert bool(((y.double() - ref).abs() <= 3 * U * size + U * ref.abs()).all()), (M, N, K)
+
+
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,N", [(60, 300), (300, 260), (1300, 2060), (2600, 2100)])
+def test_product_moved_fragments(M, N, off):
+    """Rows of odd distances that begin `off` bytes behind a whole word, in arrays that end with
+    their last byte, and whole stages of the reduction up to it."""
+    for K in (256, 512, 385, 20):
+        pad = 1 + (K % 2)
+        wide_a, wide_w = (codes((n - 1) * (K + pad) + K + off, seed=n).cuda() for n in (M, N))
+        a = wide_a[off:].as_strided((M, K), (K + pad, 1))
+        w = wide_w[off:].as_strided((N, K), (K + pad, 1))
+        sa, sw = rand(M, seed=3).abs().cuda() + 0.1, rand(N, seed=4).abs().cuda()
+        size, ref = product_reference(a, sa, w, sw, None)
+        note(f"M={M} N={N} K={K} off={off}")
+        y = gdr.matmul_i8(a, sa, w, sw, out_dtype=F32)
+        assert bool(((y.double() - ref).abs() <= 3 * U * size + U * ref.abs()).all()), (M, N, K)
+
+
+@pytest.mark.parametrize("stride", [(1 << 24) + 16, (1 << 24) + 4, (1 << 24) + 1])
+@pytest.mark.parametrize("M", [40, 150])
+def test_product_rows_far_apart(M, stride):
+    """Rows further apart than a tile's 2^31 bytes: the forms that address each row by itself."""
+    K = 300
+    buf = torch.zeros((M - 1) * stride + K, dtype=torch.int8, device="cuda")
+    a = buf.as_strided((M, K), (stride, 1))
+    a.copy_(codes(M, K, seed=1))
+    w = codes(2000, K, seed=2).cuda()
+    one, ones = torch.ones(M, device="cuda"), torch.ones(2000, device="cuda")
+    note(f"rows far apart M={M} stride={stride}")
+    want = a.contiguous().double() @ w.double().t()
+    assert torch.equal(gdr.matmul_i8(a, one, w, ones, out_dtype=F32).double(), want)
+    assert torch.equal(gdr.matmul_i8(w, ones, a, one, out_dtype=F32).double(), want.t())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("out", [(1, 1, 1, 1, 1, 1, 1, 255), (131, 127), (5, 250, 3), (7, 1, 250)])
+@pytest.mark.parametrize("M", [90, 700, 2500])
+def test_product_outputs_that_end_anywhere(M, out, dtype):
+    """Outputs whose rows begin at odd addresses and end inside a store, side by side in one array
+    that is written nowhere else."""
+    K, N = 192, sum(out)
+    a, w = codes(M, K, seed=1).cuda(), codes(N, K, seed=2).cuda()
+    sa, sw = rand(M, seed=3).abs().cuda() + 0.1, rand(N, seed=4).abs().cuda()
+    room = torch.full((M + 2, N + 3 * len(out) + 2), 7.0, dtype=dtype, device="cuda")
+    at, parts = 1, []
+    for n in out:
+        parts.append(room[1:M + 1, at:at + n])
+        at += n + 3
+    note(f"M={M} out={out} {dtype}")
+    gdr.matmul_i8(a, sa, w, sw, out=parts)
+    size, ref = product_reference(a, sa, w, sw, None)
+    tol = 3 * U * size + U * (ref.abs() + 4 * U * size)
+    if dtype == BF:
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    assert bool(((torch.cat(parts, 1).double() - ref).abs() <= tol).all())
+    for p in parts:
+        p.fill_(7.0)
+    assert bool((room == 7.0).all())
+
+
 @pytest.mark.parametrize("out", [(100, 156), (4, 8, 244), (1, 255), (3, 5, 7, 11, 13, 17, 19, 181), (128, 128), (64, 60, 132)])
 @pytest.mark.parametrize("M", [1, 40, 70, 300, 1030])
 def test_product_separate_outputs(M, out):
