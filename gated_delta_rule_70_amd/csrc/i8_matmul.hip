@@ -153,11 +153,18 @@ __device__ __forceinline__ void store_quad(const MatmulArgs& g, int m, int n, i3
         }
         return;
     }
+    // columns of this output, of the next one, and of any after that one by one
+    const int all = min(4, g.N - n);
+    const Where then = where(g.out, min(n + to.left, g.N - 1), E);
+    char *p = to.p + m * to.stride * E, *p2 = then.p + m * then.stride * E;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (n + j < g.N) {
-            const Where to = where(g.out, n + j, E);
-            store_value<BF16>(to.p + m * to.stride * E, v[j]);
+        if (j < min(to.left + then.left, all)) store_value<BF16>(j < to.left ? p + j * E : p2 + (j - to.left) * E, v[j]);
+#pragma unroll
+    for (int j = 2; j < 4; ++j)
+        if (j >= to.left + then.left && j < all) {
+            const Where one = where(g.out, n + j, E);
+            store_value<BF16>(one.p + m * one.stride * E, v[j]);
         }
 }
 
