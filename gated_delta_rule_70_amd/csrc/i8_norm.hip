@@ -271,7 +271,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_rmsnorm_kernel(No
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)n[i][j], (double)n[i][j], ss);
         ss = sum_head(ss, V);
-        const float rho = (float)rsqrt64(__builtin_fma(ss, per_v, (double)a.eps));
+        double rho64 = rsqrt64(__builtin_fma(ss, per_v, (double)a.eps));
+        if (rho64 > 0x1p126) {  // eps = 0 and a head of values below fp32's normal ones
+            rho64 *= 0x1p-64;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n[i][j] *= 0x1p64f;
+        }
+        const float rho = (float)rho64;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float silu = zv[j] * __builtin_amdgcn_rcpf(1.f + exp_neg(zv[j]));

@@ -73,7 +73,8 @@ int gdr_add_rmsnorm_i8(const gdr_norm_dims* dims, const void* x, const void* res
  *   q   = rint(127 n / A)                                  -> q      [rows][heads*cols] int8
  *   A / 127                                                -> scale  [rows]             fp32
  * n is computed in fp32 (sums of squares in fp64), so a value within fp32 rounding of the
- * border between two codes may take either.  Empty and non-finite rows as above.
+ * border between two codes may take either, and a gate below -87, where silu is less than 1e-35,
+ * may count as closed.  Empty and non-finite rows as above.
  * out_stride is ignored.
  */
 int gdr_gated_rmsnorm_i8(const gdr_norm_dims* dims, const void* o, const void* gate, const void* weight,

@@ -258,6 +258,20 @@ def test_gated_rmsnorm_special_rows(zt):
         check_gated(torch.ones(1, 1, 64), z[:, i:i + 1].contiguous(), w)
 
 
+@pytest.mark.parametrize("ot", [BF, F32])
+def test_gated_rmsnorm_heads_below_the_normal_range(ot):
+    """Without eps a head's norm is finite however small its values are: one value of fp32's
+    smallest ones among normal heads, and rows of nothing else."""
+    o, z = rand(4, 6, 64, seed=1).to(ot), rand(4, 6, 64, dtype=BF, seed=2)
+    tiny = torch.finfo(ot).smallest_normal / 64
+    o[0, 2] = tiny
+    o[1] = (rand(6, 64, seed=3).sign() * tiny).to(ot)
+    o[2, 1] = 0.0
+    o[2, 1, 5] = -tiny
+    o[3] = rand(6, 64, seed=4, scale=1e-38).to(ot)
+    check_gated(o, z, torch.ones(64), eps=0.0)
+
+
 def test_gated_rmsnorm_strides():
     wide_o, wide_z = rand(5, 1000, seed=1), rand(5, 900, dtype=BF, seed=2)
     w = rand(32, seed=3)
