@@ -5,7 +5,7 @@
 //
 // Forms, by how many outputs there are (see plan()): 16 x 16 outputs by 8 waves that share the
 // reduction, without LDS staging; small tiles whose waves share the reduction; 128-wide tiles;
-// 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 10.4 us, 4.8 TB/s,
+// 192 x 256 and 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 10.4 us, 4.8 TB/s,
 // the rate of a large copy being 5.1.  At 32768 x 4096 x 4096 the chip is limited by power: 447 us,
 // 2460 TOP/s (the library's int8 product reaches 2070 on 8192^3).
 #include "i8_launch.h"
@@ -250,6 +250,8 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
 // copied from the aligned word that its first byte lies in, with one more word behind each stage's
 // 128 bytes, and a fragment is moved into place, by 0 to 3 bytes, as it is read from LDS.  Words
 // are read whole: the first and the last may begin before the operand or end behind it.
+// At 4096 x 4096 x K, 256 x 256 tiles: K = 4096 60 us; 4100, where a stage's bytes of a row lie in two
+// lines, 78; 4097, moved, 95 (through registers, at any alignment, 92; 128 x 64 tiles 215, registers 278).
 // What bounds the 256 x 256 form: at 8192^3 the matrix cores are busy 74 % of the time at a clock of
 // 1.83 GHz; an order of issue with 68 % busy ran at 1.94 GHz and took the same time, so it is the
 // power that a product costs.  Tried and dropped (8192^3, 430 us): 32x32x32 products, 457;

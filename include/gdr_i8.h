@@ -20,7 +20,8 @@
  * nothing; statuses are gdr_status; results are bitwise reproducible (no atomics).  rows == 0
  * is a valid call that does nothing (pointers may then be NULL).  Strides are in elements,
  * between rows; within a row values are contiguous.  Pointers need only their element type's
- * alignment; the product is faster where a, w and their row strides are multiples of 16 bytes.
+ * alignment; the product is fastest where a, w and their row strides are multiples of 128 bytes,
+ * then of 4.  It reads the aligned words of 4 bytes that hold an operand's first and last bytes whole.
  */
 #ifndef GDR_I8_H
 #define GDR_I8_H
