@@ -11,7 +11,6 @@
 #include "i8_launch.h"
 
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "gdr_device.h"
@@ -615,7 +614,7 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
 }
 
 // ---- small tiles --------------------------------------------------------------------------
-// For products whose 256 x 256 tiles would leave most of the chip idle.  BM x BN outputs for a
+// For products whose larger tiles would leave most of the chip idle.  BM x BN outputs for a
 // workgroup; each wave makes a 32 x 32 block, and KG groups of waves share the reduction: a stage
 // is KG * 64 bytes of it, group k takes the k-th 64, and the groups' sums meet in LDS.  What bounds
 // these products is how fast a CU can bring its operands in, so the loop keeps STAGES - 1 stages
@@ -794,7 +793,7 @@ bool near(int64_t stride, int rows, int K) { return rows == 1 || stride <= (INT3
 // (filling the pipeline, storing) and a part for each reduction byte.  Forms of which two
 // workgroups fit a CU overlap their fixed parts; the others slow down as more CUs draw on memory
 // and power.  Where rows do not begin at whole lines, the 128 bytes of a stage lie in two lines and
-// all forms but those that read 256 in a row take longer; fragments that have to be moved into
+// all forms but those that read 256 or more in a row take longer; fragments that have to be moved into
 // place cost more again.  The constants were fitted to 11000 random sizes (17 to 32768 rows, 128 to
 // 12288 columns, reductions of 256 to 8192); the form so chosen takes 0.6 % longer than the fastest
 // on average, 14 % at the 99th percentile.
@@ -811,41 +810,52 @@ bool near(int64_t stride, int rows, int K) { return rows == 1 || stride <= (INT3
 //    1691 x  5760 x 4096 108.6    61.7          /  63.3           47.0     51.7
 //    3000 x  4096 x 4096 133.3    69.6          /  61.3           50.5     56.0
 //    8192 x  2048 x 8192 334.1   185.9          / 137.1          148.3    111.0
-// The form without tiles is also taken up to 16 rows and 8192 columns (1 x 4096 x 4096 6.5 against
-// 8.8 us; 1 x 12288 x 4096 12.6 against 11.1).
+// Fewer outputs, 16x16 without LDS / 32x32 / 32x64 (weights from memory; from the last-level cache):
+//       1 x  4096 x 4096  5.1 /  5.9 /  7.5    (5.2 / 5.8 / 7.5)
+//       1 x 12288 x 4096 11.2 /      / 12.8    (9.6 /     / 9.9)
+//      16 x  8192 x 4096  9.8 /  8.3 / 10.3
+//      64 x  4096 x 4096 16.3 /  6.7 /  8.2
+//     178 x  1280 x 3712 16.1 /  7.0 /  8.6
+//     256 x  1024 x 8192 29.8 /  9.2 / 12.6
+// 32x32 tiles serve where each CU has at most one: 3900 random sizes of that kind take 6 to 10 %
+// longer without them (the form chosen 0.6 % longer than the fastest).
 constexpr int64_t kMostTiles = (1 << 23) - 1;  // a launch has fewer than 2^32 threads, 512 for each tile
-enum class Form { rows, t32x64, t128x64, t128x128_deep, t128x128, t192x256, t256x256 };
+enum class Form { rows, t32x32, t32x64, t128x64, t128x128_deep, t128x128, t192x256, t256x256 };
 struct Plan {
     Form form;
     double us;
 };
 struct Cost {
-    int rows, cols, a_cu;     // of a tile; workgroups that fit a CU
+    uint32_t rows, cols;      // of a tile
+    int a_cu;                 // workgroups that fit a CU
     double fixed, per_k;      // us for a tile, and for 1000 reduction bytes of it
     double more;              // added to per_k: for a CU's first tile (two a CU), once every CU has one (one a CU)
     double places[4];         // per_k for each of places_of(), in relation to the first
 };
-constexpr Cost kCosts[] = {{16, 16, 0, 1.05, 1.43, 0, {1, .65, .75, 1.27}},
+constexpr Cost kCosts[] = {{16, 16, 2, 1.0, .85, 0, {1, .72, .82, 1.42}},
+                           {32, 32, 1, 2.3, .53, .27, {1, 1.17, 1.18, 1.75}},
                            {32, 64, 2, 2.6, 1.25, 0, {1, 1.02, 1.11, 1.54}},
                            {128, 64, 2, 2.7, 2.34, 0, {1, 1.51, 1.57, 2.50}},
                            {128, 128, 1, 3.5, 2.5, .9, {1, 1.60, 1.72, 0}},  // four stages: not where fragments are moved
                            {128, 128, 2, 4.4, 3.3, .5, {1, 1.41, 1.49, 2.05}},
                            {192, 256, 1, 7.3, 7.3, 1.2, {1, 1.32, 1.37, 1.90}},
                            {256, 256, 1, 9.9, 8.1, 1.6, {1, 1.38, 1.35, 1.95}}};
-Plan plan(int64_t M, int64_t N, int K, int places) {
+Plan plan(uint32_t M, uint32_t N, int K, int places) {
     Plan best{Form::rows, 1e30};
-    for (int f = 0; f < 7; ++f) {
+    for (int f = 0; f < 8; ++f) {
         const Cost& c = kCosts[f];
-        const int64_t tiles = ((M + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
-        if (tiles > kMostTiles || (f == (int)Form::t128x128_deep && (tiles > 256 || places == 3))) continue;
-        const double k = K * 1e-3 * c.places[places];
+        const int64_t tiles = (int64_t)((M + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
+        if (tiles > kMostTiles || ((f == (int)Form::t32x32 || f == (int)Form::t128x128_deep) && tiles > 256) ||
+            (f == (int)Form::t128x128_deep && places == 3))
+            continue;
+        double k = K * 1e-3 * c.places[places];
+        if (f == (int)Form::rows && M < 16) k *= .6 + .025 * M;  // rows of a that are read once
         const double n = tiles <= 1024 ? (double)((tiles + 255) / 256) : tiles / 256. + .5;
         const double fill = std::min(1.0, tiles / 256.0);
-        const double us = c.a_cu == 0   ? std::max(1.0, .5 + tiles / 512.) * (c.fixed + c.per_k * k)
-                          : c.a_cu == 2 ? c.fixed * std::ceil(n / 2) + k * (c.per_k * n + c.more)
+        const double pairs = tiles <= 1024 ? (double)((tiles + 511) / 512) : n / 2 + .5;
+        const double us = c.a_cu == 2 ? c.fixed * pairs + k * (c.per_k * n + c.more)
                                         : n * (c.fixed + k * (c.per_k + c.more * fill * fill));
         if (2.0 + us < best.us) best = Plan{(Form)f, 2.0 + us};  // 2: a launch
-        if (f == 0 && M <= 16 && N <= 8192) break;
     }
     return best;
 }
@@ -854,6 +864,7 @@ template <bool SHIFT>
 void start(Form f, const MatmulArgs& g) {
     switch (f) {
         case Form::rows: SHIFT ? rows<1>(g) : g.K % 16 == 0 ? rows<16>(g) : rows<4>(g); break;
+        case Form::t32x32: small<32, 32, 8, 3, SHIFT>(g); break;
         case Form::t32x64: small<32, 64, 4, 3, SHIFT>(g); break;
         case Form::t128x64: tiles<128, 64, 4, 2, 3, SHIFT>(g); break;
         case Form::t128x128_deep: tiles<128, 128, 2, 4, 4, false>(g); break;  // of whole words only
@@ -891,7 +902,7 @@ hipError_t launch_matmul_i8(const MatmulArgs& g) {
             return e == hipSuccess ? launch_matmul_i8(rows_of(g, half, g.M - half)) : e;
         }
         const Form f = plan(g.M, g.N, g.K, places).form;
-        return launch(f == Form::rows ? f : Form::t32x64, g);
+        return launch(f == Form::rows || f == Form::t32x32 ? f : Form::t32x64, g);
     }
     const Plan whole = plan(g.M, g.N, g.K, places);
     // Rows that would cost a round of large tiles of their own go into a second launch, of smaller

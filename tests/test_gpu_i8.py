@@ -368,7 +368,8 @@ def test_product_forms(form, dtype):
 
 # The same where rows begin at whole lines, at multiples of 16, at whole words and anywhere: fragments
 # are read in place in the first three, and moved by 0 to 3 bytes in the last.
-PLACES = [(33, 2048, (2048, 2064, 2068, 2049)), (250, 700, (512, 528, 532, 515, 510)), (640, 1024, (1024, 1040, 1044, 1001)),
+PLACES = [(1, 12288, (512, 528, 532, 515)), (9, 5000, (1024, 1040, 1044, 1001)), (33, 2048, (2048, 2064, 2068, 2049)),
+          (64, 4096, (4096, 4112, 4100, 4099, 1023)), (500, 510, (512, 528, 532, 515)), (250, 700, (512, 528, 532, 515, 510)), (640, 1024, (1024, 1040, 1044, 1001)),
           (1000, 2050, (2048, 2064, 2068, 2049, 514)), (1024, 8192, (1024, 1040, 1044, 1001)), (1486, 7920, (2048, 2064, 2068, 2326)),
           (3000, 4001, (1024, 1040, 1044, 1001, 1003)), (4096, 4001, (2048, 2064, 2068, 2049)),
           (4097, 12288, (4096, 2064, 2068, 2049)), (6023, 2690, (2064, 2068, 2049))]
