@@ -5,7 +5,7 @@
 //
 // Forms, by how many outputs there are (see plan()): 16 x 16 outputs by 8 waves that share the
 // reduction, without LDS staging; small tiles whose waves share the reduction; 128-wide tiles;
-// 192 x 256 and 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 10.4 us, 4.8 TB/s,
+// 192 x 256 and 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 9.7 us, 5.2 TB/s,
 // the rate of a large copy being 5.1.  At 32768 x 4096 x 4096 the chip is limited by power: 447 us,
 // 2460 TOP/s (the library's int8 product reaches 2070 on 8192^3).
 #include "i8_launch.h"
@@ -790,7 +790,7 @@ bool near(int64_t stride, int rows, int K) { return rows == 1 || stride <= (INT3
 
 // Form of a product and its expected time, from how many tiles a CU of the 256 gets (past four of
 // them the CUs no longer keep step, and a fraction counts) and what a tile takes: a fixed part
-// (filling the pipeline, storing) and a part for each reduction byte.  Forms of which two
+// (filling the pipeline, storing) and a part for each reduction byte.  Forms of which several
 // workgroups fit a CU overlap their fixed parts; the others slow down as more CUs draw on memory
 // and power.  Where rows do not begin at whole lines, the 128 bytes of a stage lie in two lines and
 // all forms but those that read 256 or more in a row take longer; fragments that have to be moved into
@@ -829,10 +829,10 @@ struct Cost {
     uint32_t rows, cols;      // of a tile
     int a_cu;                 // workgroups that fit a CU
     double fixed, per_k;      // us for a tile, and for 1000 reduction bytes of it
-    double more;              // added to per_k: for a CU's first tile (two a CU), once every CU has one (one a CU)
+    double more;              // added to per_k: for a CU's first tile (several a CU), once every CU has one (one a CU)
     double places[4];         // per_k for each of places_of(), in relation to the first
 };
-constexpr Cost kCosts[] = {{16, 16, 2, 1.0, .85, 0, {1, .72, .82, 1.42}},
+constexpr Cost kCosts[] = {{16, 16, 4, 1.0, .85, 0, {1, .72, .82, 1.42}},
                            {32, 32, 1, 2.3, .53, .27, {1, 1.17, 1.18, 1.75}},
                            {32, 64, 2, 2.6, 1.25, 0, {1, 1.02, 1.11, 1.54}},
                            {128, 64, 2, 2.7, 2.34, 0, {1, 1.51, 1.57, 2.50}},
@@ -852,8 +852,8 @@ Plan plan(uint32_t M, uint32_t N, int K, int places) {
         if (f == (int)Form::rows && M < 16) k *= .6 + .025 * M;  // rows of a that are read once
         const double n = tiles <= 1024 ? (double)((tiles + 255) / 256) : tiles / 256. + .5;
         const double fill = std::min(1.0, tiles / 256.0);
-        const double pairs = tiles <= 1024 ? (double)((tiles + 511) / 512) : n / 2 + .5;
-        const double us = c.a_cu == 2 ? c.fixed * pairs + k * (c.per_k * n + c.more)
+        const double groups = tiles <= 1024 ? (double)((tiles + 256 * c.a_cu - 1) / (256 * c.a_cu)) : n / c.a_cu + .5;
+        const double us = c.a_cu > 1 ? c.fixed * groups + k * (c.per_k * n + c.more)
                                         : n * (c.fixed + k * (c.per_k + c.more * fill * fill));
         if (2.0 + us < best.us) best = Plan{(Form)f, 2.0 + us};  // 2: a launch
     }
