@@ -5,7 +5,7 @@
 // rho = (mean s^2 + eps)^(-1/2), the code of the normed value t * rho at scale A * rho / 127 is
 // rint(127 t / A): rho cancels.  So the sum of squares and the maximum are reduced together,
 // the row stays in registers in between, and codes are stored after one reduction.  Bound by
-// memory: 32768 x 4096 bf16 with residual 155 us, 6.05 TB/s (a copy of 1 GiB reaches 5.1; part of
+// memory: 32768 x 4096 bf16 with residual 156 us, 6.0 TB/s (a copy of 1 GiB reaches 5.1; part of
 // what is read is still in the last-level cache); 4097 tokens of 32 x 128 bf16 through the gated
 // norm 20.0 us, 4.2 TB/s, where the exponentials cost about as much time as the memory.
 #include "i8_launch.h"
@@ -316,10 +316,18 @@ dim3 grid_of(int rows) {
 }
 
 // Threads for a row and groups for a thread: as many threads as the row fills with one or two groups
-// each, since a row is read and written once and what counts is loads in flight.  A row of up to
-// 2048 values by one wave (no barrier) pays once there are rows enough to fill the chip with them.
-// At 4097 rows of 4096 bf16: 256 threads with two groups 25.8 us, one wave with eight 45.6; in the
-// gated norm 512 threads with one group 20.1 us, 256 with two 21.4, one wave 39.9.
+// each, since a row is read and written once and what counts is loads in flight; groups beyond a
+// row's end cost time too.  A row of up to 1024 values by one wave (no barrier) pays once there are
+// rows enough to fill the chip with them.  us, threads x groups, bf16 with residual:
+//    8192 x  1024    64x2 15.1   64x4 16.3   256x1 16.0
+//   16384 x  2048    64x4 55.5  256x1 43.9   256x2 47.6
+//    4097 x  4096   256x2 25.6   64x8 45.6
+//    8192 x  8192   256x4 90.2  512x2 84.1  1024x1 89.1
+//    4096 x 16384  1024x2 86.1 1024x4 126.4
+// and in the gated norm, bf16:
+//    4097 x 32 x 128  512x1 16.4  256x2 17.5  1024x1 26.9
+//    8000 x 48 x 128  512x2 56.1 1024x1 60.8   (4097 x 64 x 128 fp32 56.1 and 53.7)
+//    4097 x 128 x 128 1024x2 83.3 1024x4 127.6
 template <typename TX, typename TW, typename T>
 void add_rmsnorm_typed(const NormArgs& a) {
     auto go = [&](auto tpr, auto nv) {
@@ -333,14 +341,16 @@ void add_rmsnorm_typed(const NormArgs& a) {
     using std::integral_constant;
     if (a.cols <= 512)
         go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (a.cols <= 2048 && a.rows > 4096)
-        go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    else if (a.cols <= 1024 && a.rows > 4096)
+        go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     else if (a.cols <= 2048)
         go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (a.cols <= 4096)
         go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     else if (a.cols <= 8192)
-        go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+        go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else if (a.cols <= 16384)
+        go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
     else
         go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
@@ -362,8 +372,12 @@ void gated_typed(const NormArgs& a) {
         go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (D <= 4096)
         go(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+    else if (D <= 8192 && a.x_bf16)
+        go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
     else if (D <= 8192)
         go(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
+    else if (D <= 16384)
+        go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
     else
         go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }

@@ -63,6 +63,20 @@ def test_add_rmsnorm(D, dtypes):
     check_norm(x[:1], w, None)
 
 
+@pytest.mark.parametrize("D", [520, 1000, 1001, 1024, 1032, 8192, 8195, 16384])
+def test_add_rmsnorm_of_many_rows(D):
+    M = 4100 if D < 2000 else 300
+    x, r, w = rand(M, D, dtype=BF, seed=D), rand(M, D, dtype=BF, seed=D + 1, scale=4.0), rand(D, dtype=BF, seed=D + 2)
+    check_norm(x, w, r)
+    check_norm(x.float(), w.float(), None)
+
+
+@pytest.mark.parametrize("M,H,V", [(2100, 8, 128), (300, 48, 128), (300, 65, 64), (60, 100, 128), (60, 129, 128)])
+@pytest.mark.parametrize("types", [(BF, BF, F32), (F32, BF, F32)], ids=["bf16", "f32"])
+def test_gated_rmsnorm_widths(M, H, V, types):
+    check_gated(rand(M, H, V, dtype=types[0], seed=M), rand(M, H, V, dtype=types[1], seed=M + 1), rand(V, seed=V).to(types[2]))
+
+
 @pytest.mark.parametrize("D", [96, 100])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_add_rmsnorm_many_rows_and_ties(D, dtype):
