@@ -10,8 +10,9 @@ Activations and weights are int8 codes with an fp32 scale for each token and eac
 channel; residual stream, gate and outputs are bf16 or fp32.  Forward only.
 
 Work is enqueued on the current stream, or on ``stream`` (a torch stream or a handle), which the
-caller orders after whatever made the inputs; memory used there is not reused before it is done.
-Calls allocate nothing but the outputs that are not given, and can be captured into graphs.
+caller orders after whatever made the inputs (and last used the outputs that are given); memory used
+there is not reused before it is done.  Calls allocate nothing but the outputs that are not given,
+of the memory of the stream that writes them, and can be captured into graphs.
 """
 from __future__ import annotations
 
@@ -122,9 +123,9 @@ def _stream(stream, dev, names, tensors):
             here = _raw_stream(dev)
             if stream is None:
                 return here
-            there = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            there = _handle(stream)
             if there != here:  # the allocator must not hand the memory on before that stream is done
-                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(there)
+                s = _torch_stream(stream)
                 for t in tensors:
                     if t is not None:
                         t.record_stream(s)
@@ -136,6 +137,28 @@ def _stream(stream, dev, names, tensors):
     for name, t in zip(names, tensors):
         if t is not None and t.get_device() != at:
             raise ValueError(f"{name} is on GPU {t.get_device()}, the current one is {at}")
+
+
+def _handle(stream):
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _torch_stream(stream):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream))
+
+
+def _empty(shape, dtype, like, stream):
+    """A new tensor on the GPU of ``like``, of memory that ``stream`` may write at once.  What the
+    allocator takes from the current stream's memory may still be in use by work queued there, which
+    another stream does not wait for; so that other stream's own memory is taken, and kept until the
+    current one, on which the caller will read it, is done too."""
+    if stream is None or not like.is_cuda or _handle(stream) == _raw_stream(like.get_device()):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(here)
+    return t
 
 
 def _rows(t, name, tail=1):
@@ -161,9 +184,9 @@ def _rows(t, name, tail=1):
     return step if row is None or t.numel() == 0 else row
 
 
-def _out(t, name, shape, dtype, device):
+def _out(t, name, shape, dtype, like, stream):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, like, stream)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -219,7 +242,7 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
             raise TypeError(f"residual must be {dtype}, got {residual.dtype}")
         r_stride = D if residual.is_contiguous() else _rows(residual, "residual")
         if out_residual is None:
-            out_residual = torch.empty(shape, dtype=dtype, device=x.device)
+            out_residual = _empty(shape, dtype, x, stream)
         if out_residual.shape != shape:
             raise ValueError(f"out_residual must be {list(shape)}, got {list(out_residual.shape)}")
         if out_residual.dtype is not dtype:
@@ -227,9 +250,9 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
         out_stride = D if out_residual.is_contiguous() else _rows(out_residual, "out_residual")
     lead = shape[:-1]
     if q is None or q.shape != shape or q.dtype is not _I8 or not q.is_contiguous():
-        q = _out(q, "q", shape, _I8, x.device)
+        q = _out(q, "q", shape, _I8, x, stream)
     if scale is None or scale.shape != lead or scale.dtype is not _F32 or not scale.is_contiguous():
-        scale = _out(scale, "scale", lead, _F32, x.device)
+        scale = _out(scale, "scale", lead, _F32, x, stream)
     dims = _NORM.pack(scale.numel(), 1, D, xc, 0, _CODE[wt], eps if 0 <= eps <= _F32_MAX else _eps(eps),
                       D if x.is_contiguous() else _rows(x, "x"), r_stride, out_stride)
     s = _stream(stream, x.get_device(), _NORM_NAMES, (weight, residual, q, scale, out_residual, x))
@@ -269,9 +292,9 @@ def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, str
     D = H * V
     qshape = (*lead, D)
     if q is None or q.shape != qshape or q.dtype is not _I8 or not q.is_contiguous():
-        q = _out(q, "q", qshape, _I8, o.device)
+        q = _out(q, "q", qshape, _I8, o, stream)
     if scale is None or scale.shape != lead or scale.dtype is not _F32 or not scale.is_contiguous():
-        scale = _out(scale, "scale", lead, _F32, o.device)
+        scale = _out(scale, "scale", lead, _F32, o, stream)
     dims = _NORM.pack(scale.numel(), H, V, oc, gc, wc, eps if 0 <= eps <= _F32_MAX else _eps(eps),
                       D if o.is_contiguous() else _rows(o, "o", 2),
                       D if gate.is_contiguous() else _rows(gate, "gate", 2), 0)
@@ -318,7 +341,7 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
         raise ValueError(f"1 to {MATMUL_I8_MAX_OUT} outputs are supported, got {n}")
     for i, t in enumerate(outs):
         if isinstance(t, int) and t > 0:
-            outs[i] = torch.empty(*lead, t, dtype=out_dtype, device=a.device)
+            outs[i] = _empty((*lead, t), out_dtype, a, stream)
     matrix = len(lead) == 1
     dtype, cols, strides, ptrs = None, [], [], []
     for t in outs:
