@@ -144,7 +144,10 @@ def _handle(stream):
 
 
 def _torch_stream(stream):
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream))
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _handle(stream)  # 0: the default stream, which ExternalStream takes for no handle at all
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
 def _empty(shape, dtype, like, stream):

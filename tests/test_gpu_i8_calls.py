@@ -37,3 +37,21 @@ def test_new_outputs_on_another_stream(given):
     side.synchronize()
     for a, b in zip((*got, *y), (*want, *y_want)):
         assert torch.equal(a, b)
+
+
+def test_default_stream_by_handle():
+    """Handle 0, given while another stream is the current one: the default stream, whose memory new
+    outputs are then of."""
+    M, D = 4099, 1024
+    x, r, nw, w, ws = inputs(M, D)
+    want = gdr.add_rmsnorm_i8(x, nw, residual=r)
+    note("default stream by its handle")
+    freed = [torch.empty_like(t) for t in want]
+    places = {t.data_ptr() for t in freed}
+    del freed
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = gdr.add_rmsnorm_i8(x, nw, residual=r, stream=0)
+    torch.cuda.synchronize()
+    assert places & {t.data_ptr() for t in got}
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -10,6 +10,7 @@ import gated_delta_rule_70_amd as gdr
 from gated_delta_rule_70_amd import quantized as qz
 
 HERE, THERE = 111, 222   # handles of the current stream and of another one
+NEW = 333                # and of one that nobody uses
 
 
 class Gpu(torch.Tensor):
@@ -49,7 +50,9 @@ def machine(monkeypatch):
 
     monkeypatch.setattr(torch, "empty", take)
     monkeypatch.setattr(torch.cuda, "stream", on)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    # torch's, given the handle 0, is a new stream
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: Stream(handle or NEW))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: Stream(0))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(active[-1]))
     monkeypatch.setattr(qz, "_current_device", lambda: 0)
     monkeypatch.setattr(qz, "_raw_stream", lambda dev: active[-1])
@@ -92,3 +95,10 @@ def test_given_tensors_on_another_stream(machine):
     x, w, r, q, s, o = gpu(3, 64), gpu(64), gpu(3, 64), i8(3, 64), gpu(3), gpu(3, 64)
     gdr.add_rmsnorm_i8(x, w, residual=r, q=q, scale=s, out_residual=o, stream=THERE)
     assert all(t.kept_for == (THERE,) for t in (x, w, r, q, s, o))
+
+
+def test_handle_of_the_default_stream(machine):
+    x, w = gpu(3, 64), gpu(64)
+    q, s, _ = gdr.add_rmsnorm_i8(x, w, stream=0)
+    assert x.kept_for == w.kept_for == (0,)
+    assert q.taken_from == s.taken_from == 0
