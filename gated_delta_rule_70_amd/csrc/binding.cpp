@@ -1,7 +1,9 @@
 // The short way into the 8-bit operators from Python: a call whose tensors are all given,
 // contiguous, of matching types and shapes and on the current GPU goes straight from here to the
-// C entry point.  Any other call returns None, and the Python binding takes it: it allocates,
-// handles strides and raises the errors.  The checks cost 0.3 us here and 3 us in Python, where the
+// C entry point, whose status is returned.  Any other call returns None, and so does one whose
+// arguments are refused, and the Python binding takes it: it allocates, handles strides and raises
+// the errors.  A call that failed past the checks of its arguments is not handed over: part of it may
+// have run, and a second try would add a residual twice.  The checks cost 0.3 us here and 3 us in Python, where the
 // kernels of a few tokens take 4 us.
 #include <Python.h>
 
@@ -57,8 +59,8 @@ bool stream_of(int dev, void** stream) {
 }
 
 PyObject* result(int status) {
-    if (status == GDR_OK) Py_RETURN_TRUE;
-    Py_RETURN_NONE;
+    if (status >= GDR_ERR_NULL && status <= GDR_ERR_ALIAS) Py_RETURN_NONE;  // nothing was enqueued
+    return PyLong_FromLong(status);
 }
 
 // Runs f and turns whatever goes wrong into None.

@@ -218,8 +218,12 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
     (which may be ``x`` or ``residual`` itself), and is None without a residual.  A row of
     zeros has scale 0, a row that holds NaN or infinity scale NaN and q 0.
     """
-    if stream is None and (_B or _binding()).add_rmsnorm(x, weight, residual, eps, q, scale, out_residual):
-        return q, scale, out_residual
+    if stream is None:
+        status = (_B or _binding()).add_rmsnorm(x, weight, residual, eps, q, scale, out_residual)
+        if status is not None:
+            if status:
+                _fail(status)
+            return q, scale, out_residual
     shape, dtype = x.shape, x.dtype
     if not shape or shape[-1] < 1:
         raise ValueError(f"x must be [..., D], got {list(shape)}")
@@ -274,8 +278,12 @@ def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, str
     ``o`` and ``gate`` are ``[..., HV, dv]`` (bf16 or fp32 each; dv 32, 64 or 128), ``weight``
     ``[dv]`` (bf16 or fp32).  Returns ``q`` (int8, ``[..., HV * dv]``) and ``scale`` (fp32, ``[...]``).
     """
-    if stream is None and (_B or _binding()).gated_rmsnorm(o, gate, weight, eps, q, scale):
-        return q, scale
+    if stream is None:
+        status = (_B or _binding()).gated_rmsnorm(o, gate, weight, eps, q, scale)
+        if status is not None:
+            if status:
+                _fail(status)
+            return q, scale
     shape = o.shape
     if len(shape) < 2:
         raise ValueError(f"o must be [..., HV, dv], got {list(shape)}")
@@ -319,8 +327,12 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     output, a sequence of column counts for that many new tensors, or a sequence of tensors (of
     one type; their rows may be strided).  Returns a tensor, or a tuple for a sequence.
     """
-    if stream is None and (_B or _binding()).matmul(a, a_scale, w, w_scale, bias, out):
-        return out if isinstance(out, torch.Tensor) else tuple(out)
+    if stream is None:
+        status = (_B or _binding()).matmul(a, a_scale, w, w_scale, bias, out)
+        if status is not None:
+            if status:
+                _fail(status)
+            return out if isinstance(out, torch.Tensor) else tuple(out)
     shape, wshape = a.shape, w.shape
     if not shape or len(wshape) != 2 or shape[-1] != wshape[1]:
         raise ValueError(f"a must be [..., K] and w [N, K], got {list(shape)} and {list(wshape)}")

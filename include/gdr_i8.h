@@ -16,8 +16,8 @@
  *
  * Conventions (those of gdr.h unless said otherwise): device pointers; the caller owns every
  * buffer; work is enqueued on `stream` and the call returns without waiting; every argument
- * check runs on the host before any HIP call, so a call that returns an error has enqueued
- * nothing; statuses are gdr_status; results are bitwise reproducible (no atomics).  rows == 0
+ * check runs on the host before any HIP call, so a call that is refused has enqueued nothing
+ * (one that returns GDR_ERR_HIP may have); statuses are gdr_status; results are bitwise reproducible (no atomics).  rows == 0
  * is a valid call that does nothing (pointers may then be NULL).  Strides are in elements,
  * between rows; within a row values are contiguous.  Pointers need only their element type's
  * alignment; the product is fastest where a, w and their row strides are multiples of 128 bytes,

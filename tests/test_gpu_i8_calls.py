@@ -1,4 +1,6 @@
 """How calls of the 8-bit operators go: the memory of new outputs, streams given by handle, errors."""
+import ctypes
+
 import pytest
 import torch
 
@@ -55,3 +57,53 @@ def test_default_stream_by_handle():
     assert places & {t.data_ptr() for t in got}
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+class FailingLibrary:
+    """Entry points that fail as where HIP reports an error, and count the calls of each."""
+
+    def __init__(self):
+        self.calls = []
+        self.kept = {}
+        for name, n in (("gdr_add_rmsnorm_i8", 8), ("gdr_gated_rmsnorm_i8", 7), ("gdr_matmul_i8", 8)):
+            self.kept[name] = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * n)(self.entry(name))
+            setattr(self, name, self.entry(name))
+
+    def entry(self, name):
+        def failing(*args):
+            self.calls.append(name)
+            return 7
+        return failing
+
+    def addresses(self):
+        return [ctypes.cast(self.kept[n], ctypes.c_void_p).value
+                for n in ("gdr_add_rmsnorm_i8", "gdr_gated_rmsnorm_i8", "gdr_matmul_i8")]
+
+    gdr_status_str = staticmethod(lambda status: b"a HIP call failed")
+
+
+def test_a_failed_launch_is_not_tried_again(monkeypatch):
+    """Part of a call may have run when a launch fails: adding a residual in place again would add it
+    twice.  (The library is replaced by one that launches nothing.)"""
+    qz = gdr.quantized
+    M, D = 3, 64
+    x, r, nw, w, ws = inputs(M, D)
+    q, s, h = torch.empty(M, D, device="cuda", dtype=I8), torch.empty(M, device="cuda"), torch.empty_like(x)
+    y = torch.empty(M, 64, device="cuda")
+    o = torch.empty(M, 2, 32, device="cuda")
+    qz._binding()
+    L, bad = qz._lib(), FailingLibrary()
+    real = [ctypes.cast(f, ctypes.c_void_p).value for f in (L.gdr_add_rmsnorm_i8, L.gdr_gated_rmsnorm_i8, L.gdr_matmul_i8)]
+    calls = {"gdr_add_rmsnorm_i8": lambda: gdr.add_rmsnorm_i8(x, nw, residual=r, q=q, scale=s, out_residual=r),
+             "gdr_gated_rmsnorm_i8": lambda: gdr.gated_rmsnorm_i8(o, o, torch.ones(32, device="cuda"), q=q, scale=s),
+             "gdr_matmul_i8": lambda: gdr.matmul_i8(q, s, w, ws, out=y)}
+    try:
+        qz._B.bind(*bad.addresses(), qz._current_device, qz._raw_stream)
+        monkeypatch.setattr(qz, "_L", bad)
+        for name, call in calls.items():
+            bad.calls.clear()
+            with pytest.raises(gdr.GdrError) as e:
+                call()
+            assert e.value.status == 7 and bad.calls == [name]
+    finally:
+        qz._B.bind(*real, qz._current_device, qz._raw_stream)
