@@ -150,11 +150,53 @@ __device__ __forceinline__ void reduce_row(double& sum, T& top, int& bad) {
     }
 }
 
+// Scale and codes of a row whose products all lie below 2^-100, with t in fp64: s is read again, from
+// where this thread has just written it or from what it was made of.  Such rows are rare, so t is
+// computed twice instead of being held in registers that every row would have to do without.
+template <typename TX, typename TW, int TPR, bool PART>
+__device__ __forceinline__ void norm_small_row(const TX* x, const TX* r, const TX* out, const TW* w, int8_t* q, float* scale,
+                                               int D, int tid, double sum, float eps) {
+    auto products = [&](int e, double (&t)[8]) {
+        float s[8], wv[8];
+        load8<PART>(out ? out + e : x + e, D - e, s);
+        load8<PART>(w + e, D - e, wv);
+        if (r && !out) {
+            float rv[8];
+            load8<PART>(r + e, D - e, rv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = round_to(s[j] + rv[j], x);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = (double)s[j] * (double)wv[j];
+    };
+    double top = 0., none = 0.;
+    int bad = 0;
+#pragma unroll 1
+    for (int e = tid * 8; e < D; e += TPR * 8) {
+        double t[8];
+        products(e, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmax(top, fabs(t[j]));
+    }
+    reduce_row<TPR>(none, top, bad);
+    if (tid == 0) *scale = top == 0. ? 0.f : (float)(top * (1.0 / sqrt(sum / D + (double)eps)) / 127.0);
+#pragma unroll 1
+    for (int e = tid * 8; e < D; e += TPR * 8) {
+        double t[8];
+        products(e, t);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (top == 0. ? 0.f : (float)rint(t[j] * 127.0 / top)) + kRound;
+        store_codes<PART>(q + e, D - e, pack8(y, false));
+    }
+}
+
 // Residual addition, norm and codes.  TPR threads for each row, NV groups of 8 consecutive values
 // in each thread.
 //
-// T holds t: fp32 where s and weight are bf16 (a product of two 8-bit significands is exact),
-// fp64 otherwise (exact again), so A is exact too.  127 t / A is taken in fp32 first: its error
+// T holds t: fp32 where s and weight are bf16 (a product of two 8-bit significands is exact down
+// to 2^-134; a smaller one is no longer, which matters only in rows of nothing above 2^-100: those
+// are done again, see above), fp64 otherwise (exact again), so A is exact too.  127 t / A is taken in fp32 first: its error
 // is below 4 * 2^-24 relative, 2^-15 absolute; within 2^-14 of a border between codes (one value
 // in 8000) it is taken again in fp64.
 template <typename TX, typename TW, typename T, int TPR, int NV, bool PART>
@@ -199,6 +241,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
         }
     }
     reduce_row<TPR>(sum, top, bad);
+    if constexpr (std::is_same_v<T, float>) {
+        if (__builtin_expect(top < 0x1p-100f && sum > 0. && !bad, 0)) {  // the whole row alike
+            norm_small_row<TX, TW, TPR, PART>(x, r, out, w, q, a.scale + row, D, tid, sum, a.eps);
+            return;
+        }
+    }
 
     if (tid == 0) {
         const double rho = 1.0 / sqrt(sum / D + (double)a.eps);
