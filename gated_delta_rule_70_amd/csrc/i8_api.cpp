@@ -11,23 +11,34 @@
 
 namespace {
 
+// The bytes of an array of evenly spaced rows.
 struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
+    uintptr_t lo, hi;        // [lo, hi), from the first value to the last
+    uintptr_t width, apart;  // of a row, and from one to the next (0: one row)
 };
 
-// Bytes from the first to the last value of `rows` rows of `cols` values, `stride` apart.
-// False where that passes 2^62.
+// The array of `rows` rows of `cols` values, `stride` apart.  False where that passes 2^62.
 bool range_of(const void* p, int64_t rows, int64_t cols, int64_t stride, int64_t elt, Range* r) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    *r = Range{lo, lo};
+    *r = Range{lo, lo, 0, 0};
     if (!p || rows < 1) return true;
     constexpr int64_t lim = int64_t(1) << 62;
     if (rows > 1 && stride > (lim / elt - cols) / (rows - 1)) return false;
     r->hi = lo + static_cast<uintptr_t>(((rows - 1) * stride + cols) * elt);
+    r->width = static_cast<uintptr_t>(cols * elt);
+    r->apart = rows > 1 ? static_cast<uintptr_t>(stride * elt) : 0;
     return r->hi >= lo;
 }
 
-bool overlap(const Range& a, const Range& b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+// Whether two arrays share bytes.  Those with rows equally far apart may be column ranges of one wider
+// array, one array's rows between the other's; of any others that cross, it is taken that they do.
+bool overlap(const Range& a, const Range& b) {
+    if (!(a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi)) return false;
+    if (a.apart == 0 || a.apart != b.apart) return true;
+    const Range &first = a.lo < b.lo ? a : b, &second = a.lo < b.lo ? b : a;
+    const uintptr_t at = (second.lo - first.lo) % a.apart;  // where second's rows begin, from first's
+    return at < first.width || second.width > a.apart - at;
+}
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -169,17 +180,9 @@ int gdr_matmul_i8(const gdr_matmul_i8_dims* dims, const int8_t* a, const float* 
         g.out.ptr[i] = outs[i];
         g.out.stride[i] = d.out_stride[i];
     }
-    // outputs may be column ranges of one wider array (equal strides, columns apart); any other
-    // overlap is refused
     for (int i = 0; i < d.n_out; ++i)
-        for (int j = 0; j < i; ++j) {
-            if (!overlap(out[i], out[j])) continue;
-            const int lo = out[i].lo < out[j].lo ? i : j, hi = lo == i ? j : i;
-            const int64_t apart = (int64_t)(out[hi].lo - out[lo].lo);
-            if (d.M == 1 || d.out_stride[i] != d.out_stride[j] || apart < d.out_cols[lo] * eo ||
-                apart + d.out_cols[hi] * eo > d.out_stride[i] * eo)
-                return GDR_ERR_ALIAS;
-        }
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return GDR_ERR_ALIAS;
     g.M = d.M;
     g.N = (int)N;
     g.K = d.K;

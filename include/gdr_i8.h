@@ -61,7 +61,8 @@ typedef struct {
  * the exact quotient (borders between two codes are decided in 64 bits).  A row with A = 0
  * has q = 0 and scale 0.  A row whose t holds a NaN, an infinity or a value beyond fp32's
  * range has q = 0 and scale NaN.  out_residual may be x or residual itself (same pointer and
- * stride); no other output may overlap an input or another output.
+ * stride), or a column range beside theirs in one wider array; no other output may overlap an input
+ * or another output.
  */
 int gdr_add_rmsnorm_i8(const gdr_norm_dims* dims, const void* x, const void* residual, const void* weight,
                        int8_t* q, float* scale, void* out_residual, void* stream);

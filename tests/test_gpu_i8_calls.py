@@ -107,3 +107,24 @@ def test_a_failed_launch_is_not_tried_again(monkeypatch):
             assert e.value.status == 7 and bad.calls == [name]
     finally:
         qz._B.bind(*real, qz._current_device, qz._raw_stream)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [96, 333, 4096])
+def test_streams_side_by_side(D, dtype):
+    """Input, residual and new residual stream as column ranges of one array, which is written nowhere
+    else."""
+    M = 7
+    gen = torch.Generator("cuda").manual_seed(D)
+    wide = torch.randn(M, 3 * D + 2, device="cuda", generator=gen).to(dtype)
+    w = torch.rand(D, device="cuda", generator=gen).to(dtype)
+    before = wide.clone()
+    x, out, r = wide[:, :D], wide[:, D:2 * D], wide[:, 2 * D:3 * D]
+    want = gdr.add_rmsnorm_i8(x.contiguous(), w, residual=r.contiguous())
+    note(f"streams side by side D={D} {dtype}")
+    got = gdr.add_rmsnorm_i8(x, w, residual=r, out_residual=out)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    before[:, D:2 * D] = want[2]
+    assert torch.equal(wide, before)
