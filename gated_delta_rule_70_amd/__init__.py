@@ -76,8 +76,20 @@ def lib():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run `python -m gated_delta_rule_70_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
+    try:
+        _bind(L)
+    except AttributeError as e:  # a symbol that an older library does not have
+        raise RuntimeError(f"{LIB_PATH} is of another version; rebuild it ({e})") from None
+    _lib = L
+    return L
+
+
+def _bind(L):
+    """Argument types of the entry points, once the library's version is known to be this one."""
     L.gdr_abi_version.restype = ctypes.c_int
     L.gdr_abi_version.argtypes = []
+    if L.gdr_abi_version() != ABI_VERSION:
+        raise RuntimeError("libgdr.so ABI version mismatch; rebuild it")
     L.gdr_status_str.restype = ctypes.c_char_p
     L.gdr_status_str.argtypes = [ctypes.c_int]
     L.gdr_decode_step.restype = ctypes.c_int
@@ -105,10 +117,6 @@ def lib():
     L.gdr_fused_recurrent_varlen.restype = ctypes.c_int
     L.gdr_fused_recurrent_varlen.argtypes = [ctypes.POINTER(Dims)] + [_VP] * 10
     quantized.bind(L)
-    if L.gdr_abi_version() != ABI_VERSION:
-        raise RuntimeError("libgdr.so ABI version mismatch; rebuild it")
-    _lib = L
-    return L
 
 
 def _check(status: int):
