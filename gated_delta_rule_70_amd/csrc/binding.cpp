@@ -212,4 +212,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject* m = PyModule_Create(&module);
+    // of what bind and the calls take and return: quantized.py refuses another one
+    if (m && PyModule_AddIntConstant(m, "VERSION", 1) != 0) Py_CLEAR(m);
+    return m;
+}
