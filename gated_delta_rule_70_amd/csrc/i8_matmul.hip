@@ -3,17 +3,17 @@
 // Sums are int32 in the matrix cores (v_mfma_i32_16x16x64_i8), exact for K <= 131071.  Scales and
 // bias are applied in fp32; a bf16 output is rounded once, as it is stored.
 //
-// Forms, by how many outputs there are (see plan()): 16 x 16 outputs by 8 waves that share the
+// Forms, by how many outputs there are (plan() in i8_plan.h): 16 x 16 outputs by 8 waves that share the
 // reduction, without LDS staging; small tiles whose waves share the reduction; 128-wide tiles;
 // 192 x 256 and 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 9.7 us, 5.2 TB/s,
 // the rate of a large copy being 5.1.  At 32768 x 4096 x 4096 the chip is limited by power: 447 us,
 // 2460 TOP/s (the library's int8 product reaches 2070 on 8192^3).
 #include "i8_launch.h"
 
-#include <algorithm>
 #include <type_traits>
 
 #include "gdr_device.h"
+#include "i8_plan.h"
 
 namespace gdr {
 
@@ -777,89 +777,6 @@ void tiles(const MatmulArgs& g) {
         hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, STAGES, SHIFT, false>), grid, dim3(WM * WN * 64), 0, g.stream, g);
 }
 
-// Where rows of a and w begin: all at whole lines of 128 bytes (0), at multiples of 16 (1), at
-// whole words (2), or anywhere (3).
-int places_of(const MatmulArgs& g) {
-    const uint64_t all = reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.w) |
-                         (g.M > 1 ? (uint64_t)g.a_stride : 0) | (g.N > 1 ? (uint64_t)g.w_stride : 0);
-    return all % 128 == 0 ? 0 : all % 16 == 0 ? 1 : all % 4 == 0 ? 2 : 3;
-}
-
-// A tile's rows lie within 2^31 bytes.
-bool near(int64_t stride, int rows, int K) { return rows == 1 || stride <= (INT32_MAX - K - 8) / 255; }
-
-// Form of a product and its expected time, from how many tiles a CU of the 256 gets (past four of
-// them the CUs no longer keep step, and a fraction counts) and what a tile takes: a fixed part
-// (filling the pipeline, storing) and a part for each reduction byte.  Forms of which several
-// workgroups fit a CU overlap their fixed parts; the others slow down as more CUs draw on memory
-// and power.  Where rows do not begin at whole lines, the 128 bytes of a stage lie in two lines and
-// all forms but those that read 256 or more in a row take longer; fragments that have to be moved into
-// place cost more again.  The constants were fitted to 11000 random sizes (17 to 32768 rows, 128 to
-// 12288 columns, reductions of 256 to 8192); the form so chosen takes 0.6 % longer than the fastest
-// on average, 14 % at the 99th percentile.
-// M x N x K in us, rows beginning at whole lines:
-//                        32x64  128x64  128x128 (4 / 2 stages)  192x256  256x256
-//      32 x 12288 x 4096  14.2    18.6     20.0 /  30.9           40.8     47.3
-//     128 x  4096 x 4096   8.5    12.3     15.5 /  21.9           32.4     38.1
-//     512 x  4096 x 4096  22.6    13.7     16.2 /  22.4           33.2     39.6
-//    1024 x  4096 x 4096  47.0    23.0     20.0 /  25.1           34.4     40.2
-//     512 x 12288 x 4096  77.3    43.6     44.2 /  40.3           46.6     53.3
-//    2048 x  4096 x 4096  99.1    50.4     43.0 /  38.3           47.2     50.7
-//    4096 x  4096 x 1024  73.3    32.4          /  26.0           28.9     21.8
-//    8192 x  8192 x  512          99.8          /  77.9           64.0     68.6
-//    1691 x  5760 x 4096 108.6    61.7          /  63.3           47.0     51.7
-//    3000 x  4096 x 4096 133.3    69.6          /  61.3           50.5     56.0
-//    8192 x  2048 x 8192 334.1   185.9          / 137.1          148.3    111.0
-// Fewer outputs, 16x16 without LDS / 32x32 / 32x64 (weights from memory; from the last-level cache):
-//       1 x  4096 x 4096  5.1 /  5.9 /  7.5    (5.2 / 5.8 / 7.5)
-//       1 x 12288 x 4096 11.2 /      / 12.8    (9.6 /     / 9.9)
-//      16 x  8192 x 4096  9.8 /  8.3 / 10.3
-//      64 x  4096 x 4096 16.3 /  6.7 /  8.2
-//     178 x  1280 x 3712 16.1 /  7.0 /  8.6
-//     256 x  1024 x 8192 29.8 /  9.2 / 12.6
-// 32x32 tiles serve where each CU has at most one: 3900 random sizes of that kind take 6 to 10 %
-// longer without them (the form chosen 0.6 % longer than the fastest).
-constexpr int64_t kMostTiles = (1 << 23) - 1;  // a launch has fewer than 2^32 threads, 512 for each tile
-enum class Form { rows, t32x32, t32x64, t128x64, t128x128_deep, t128x128, t192x256, t256x256 };
-struct Plan {
-    Form form;
-    double us;
-};
-struct Cost {
-    uint32_t rows, cols;      // of a tile
-    int a_cu;                 // workgroups that fit a CU
-    double fixed, per_k;      // us for a tile, and for 1000 reduction bytes of it
-    double more;              // added to per_k: for a CU's first tile (several a CU), once every CU has one (one a CU)
-    double places[4];         // per_k for each of places_of(), in relation to the first
-};
-constexpr Cost kCosts[] = {{16, 16, 4, 1.0, .85, 0, {1, .72, .82, 1.42}},
-                           {32, 32, 1, 2.3, .53, .27, {1, 1.17, 1.18, 1.75}},
-                           {32, 64, 2, 2.6, 1.25, 0, {1, 1.02, 1.11, 1.54}},
-                           {128, 64, 2, 2.7, 2.34, 0, {1, 1.51, 1.57, 2.50}},
-                           {128, 128, 1, 3.5, 2.5, .9, {1, 1.60, 1.72, 0}},  // four stages: not where fragments are moved
-                           {128, 128, 2, 4.4, 3.3, .5, {1, 1.41, 1.49, 2.05}},
-                           {192, 256, 1, 7.3, 7.3, 1.2, {1, 1.32, 1.37, 1.90}},
-                           {256, 256, 1, 9.9, 8.1, 1.6, {1, 1.38, 1.35, 1.95}}};
-Plan plan(uint32_t M, uint32_t N, int K, int places) {
-    Plan best{Form::rows, 1e30};
-    for (int f = 0; f < 8; ++f) {
-        const Cost& c = kCosts[f];
-        const int64_t tiles = (int64_t)((M + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
-        if (tiles > kMostTiles || ((f == (int)Form::t32x32 || f == (int)Form::t128x128_deep) && tiles > 256) ||
-            (f == (int)Form::t128x128_deep && places == 3))
-            continue;
-        double k = K * 1e-3 * c.places[places];
-        if (f == (int)Form::rows && M < 16) k *= .6 + .025 * M;  // rows of a that are read once
-        const double n = tiles <= 1024 ? (double)((tiles + 255) / 256) : tiles / 256. + .5;
-        const double fill = std::min(1.0, tiles / 256.0);
-        const double groups = tiles <= 1024 ? (double)((tiles + 256 * c.a_cu - 1) / (256 * c.a_cu)) : n / c.a_cu + .5;
-        const double us = c.a_cu > 1 ? c.fixed * groups + k * (c.per_k * n + c.more)
-                                        : n * (c.fixed + k * (c.per_k + c.more * fill * fill));
-        if (2.0 + us < best.us) best = Plan{(Form)f, 2.0 + us};  // 2: a launch
-    }
-    return best;
-}
-
 template <bool SHIFT>
 void start(Form f, const MatmulArgs& g) {
     switch (f) {
@@ -884,8 +801,8 @@ MatmulArgs rows_of(const MatmulArgs& g, int first, int count) {
     return r;
 }
 
-hipError_t launch(Form f, const MatmulArgs& g) {
-    places_of(g) < 3 ? start<false>(f, g) : start<true>(f, g);
+hipError_t launch(Form f, bool moved, const MatmulArgs& g) {
+    moved ? start<true>(f, g) : start<false>(f, g);
     return hipGetLastError();
 }
 
@@ -893,37 +810,13 @@ hipError_t launch(Form f, const MatmulArgs& g) {
 
 hipError_t launch_matmul_i8(const MatmulArgs& g) {
     if (g.M < 1 || g.M > GDR_I8_MAX_ROWS || g.N < 1 || g.K < 1 || g.K > GDR_MATMUL_I8_MAX_K) return hipErrorInvalidValue;
-    const int places = places_of(g);
-    if (!near(g.a_stride, g.M, g.K) || !near(g.w_stride, g.N, g.K)) {
-        // rows this far apart: the forms that address each row by itself
-        if ((g.M + 31LL) / 32 * ((g.N + 63LL) / 64) > kMostTiles) {
-            const int half = g.M / 2;
-            const hipError_t e = launch_matmul_i8(rows_of(g, 0, half));
-            return e == hipSuccess ? launch_matmul_i8(rows_of(g, half, g.M - half)) : e;
-        }
-        const Form f = plan(g.M, g.N, g.K, places).form;
-        return launch(f == Form::rows || f == Form::t32x32 ? f : Form::t32x64, g);
-    }
-    const Plan whole = plan(g.M, g.N, g.K, places);
-    // Rows that would cost a round of large tiles of their own go into a second launch, of smaller
-    // ones: those past a multiple of 256 (4097 x 12288 x 4096: 189 against 207 us), or past the last
-    // round in which every CU has a tile (6023 x 2692 x 7008: 134 against 185).  Where less than a
-    // seventh is expected to be saved the two launches were as often slower.
-    const int high = g.M / 256, wide = (g.N + 255) / 256;
-    const int heads[2] = {high * 256, (int)((int64_t)high * wide / 256 * 256 / wide * 256)};
-    Plan first{}, second{};
-    int head = 0;
-    double least = .85 * whole.us;
-    for (int h : heads) {
-        if (h < 1 || h >= g.M) continue;
-        const Plan a = plan(h, g.N, g.K, places), b = plan(g.M - h, g.N, g.K, places);
-        if (a.us + b.us < least) least = a.us + b.us, head = h, first = a, second = b;
-    }
-    if (head > 0) {
-        const hipError_t e = launch(first.form, rows_of(g, 0, head));
-        return e == hipSuccess ? launch(second.form, rows_of(g, head, g.M - head)) : e;
-    }
-    return launch(whole.form, g);
+    hipError_t e = hipErrorInvalidValue;
+    const Operands all{reinterpret_cast<uintptr_t>(g.a), reinterpret_cast<uintptr_t>(g.w), g.M, g.N, g.K, g.a_stride, g.w_stride};
+    launches(all, 0, [&](int first, int count, Form form, bool moved) {
+        e = launch(form, moved, rows_of(g, first, count));
+        return e == hipSuccess;
+    });
+    return e;
 }
 
 }  // namespace gdr
