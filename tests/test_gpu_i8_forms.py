@@ -65,3 +65,52 @@ def test_two_launches(M, N, K, dtype):
     gdr.matmul_i8(a, sa, w, sw, bias=b, out=room[1:M + 1])
     check(room[1:M + 1], size, b)
     assert bool((room[0] == 7.0).all()) and bool((room[M + 1] == 7.0).all())
+
+
+def splits(N):
+    """Ways to cut N columns: outputs of a layer, many of them inside one store of 4 or 8 columns at
+    the first column, in the middle and at the last one."""
+    third = N // 3 // 16 * 16
+    half = N // 2 | 1
+    return {"layer": (third, third, N - 2 * third),
+            "front": (3, 1, 1, 2, half, 1, 2, N - half - 10),
+            "back": (N - 18, 5, 1, 7, 2, 1, 1, 1),
+            "odd": (half - 6, N - half - 7, 13)}
+
+
+def check_splits(M, N, size, bias, dtype, call):
+    for way, cols in splits(N).items():
+        # side by side in one array that is written nowhere else, three columns apart
+        room = torch.full((M + 2, N + 3 * len(cols) + 2), 7.0, dtype=dtype, device="cuda")
+        at, parts = 1, []
+        for n in cols:
+            parts.append(room[1:M + 1, at:at + n])
+            at += n + 3
+        note(f"outputs {way} {M}x{N} {dtype}")
+        call(parts)
+        check(torch.cat(parts, 1), size, bias)
+        for p in parts:
+            p.fill_(7.0)
+        assert bool((room == 7.0).all()), way
+        # each dense, at the end of an array of its own
+        own = [torch.full((M * n + 5,), 7.0, dtype=dtype, device="cuda") for n in cols]
+        call([t[5:].view(M, n) for t, n in zip(own, cols)])
+        check(torch.cat([t[5:].view(M, n) for t, n in zip(own, cols)], 1), size, bias)
+        assert all(bool((t[:5] == 7.0).all()) for t in own), way
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", FORMS, ids=name)
+def test_outputs_that_end_inside_a_store(case, dtype):
+    form, moved, M, N, K, pad, off = case
+    a, sa, w, sw, bias, size = product(M, N, K, pad, off)
+    b = bias if dtype == F32 else None
+    check_splits(M, N, size, b, dtype, lambda out: gdr.matmul_i8(a, sa, w, sw, bias=b, out=out))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [t[:3] for t in TWO])
+def test_outputs_of_two_launches(M, N, K, dtype):
+    a, sa, w, sw, bias, size = product(M, N, K)
+    b = bias if dtype == F32 else None
+    check_splits(M, N, size, b, dtype, lambda out: gdr.matmul_i8(a, sa, w, sw, bias=b, out=out))
