@@ -128,3 +128,27 @@ def test_streams_side_by_side(D, dtype):
         assert torch.equal(a, b)
     before[:, D:2 * D] = want[2]
     assert torch.equal(wide, before)
+
+
+def test_capture_on_a_forked_stream():
+    """Calls given a stream that joined a capture, with new outputs: replays follow their inputs."""
+    M, D = 70, 512
+    x, r, nw, w, ws = inputs(M, D)
+    gdr.add_rmsnorm_i8(x, nw, residual=r)
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    note("capture on a forked stream")
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        q, s, h = gdr.add_rmsnorm_i8(x, nw, residual=r, stream=side)
+        y, z = gdr.matmul_i8(q, s, w, ws, out=(24, 40), out_dtype=F32, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for i in range(3):
+        x.copy_(inputs(M, D, seed=10 + i)[0])
+        g.replay()
+        torch.cuda.synchronize()
+        want = gdr.add_rmsnorm_i8(x, nw, residual=r)
+        y_want = gdr.matmul_i8(want[0], want[1], w, ws, out=(24, 40), out_dtype=F32)
+        for a, b in zip((q, s, h, y, z), (*want, *y_want)):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
