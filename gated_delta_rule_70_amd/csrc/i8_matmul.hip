@@ -5,9 +5,10 @@
 //
 // Forms, by how many outputs there are (plan() in i8_plan.h): 16 x 16 outputs by 8 waves that share the
 // reduction, without LDS staging; small tiles whose waves share the reduction; 128-wide tiles;
-// 192 x 256 and 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 9.7 us, 5.2 TB/s,
-// the rate of a large copy being 5.1.  At 32768 x 4096 x 4096 the chip is limited by power: 447 us,
-// 2460 TOP/s (the library's int8 product reaches 2070 on 8192^3).
+// 192 x 256 and 256 x 256 tiles.  At 1 x 12288 x 4096 what is read is the weights: 50 MB in 12.2 us from
+// memory, 4.1 TB/s (a large copy reaches 5.1), in 9.9 us from the last-level cache.  At
+// 32768 x 4096 x 4096 the chip is limited by power: 447 us, 2460 TOP/s (the library's int8 product
+// reaches 2070 on 8192^3).  Times are from one call to the next in a captured graph.
 #include "i8_launch.h"
 
 #include <type_traits>
@@ -249,11 +250,13 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(MatmulArgs g) {
 // copied from the aligned word that its first byte lies in, with one more word behind each stage's
 // 128 bytes, and a fragment is moved into place, by 0 to 3 bytes, as it is read from LDS.  Words
 // are read whole: the first and the last may begin before the operand or end behind it.
-// At 4096 x 4096 x K, 256 x 256 tiles: K = 4096 60 us; 4100, where a stage's bytes of a row lie in two
-// lines, 78; 4097, moved, 95 (through registers, at any alignment, 92; 128 x 64 tiles 215, registers 278).
+// At 4096 x 4096 x K, 256 x 256 tiles, operands from memory: K = 4096 64 us; 4100, where a stage's bytes
+// of a row lie in two lines, 80; 4097, moved, 98 (from the last-level cache 54, 63 and 83).  Rows
+// moved in registers on their way to LDS took 3 % less there, but 128 x 64 tiles 29 % more.
 // What bounds the 256 x 256 form: at 8192^3 the matrix cores are busy 74 % of the time at a clock of
-// 1.83 GHz; an order of issue with 68 % busy ran at 1.94 GHz and took the same time, so it is the
-// power that a product costs.  Tried and dropped (8192^3, 430 us): 32x32x32 products, 457;
+// 1.83 GHz (profiles/int8_product_counters.md); an order of issue with 68 % busy ran at 1.94 GHz and
+// took the same time, so it is the power that a product costs.  Tried and dropped (8192^3, against 430 us
+// in the same runs): 32x32x32 products, 457;
 // four waves of 128 x 128 each, a third fewer LDS reads but nothing to cover a wait, 477; 64-byte
 // stages, five deep, 621 (half lines cost as many requests as whole ones); touching lines two
 // stages ahead to have them in L2, 515; higher wave priority around the products, 519.
@@ -618,8 +621,8 @@ __global__ __launch_bounds__(WM* WN * 64) void matmul_tile_kernel(MatmulArgs g) 
 // workgroup; each wave makes a 32 x 32 block, and KG groups of waves share the reduction: a stage
 // is KG * 64 bytes of it, group k takes the k-th 64, and the groups' sums meet in LDS.  What bounds
 // these products is how fast a CU can bring its operands in, so the loop keeps STAGES - 1 stages
-// in flight.  32 x 12288 x 4096: 10.7 us, 4.8
-// TB/s; 128 x 4096 x 4096: 9.7 us, where each CU brings 393 KB in at 50 bytes a ns.
+// in flight.  32 x 12288 x 4096: 15.4 us with the weights from memory, 3.3 TB/s, 11.0 from the last-level
+// cache; 128 x 4096 x 4096: 11.4 and 8.7 us, where each CU brings 393 KB in at 34 and 45 bytes a ns.
 template <int BM, int BN, int KG, int STAGES, bool SHIFT, bool BF16>
 __global__ __launch_bounds__(BM / 32 * (BN / 32) * KG * 64) void matmul_small_kernel(MatmulArgs g) {
     constexpr int WN = BN / 32, WAVES = BM / 32 * WN * KG, NT = WAVES * 64;

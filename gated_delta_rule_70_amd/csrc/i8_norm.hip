@@ -5,9 +5,11 @@
 // rho = (mean s^2 + eps)^(-1/2), the code of the normed value t * rho at scale A * rho / 127 is
 // rint(127 t / A): rho cancels.  So the sum of squares and the maximum are reduced together,
 // the row stays in registers in between, and codes are stored after one reduction.  Bound by
-// memory: 32768 x 4096 bf16 with residual 156 us, 6.0 TB/s (a copy of 1 GiB reaches 5.1; part of
-// what is read is still in the last-level cache); 4097 tokens of 32 x 128 bf16 through the gated
-// norm 20.0 us, 4.2 TB/s, where the exponentials cost about as much time as the memory.
+// memory: 32768 x 4096 bf16 with residual 163 us from one call to the next, 5.8 TB/s (156 in a
+// kernel trace; a copy of 1 GiB reaches 5.1, and part of what is read here is still in the last-level
+// cache); 4097 tokens of 32 x 128 bf16 through the gated norm 20.0 us with inputs from memory, 4.2
+// TB/s (19.9 in a trace, 17.1 with inputs in the cache), where the exponentials cost about as much
+// time as the memory.
 #include "i8_launch.h"
 
 #include <type_traits>
@@ -366,16 +368,18 @@ dim3 grid_of(int rows) {
 // Threads for a row and groups for a thread: as many threads as the row fills with one or two groups
 // each, since a row is read and written once and what counts is loads in flight; groups beyond a
 // row's end cost time too.  A row of up to 1024 values by one wave (no barrier) pays once there are
-// rows enough to fill the chip with them.  us, threads x groups, bf16 with residual:
-//    8192 x  1024    64x2 15.1   64x4 16.3   256x1 16.0
-//   16384 x  2048    64x4 55.5  256x1 43.9   256x2 47.6
-//    4097 x  4096   256x2 25.6   64x8 45.6
-//    8192 x  8192   256x4 90.2  512x2 84.1  1024x1 89.1
-//    4096 x 16384  1024x2 86.1 1024x4 126.4
+// rows enough to fill the chip with them.  us from one call to the next, three sets of inputs in turn /
+// inputs from memory; threads x groups, bf16 with residual:
+//    8192 x  1024    64x2 15.7 / 19.0    64x4 16.5 / 20.2    256x1 15.9 / 19.1
+//   16384 x  2048    64x4 56.6 / 57.5   256x1 43.7 / 44.9    256x2 47.3 / 47.7
+//    4097 x  4096   256x2 26.6 / 26.9   512x1 25.9 / 26.1     64x8 45.5 / 45.9
+//    8192 x  8192   256x4 90.3 / 92.2   512x2 84.0 / 84.4   1024x1 90.3 / 92.8
+//    4096 x 16384  1024x2 86.8 / 88.3  1024x4 132 / 133
 // and in the gated norm, bf16:
-//    4097 x 32 x 128  512x1 16.4  256x2 17.5  1024x1 26.9
-//    8000 x 48 x 128  512x2 56.1 1024x1 60.8   (4097 x 64 x 128 fp32 56.1 and 53.7)
-//    4097 x 128 x 128 1024x2 83.3 1024x4 127.6
+//    4097 x  32 x 128   512x1 17.1 / 20.0   256x2 17.5 / 20.4  1024x1 27.6 / 28.6
+//    8000 x  48 x 128   512x2 56.4 / 59.6  1024x1 58.5 / 60.5
+//    4097 x  64 x 128   512x2 58.0 / 58.9  1024x1 54.9 / 55.9   (fp32)
+//    4097 x 128 x 128  1024x2 83.6 / 85.3  1024x4 129 / 129
 template <typename TX, typename TW, typename T>
 void add_rmsnorm_typed(const NormArgs& a) {
     auto go = [&](auto tpr, auto nv) {

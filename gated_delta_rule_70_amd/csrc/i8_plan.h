@@ -29,28 +29,32 @@ inline bool near(int64_t stride, int rows, int K) { return rows == 1 || stride <
 // and power.  Where rows do not begin at whole lines, the 128 bytes of a stage lie in two lines and
 // all forms but those that read 256 or more in a row take longer; fragments that have to be moved into
 // place cost more again.  The constants were fitted to 11000 random sizes (17 to 32768 rows, 128 to
-// 12288 columns, reductions of 256 to 8192); the form so chosen takes 0.6 % longer than the fastest
-// on average, 14 % at the 99th percentile.
-// M x N x K in us, rows beginning at whole lines:
-//                        32x64  128x64  128x128 (4 / 2 stages)  192x256  256x256
-//      32 x 12288 x 4096  14.2    18.6     20.0 /  30.9           40.8     47.3
-//     128 x  4096 x 4096   8.5    12.3     15.5 /  21.9           32.4     38.1
-//     512 x  4096 x 4096  22.6    13.7     16.2 /  22.4           33.2     39.6
-//    1024 x  4096 x 4096  47.0    23.0     20.0 /  25.1           34.4     40.2
-//     512 x 12288 x 4096  77.3    43.6     44.2 /  40.3           46.6     53.3
-//    2048 x  4096 x 4096  99.1    50.4     43.0 /  38.3           47.2     50.7
-//    4096 x  4096 x 1024  73.3    32.4          /  26.0           28.9     21.8
-//    8192 x  8192 x  512          99.8          /  77.9           64.0     68.6
-//    1691 x  5760 x 4096 108.6    61.7          /  63.3           47.0     51.7
-//    3000 x  4096 x 4096 133.3    69.6          /  61.3           50.5     56.0
-//    8192 x  2048 x 8192 334.1   185.9          / 137.1          148.3    111.0
-// Fewer outputs, 16x16 without LDS / 32x32 / 32x64 (weights from memory; from the last-level cache):
-//       1 x  4096 x 4096  5.1 /  5.9 /  7.5    (5.2 / 5.8 / 7.5)
-//       1 x 12288 x 4096 11.2 /      / 12.8    (9.6 /     / 9.9)
-//      16 x  8192 x 4096  9.8 /  8.3 / 10.3
-//      64 x  4096 x 4096 16.3 /  6.7 /  8.2
-//     178 x  1280 x 3712 16.1 /  7.0 /  8.6
-//     256 x  1024 x 8192 29.8 /  9.2 / 12.6
+// 12288 columns, reductions of 256 to 8192), on operands that stay in the last-level cache; the form so
+// chosen takes 0.6 % longer than the fastest on average, 14 % at the 99th percentile.  Below 17 rows
+// they are carried on, with one factor for rows of a that the first form reads once, set on single rows
+// of 4096 and 12288 columns.
+// M x N x K in us from one call to the next, rows beginning at whole lines; operands in the last-level
+// cache / from memory:
+//                           32x64        128x64     128x128 deep     128x128       192x256       256x256
+//      32 x 12288 x 4096  11.0 / 15.4  12.6 / 18.8  15.1 / 20.5  22.1 / 31.4   32.0 / 40.9   37.8 / 48.1
+//     128 x  4096 x 4096   8.7 / 11.4  12.8 / 18.5  15.8 / 22.7  22.4 / 31.7   33.0 / 44.5   39.0 / 48.7
+//     512 x  4096 x 4096  22.3 / 28.5  14.1 / 18.3  16.4 / 22.1  22.7 / 31.4   33.7 / 45.1   40.3 / 52.4
+//    1024 x  4096 x 4096  43.6 / 55.0  23.1 / 28.4  20.5 / 23.8  24.4 / 32.6   34.4 / 43.5   40.9 / 52.9
+//     512 x 12288 x 4096  56.7 / 77.2  34.0 / 43.8               28.7 / 40.9   35.6 / 47.1   41.6 / 54.1
+//    2048 x  4096 x 4096  86.8 / 98.4  43.6 / 51.4               34.2 / 39.2   36.9 / 48.0   42.1 / 54.9
+//    4096 x  4096 x 1024  67.9 / 72.9  29.9 / 37.8               24.4 / 29.7   28.6 / 31.1   21.5 / 24.1
+//    8192 x  8192 x  512                101 /  104               78.6 / 78.4   62.9 / 64.9   72.4 / 72.1
+//    1691 x  5760 x 4096  99.1 /  107  53.5 / 61.5               52.3 / 64.2   38.8 / 46.8   42.2 / 52.6
+//    3000 x  4096 x 4096   125 /  131  64.5 / 70.6               54.4 / 59.1   43.3 / 51.2   45.3 / 56.0
+//    8192 x  2048 x 8192   324 /  332   181 /  183                132 /  135    142 /  151    109 /  109
+// Fewer outputs:            16x16        32x32        32x64
+//       1 x  4096 x 4096   5.5 /  6.2   6.2 /  8.3   7.9 / 10.3
+//       1 x 12288 x 4096  10.0 / 12.2               10.3 / 14.1
+//       2 x 12288 x 4096  10.2 / 12.4               10.4 / 14.1
+//      16 x  8192 x 4096   9.9 / 12.5   8.4 / 10.3   8.4 / 13.1
+//      64 x  4096 x 4096  16.9 / 17.4   6.9 /  9.2   8.4 / 11.4
+//     178 x  1280 x 3712  15.7 / 16.0   6.6 /  7.3   8.4 /  9.0
+//     256 x  1024 x 8192  30.7 / 31.1   9.1 / 11.7  12.5 / 16.8
 // 32x32 tiles serve where each CU has at most one: 3900 random sizes of that kind take 6 to 10 %
 // longer without them (the form chosen 0.6 % longer than the fastest).
 constexpr int64_t kMostTiles = (1 << 23) - 1;  // a launch has fewer than 2^32 threads, 512 for each tile

@@ -17,11 +17,12 @@
  * Conventions (those of gdr.h unless said otherwise): device pointers; the caller owns every
  * buffer; work is enqueued on `stream` and the call returns without waiting; every argument
  * check runs on the host before any HIP call, so a call that is refused has enqueued nothing
- * (one that returns GDR_ERR_HIP may have); statuses are gdr_status; results are bitwise reproducible (no atomics).  rows == 0
- * is a valid call that does nothing (pointers may then be NULL).  Strides are in elements,
- * between rows; within a row values are contiguous.  Pointers need only their element type's
- * alignment; the product is fastest where a, w and their row strides are multiples of 128 bytes,
- * then of 4.  It reads the aligned words of 4 bytes that hold an operand's first and last bytes whole.
+ * (one that returns GDR_ERR_HIP may have); statuses are gdr_status; results are bitwise
+ * reproducible (no atomics).  rows == 0 is a valid call that does nothing (pointers may then be
+ * NULL).  Strides are in elements, between rows; within a row values are contiguous.  Pointers
+ * need only their element type's alignment; the product is fastest where a, w and their row
+ * strides are multiples of 128 bytes, then of 4.  It reads the aligned words of 4 bytes that hold
+ * an operand's first and last bytes whole.
  */
 #ifndef GDR_I8_H
 #define GDR_I8_H
@@ -76,7 +77,9 @@ int gdr_add_rmsnorm_i8(const gdr_norm_dims* dims, const void* x, const void* res
  *   A / 127                                                -> scale  [rows]             fp32
  * n is computed in fp32 (sums of squares in fp64), so a value within fp32 rounding of the
  * border between two codes may take either, and a gate below -87, where silu is less than 1e-35,
- * may count as closed.  Empty and non-finite rows as above.
+ * may count as closed.  The range is fp32's too: weight times silu counts as infinite beyond it,
+ * and a token of nothing above 1e-38 has the bits that fp32 has there.  Empty and non-finite rows
+ * as above.
  * out_stride is ignored.
  */
 int gdr_gated_rmsnorm_i8(const gdr_norm_dims* dims, const void* o, const void* gate, const void* weight,
