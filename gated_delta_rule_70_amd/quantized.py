@@ -162,18 +162,28 @@ def _torch_stream(stream):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
-def _empty(shape, dtype, like, stream):
-    """A new tensor on the GPU of ``like``, of memory that ``stream`` may write at once.  What the
-    allocator takes from the current stream's memory may still be in use by work queued there, which
-    another stream does not wait for; so that other stream's own memory is taken, and kept until the
-    current one, on which the caller will read it, is done too."""
-    if stream is None or not like.is_cuda or _handle(stream) == _raw_stream(like.get_device()):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    here = torch.cuda.current_stream(like.device)
-    with torch.cuda.stream(_torch_stream(stream)):
-        t = torch.empty(shape, dtype=dtype, device=like.device)
-    t.record_stream(here)
-    return t
+def _elsewhere(stream, t):
+    """Whether ``stream`` is another one than the current stream of t's GPU."""
+    return t.is_cuda and _handle(stream) != _raw_stream(t.get_device())
+
+
+def _on(stream, call, *args):
+    """``call(*args)``, which makes new outputs, with ``stream`` as the current one, so that they come
+    from that stream's memory: what the allocator takes from the current stream's may still be in use
+    by work queued there, which another stream does not wait for.  They are kept until the current
+    stream, on which the caller will read them, is done too."""
+    here, there = torch.cuda.current_stream(), _torch_stream(stream)
+    torch.cuda.set_stream(there)
+    try:
+        outs = call(*args)
+    finally:
+        torch.cuda.set_stream(here)
+    for group, user in ((args, there), ((outs,), here)):
+        for t in group:
+            for u in t if isinstance(t, (tuple, list)) else (t,):
+                if isinstance(u, torch.Tensor):
+                    u.record_stream(user)
+    return outs
 
 
 def _rows(t, name, tail=1):
@@ -199,9 +209,9 @@ def _rows(t, name, tail=1):
     return step if row is None or t.numel() == 0 else row
 
 
-def _out(t, name, shape, dtype, like, stream):
+def _out(t, name, shape, dtype, device):
     if t is None:
-        return _empty(shape, dtype, like, stream)
+        return torch.empty(shape, dtype=dtype, device=device)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -236,6 +246,8 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
             if status:
                 _fail(status)
             return q, scale, out_residual
+    elif (q is None or scale is None or out_residual is None and residual is not None) and _elsewhere(stream, x):
+        return _on(stream, add_rmsnorm_i8, x, weight, residual, eps, q, scale, out_residual)
     shape, dtype = x.shape, x.dtype
     if not shape or shape[-1] < 1:
         raise ValueError(f"x must be [..., D], got {list(shape)}")
@@ -261,7 +273,7 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
             raise TypeError(f"residual must be {dtype}, got {residual.dtype}")
         r_stride = D if residual.is_contiguous() else _rows(residual, "residual")
         if out_residual is None:
-            out_residual = _empty(shape, dtype, x, stream)
+            out_residual = torch.empty(shape, dtype=dtype, device=x.device)
         if out_residual.shape != shape:
             raise ValueError(f"out_residual must be {list(shape)}, got {list(out_residual.shape)}")
         if out_residual.dtype is not dtype:
@@ -269,9 +281,9 @@ def add_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=No
         out_stride = D if out_residual.is_contiguous() else _rows(out_residual, "out_residual")
     lead = shape[:-1]
     if q is None or q.shape != shape or q.dtype is not _I8 or not q.is_contiguous():
-        q = _out(q, "q", shape, _I8, x, stream)
+        q = _out(q, "q", shape, _I8, x.device)
     if scale is None or scale.shape != lead or scale.dtype is not _F32 or not scale.is_contiguous():
-        scale = _out(scale, "scale", lead, _F32, x, stream)
+        scale = _out(scale, "scale", lead, _F32, x.device)
     dims = _NORM.pack(scale.numel(), 1, D, xc, 0, _CODE[wt], eps if 0 <= eps <= _F32_MAX else _eps(eps),
                       D if x.is_contiguous() else _rows(x, "x"), r_stride, out_stride)
     s = _stream(stream, x.get_device(), _NORM_NAMES, (weight, residual, q, scale, out_residual, x))
@@ -296,6 +308,8 @@ def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, str
             if status:
                 _fail(status)
             return q, scale
+    elif (q is None or scale is None) and _elsewhere(stream, o):
+        return _on(stream, gated_rmsnorm_i8, o, gate, weight, eps, q, scale)
     shape = o.shape
     if len(shape) < 2:
         raise ValueError(f"o must be [..., HV, dv], got {list(shape)}")
@@ -315,9 +329,9 @@ def gated_rmsnorm_i8(o, gate, weight, eps: float = 1e-6, q=None, scale=None, str
     D = H * V
     qshape = (*lead, D)
     if q is None or q.shape != qshape or q.dtype is not _I8 or not q.is_contiguous():
-        q = _out(q, "q", qshape, _I8, o, stream)
+        q = _out(q, "q", qshape, _I8, o.device)
     if scale is None or scale.shape != lead or scale.dtype is not _F32 or not scale.is_contiguous():
-        scale = _out(scale, "scale", lead, _F32, o, stream)
+        scale = _out(scale, "scale", lead, _F32, o.device)
     dims = _NORM.pack(scale.numel(), H, V, oc, gc, wc, eps if 0 <= eps <= _F32_MAX else _eps(eps),
                       D if o.is_contiguous() else _rows(o, "o", 2),
                       D if gate.is_contiguous() else _rows(gate, "gate", 2), 0)
@@ -349,6 +363,8 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
             if status:
                 _fail(status)
             return out if isinstance(out, torch.Tensor) else tuple(out)
+    elif not isinstance(out, torch.Tensor) and _elsewhere(stream, a):
+        return _on(stream, matmul_i8, a, a_scale, w, w_scale, bias, out, out_dtype)
     shape, wshape = a.shape, w.shape
     if not shape or len(wshape) != 2 or shape[-1] != wshape[1]:
         raise ValueError(f"a must be [..., K] and w [N, K], got {list(shape)} and {list(wshape)}")
@@ -372,7 +388,7 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
         raise ValueError(f"1 to {MATMUL_I8_MAX_OUT} outputs are supported, got {n}")
     for i, t in enumerate(outs):
         if isinstance(t, int) and t > 0:
-            outs[i] = _empty((*lead, t), out_dtype, a, stream)
+            outs[i] = torch.empty(*lead, t, dtype=out_dtype, device=a.device)
     matrix = len(lead) == 1
     dtype, cols, strides, ptrs = None, [], [], []
     for t in outs:

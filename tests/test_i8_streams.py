@@ -1,8 +1,6 @@
 """Streams and memory of the 8-bit operators' binding, on the host: tensors that say they are on a
 GPU, an allocator that notes from which stream's memory a tensor is taken and which streams it is
 kept for, and a library that does nothing."""
-import contextlib
-
 import pytest
 import torch
 
@@ -37,26 +35,24 @@ class NoLibrary:
 def machine(monkeypatch):
     active, empty = [HERE], torch.empty
 
-    @contextlib.contextmanager
-    def on(s):
-        active.append(s.cuda_stream)
-        yield
-        active.pop()
+    def set_stream(s):
+        active[0] = s.cuda_stream
 
     def take(*a, **kw):
         t = empty(*a, **kw).as_subclass(Gpu)
-        t.taken_from = active[-1]
+        t.taken_from = active[0]
         return t
 
     monkeypatch.setattr(torch, "empty", take)
-    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "set_stream", set_stream)
     # torch's, given the handle 0, is a new stream
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: Stream(handle or NEW))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: Stream(0))
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(active[-1]))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(active[0]))
     monkeypatch.setattr(qz, "_current_device", lambda: 0)
-    monkeypatch.setattr(qz, "_raw_stream", lambda dev: active[-1])
+    monkeypatch.setattr(qz, "_raw_stream", lambda dev: active[0])
     monkeypatch.setattr(qz, "_L", NoLibrary)
+    monkeypatch.setattr(qz, "_B", qz._NoBinding)
 
 
 def gpu(*shape, dtype=torch.float32):
@@ -84,6 +80,14 @@ def test_new_outputs_on_another_stream(call, stream, machine):
         assert t.taken_from == THERE and HERE in t.kept_for
 
 
+@pytest.mark.parametrize("given", [False, True], ids=["new", "given"])
+def test_inputs_are_kept_for_the_stream(given, machine):
+    a, sa, w, sw, b = i8(3, 64), gpu(3), i8(20, 64), gpu(20), gpu(20)
+    outs = [gpu(3, 8), gpu(3, 12)] if given else (8, 12)
+    gdr.matmul_i8(a, sa, w, sw, bias=b, out=outs, stream=THERE)
+    assert all(THERE in t.kept_for for t in (a, sa, w, sw, b, *(outs if given else ())))
+
+
 @pytest.mark.parametrize("call", CALLS)
 @pytest.mark.parametrize("stream", [HERE, Stream(HERE)], ids=["handle", "stream"])
 def test_new_outputs_on_the_current_stream(call, stream, machine):
@@ -95,6 +99,18 @@ def test_given_tensors_on_another_stream(machine):
     x, w, r, q, s, o = gpu(3, 64), gpu(64), gpu(3, 64), i8(3, 64), gpu(3), gpu(3, 64)
     gdr.add_rmsnorm_i8(x, w, residual=r, q=q, scale=s, out_residual=o, stream=THERE)
     assert all(t.kept_for == (THERE,) for t in (x, w, r, q, s, o))
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_current_stream_stays(call, machine):
+    CALLS[call](THERE)
+    assert torch.cuda.current_stream().cuda_stream == HERE
+
+
+def test_the_current_stream_stays_after_a_refusal(machine):
+    with pytest.raises(ValueError, match="weight must be"):
+        gdr.add_rmsnorm_i8(gpu(3, 64), gpu(65), stream=THERE)
+    assert torch.cuda.current_stream().cuda_stream == HERE
 
 
 def test_handle_of_the_default_stream(machine):
