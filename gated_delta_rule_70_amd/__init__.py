@@ -16,7 +16,9 @@ fp32; o ``[B,T,HV,dv]`` fp32, or bf16 with ``out_dtype=torch.bfloat16`` (or a bf
 passed in): every entry point then stores each fp32 output rounded to nearest even.
 
 The projections on either side of the delta rule, in 8-bit integers, are in
-:mod:`.quantized`: ``add_rmsnorm_i8``, ``matmul_i8`` and ``gated_rmsnorm_i8``.
+:mod:`.quantized`: ``add_rmsnorm_i8``, ``matmul_i8`` and ``gated_rmsnorm_i8``.  The operators in front
+of a recurrence and beside it are in :mod:`.layer`: ``causal_conv``, ``qk_norm_rope`` and
+``selective_scan``, with ``causal_conv_step`` and ``selective_scan_step`` for single tokens.
 """
 from __future__ import annotations
 
@@ -25,7 +27,9 @@ import os
 
 import torch
 
-from . import quantized
+from . import layer, quantized
+from .layer import (causal_conv, causal_conv_step, qk_norm_rope, rope_table, selective_scan,
+                    selective_scan_step)
 from .quantized import add_rmsnorm_i8, gated_rmsnorm_i8, matmul_i8, quantize_rows_i8
 
 __all__ = ["decode_step", "fused_recurrent", "chunk_prefill", "chunk_prefill_noalloc", "forward",
@@ -33,7 +37,9 @@ __all__ = ["decode_step", "fused_recurrent", "chunk_prefill", "chunk_prefill_noa
            "NOALLOC_SCRATCH_BYTES", "VARLEN_MAX_SEQS",
            "workspace_bytes", "GdrError", "lib", "Dims", "LIB_PATH", "ABI_VERSION",
            "RECURRENT_MAX_T", "TREE_MAX_T", "O_BF16",
-           "add_rmsnorm_i8", "gated_rmsnorm_i8", "matmul_i8", "quantize_rows_i8"]
+           "add_rmsnorm_i8", "gated_rmsnorm_i8", "matmul_i8", "quantize_rows_i8",
+           "causal_conv", "causal_conv_step", "qk_norm_rope", "rope_table", "selective_scan",
+           "selective_scan_step"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdr.so")
 ABI_VERSION = 8
@@ -117,6 +123,7 @@ def _bind(L):
     L.gdr_fused_recurrent_varlen.restype = ctypes.c_int
     L.gdr_fused_recurrent_varlen.argtypes = [ctypes.POINTER(Dims)] + [_VP] * 10
     quantized.bind(L)
+    layer.bind(L)
 
 
 def _check(status: int):

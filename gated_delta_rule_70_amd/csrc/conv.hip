@@ -1,0 +1,234 @@
+// Short causal convolution of each channel over time (gdr_causal_conv).
+//
+// y[t][d] = act(bias[d] + sum_j w[d][j] x[t - (W - 1) + j][d]).  Each thread holds eight channels'
+// taps and the window of the last W - 1 rows in registers and walks down the rows, so x is read once
+// (and W - 1 rows again for each tile of rows) and y written once: bound by memory.
+//
+// The first W - 1 tokens of a sequence, whose windows reach into its state, and the new state are one
+// thread's work for each sequence and channel group ("heads"); all other rows need nothing but x
+// ("tiles").  So a state can be replaced in place, its only reader being its writer, and a single
+// token for each sequence is the heads' part alone.
+#include "layer_launch.h"
+
+#include <type_traits>
+
+#include "row_device.h"
+
+namespace gdr {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 16;  // rows of a tile, at most 64
+constexpr int kUnroll = 4;
+
+struct ConvGroups {
+    int groups;                           // of eight channels; an output's last one may have fewer
+    int first[GDR_CONV_MAX_OUT + 1];      // first group of each output
+    int64_t head_blocks, block0, col_waves;  // col_waves: waves across the channels
+};
+
+// A thread's channels: the output, their place in it, and in x.
+struct Cols {
+    int out, at, channel, n;
+};
+__device__ __forceinline__ Cols cols_of(const ConvArgs& a, const ConvGroups& c, int g) {
+    int i = 0;
+    while (i + 1 < a.n_out && g >= c.first[i + 1]) ++i;
+    const int at = (g - c.first[i]) * 8;
+    return Cols{i, at, a.begin[i] + at, a.begin[i + 1] - a.begin[i] - at};
+}
+
+template <typename TW, int W, bool PART>
+struct Taps {
+    float w[W][8], bias[8];
+    __device__ __forceinline__ void load(const ConvArgs& a, const Cols& c) {
+        const TW* p = static_cast<const TW*>(a.w) + (int64_t)c.channel * W;
+        // the 8 W values of eight channels, in W groups of 8
+        float v[W][8];
+#pragma unroll
+        for (int j = 0; j < W; ++j) load8<PART>(p + 8 * j, c.n * W - 8 * j, v[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = v[(i * W + j) / 8][(i * W + j) % 8];
+        if (a.bias) {
+            load8<PART>(static_cast<const TW*>(a.bias) + c.channel, c.n, bias);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bias[i] = 0.f;
+        }
+    }
+    // f: the window's W rows, oldest first
+    template <typename TX>
+    __device__ __forceinline__ void store(const ConvArgs& a, const Cols& c, int64_t row, const float (*f)[8], const TX*) const {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float s = bias[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) s = __builtin_fmaf(w[j][i], f[j][i], s);
+            y[i] = a.silu ? silu(s) : s;
+        }
+        store8<PART>(static_cast<TX*>(a.out[c.out]) + row * a.out_stride[c.out] + c.at, c.n, y);
+    }
+};
+
+template <typename TX, typename TW, int W, bool PART>
+__device__ __forceinline__ void head(const ConvArgs& a, const ConvGroups& c, int64_t item) {
+    if (item >= (int64_t)a.B * c.groups) return;
+    const int seq = (int)(item / c.groups);
+    const Cols col = cols_of(a, c, (int)(item % c.groups));
+    int64_t first = (int64_t)seq * a.T;
+    int len = a.T;
+    if (a.cu) {
+        const Span s = packed_span(a.cu, seq, a.T);
+        first = s.first, len = s.count;
+    }
+    constexpr int P = W - 1;
+    float f[2 * P][8];  // the state's rows, then the sequence's first ones
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        if (a.state)
+            load8<PART>(static_cast<const TX*>(a.state) + ((int64_t)seq * P + j) * a.D + col.channel, col.n, f[j]);
+        else
+            for (int i = 0; i < 8; ++i) f[j][i] = 0.f;
+        if (j < len)
+            load8<PART>(static_cast<const TX*>(a.x) + (first + j) * a.x_stride + col.channel, col.n, f[P + j]);
+        else
+            for (int i = 0; i < 8; ++i) f[P + j][i] = 0.f;
+    }
+    if (a.out_state) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {  // the last P rows of state and x: row len + j of both
+            float v[8];
+            if (len >= P) {
+                load8<PART>(static_cast<const TX*>(a.x) + (first + len - P + j) * a.x_stride + col.channel, col.n, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = f[j][i];
+#pragma unroll
+                    for (int l = 1; l < P; ++l)
+                        if (len == l) v[i] = f[j + l][i];
+                }
+            }
+            store8<PART>(static_cast<TX*>(a.out_state) + ((int64_t)seq * P + j) * a.D + col.channel, col.n, v);
+        }
+    }
+    if (len < 1) return;
+    Taps<TW, W, PART> taps;
+    taps.load(a, col);
+#pragma unroll
+    for (int t = 0; t < P; ++t)
+        if (t < len) taps.store(a, col, first + t, f + t, static_cast<const TX*>(nullptr));
+}
+
+// Which of the tile's rows have their whole window in their own sequence.
+template <int W>
+__device__ __forceinline__ uint64_t whole_windows(const ConvArgs& a, int r0) {
+    const int lane = threadIdx.x & 63, r = r0 + lane;
+    bool ok = lane < kTile && r < a.rows;
+    if (ok && !a.cu) {
+        ok = r % a.T >= W - 1;
+    } else if (ok) {
+        int lo = 0, hi = a.B - 1;  // the last sequence that begins at or before r
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.cu[mid] <= r)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const Span s = packed_span(a.cu, lo, a.T);
+        ok = r - s.first >= W - 1 && r - s.first < s.count;
+    }
+    return __ballot(ok);
+}
+
+template <typename TX, typename TW, int W, bool PART>
+__device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int64_t wave) {
+    const int64_t t = wave / c.col_waves;
+    const int64_t row0 = t * kTile;
+    if (row0 >= a.rows) return;
+    const int r0 = (int)row0;
+    const uint64_t whole = whole_windows<W>(a, r0);
+    const int g = (int)(wave % c.col_waves) * 64 + (threadIdx.x & 63);
+    if (whole == 0 || g >= c.groups) return;
+    const Cols col = cols_of(a, c, g);
+    Taps<TW, W, PART> taps;
+    taps.load(a, col);
+    const TX* x = static_cast<const TX*>(a.x) + col.channel;
+    float f[W - 1 + kUnroll][8];
+    auto load = [&](int r, float(&v)[8]) {
+        if (r >= 0 && r < a.rows) {
+            load8<PART>(x + r * a.x_stride, col.n, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load(r0 - (W - 1) + j, f[j]);
+#pragma unroll 1
+    for (int k = 0; k < kTile; k += kUnroll) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) load(r0 + k + u, f[W - 1 + u]);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (whole >> (k + u) & 1) taps.store(a, col, (int64_t)r0 + k + u, f + u, static_cast<const TX*>(nullptr));
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[j][i] = f[kUnroll + j][i];
+    }
+}
+
+template <typename TX, typename TW, int W, bool PART>
+__global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvArgs a, ConvGroups c) {
+    const int64_t b = c.block0 + blockIdx.x;
+    if (b < c.head_blocks)
+        head<TX, TW, W, PART>(a, c, b * kThreads + threadIdx.x);
+    else
+        tile<TX, TW, W, PART>(a, c, (b - c.head_blocks) * (kThreads / 64) + threadIdx.x / 64);
+}
+
+template <typename TX, typename TW, int W>
+hipError_t launch(const ConvArgs& a) {
+    ConvGroups c{};
+    bool part = false;
+    for (int i = 0; i < a.n_out; ++i) {
+        const int n = a.begin[i + 1] - a.begin[i];
+        part |= n % 8 != 0;
+        c.first[i] = c.groups;
+        c.groups += (n + 7) / 8;
+    }
+    for (int i = a.n_out; i <= GDR_CONV_MAX_OUT; ++i) c.first[i] = c.groups;
+    c.col_waves = (c.groups + 63) / 64;
+    c.head_blocks = ((int64_t)a.B * c.groups + kThreads - 1) / kThreads;
+    const bool tiles = a.rows > 0 && a.T >= W;  // some sequence may be longer than its head
+    const int64_t waves = tiles ? ((int64_t)a.rows + kTile - 1) / kTile * c.col_waves : 0;
+    const int64_t blocks = c.head_blocks + (waves + kThreads / 64 - 1) / (kThreads / 64);
+    return by_blocks(blocks, kThreads, [&](int64_t first, unsigned count) {
+        c.block0 = first;
+        if (part)
+            hipLaunchKernelGGL((causal_conv_kernel<TX, TW, W, true>), dim3(count), dim3(kThreads), 0, a.stream, a, c);
+        else
+            hipLaunchKernelGGL((causal_conv_kernel<TX, TW, W, false>), dim3(count), dim3(kThreads), 0, a.stream, a, c);
+    });
+}
+
+}  // namespace
+
+hipError_t launch_causal_conv(const ConvArgs& a) {
+    if (a.B < 1 || a.D < 1 || a.n_out < 1 || a.n_out > GDR_CONV_MAX_OUT) return hipErrorInvalidValue;
+    auto width = [&](auto x, auto w) {
+        using TX = decltype(x);
+        using TW = decltype(w);
+        return a.W == 2 ? launch<TX, TW, 2>(a) : a.W == 3 ? launch<TX, TW, 3>(a) : a.W == 4 ? launch<TX, TW, 4>(a) : hipErrorInvalidValue;
+    };
+    if (!a.bf16) return width(float{}, float{});
+    return a.w_bf16 ? width(bf16_t{}, bf16_t{}) : width(bf16_t{}, float{});
+}
+
+}  // namespace gdr

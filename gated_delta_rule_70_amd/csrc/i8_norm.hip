@@ -14,67 +14,13 @@
 
 #include <type_traits>
 
-#include "gdr_device.h"
+#include "row_device.h"
 
 namespace gdr {
 
 namespace {
 
 constexpr float kFltMax = 3.402823466e38f;
-
-// Values 0 .. 7 at p as fp32, zeros from n on.  Vector loads at any alignment of the elements: the
-// hardware takes them unaligned, so only a row's last group of fewer than 8 (PART: there may be
-// one) goes value by value.
-template <bool PART>
-__device__ __forceinline__ void load8(const bf16_t* p, int n, float (&v)[8]) {
-    if (!PART || n >= 8) {
-        u32x4 u;
-        __builtin_memcpy(&u, p, 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(u[j] << 16);
-            v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f32(p[j]) : 0.f;
-    }
-}
-template <bool PART>
-__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
-    if (!PART || n >= 8) {
-        __builtin_memcpy(v, p, 32);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.f;
-    }
-}
-__device__ __forceinline__ float round_to(float x, const float*) { return x; }
-__device__ __forceinline__ float round_to(float x, const bf16_t*) {
-    return static_cast<float>(static_cast<__bf16>(x));
-}
-template <bool PART>
-__device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
-    if (!PART || n >= 8) {
-        __builtin_memcpy(p, v, 32);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = v[j];
-    }
-}
-template <bool PART>
-__device__ __forceinline__ void store8(bf16_t* p, int n, const float (&v)[8]) {
-    const u32x2 a = bf16x4_bits(f32x4{v[0], v[1], v[2], v[3]}), b = bf16x4_bits(f32x4{v[4], v[5], v[6], v[7]});
-    const u32x4 u = {a[0], a[1], b[0], b[1]};
-    if (!PART || n >= 8) {
-        __builtin_memcpy(p, &u, 16);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) p[j].bits = (uint16_t)(u[j / 2] >> (j % 2 * 16));
-    }
-}
 
 // Rounding to whole numbers, ties to even, by one addition: x + kRound (|x| < 2^22) has the whole
 // number's low bits at its end.
@@ -99,29 +45,6 @@ __device__ __forceinline__ void store_codes(int8_t* q, int n, u32x2 c) {
         for (int j = 0; j < 8; ++j)
             if (j < n) q[j] = (int8_t)(c[j / 4] >> (j % 4 * 8));
     }
-}
-
-// Sum over the V / 8 neighbouring lanes (4, 8 or 16) that hold a head's V values, in all of them.
-template <int CTRL>
-__device__ __forceinline__ double dpp_mov64(double x) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double sum_head(double x, int V) {
-    x += dpp_mov64<0xB1>(x);               // quad_perm [1,0,3,2]
-    x += dpp_mov64<0x4E>(x);               // quad_perm [2,3,0,1]
-    if (V > 32) x += dpp_mov64<0x141>(x);  // row_half_mirror: the other quad of 8 lanes
-    if (V > 64) x += dpp_mov64<0x140>(x);  // row_mirror: the other half of 16 lanes
-    return x;
-}
-
-// 1 / sqrt(m) in fp64: the hardware's estimate and one Newton step.  Zero for m = 0.
-__device__ __forceinline__ double rsqrt64(double m) {
-    const double r = __builtin_amdgcn_rsq(m);
-    const double e = __builtin_fma(-m * r, r, 1.0);
-    return m == 0. ? 0. : __builtin_fma(r * 0.5, e, r);
 }
 
 // Sum and maximum of TPR consecutive threads (64, or the whole workgroup), in all of them.
@@ -276,16 +199,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
         const int e = (i * TPR + tid) * 8;
         if (e < D) store_codes<PART>(q + e, D - e, pack8(y, zero));
     }
-}
-
-// exp(-z) to about 1 ulp: the product with log2(e) is taken in two parts, so that the error of
-// the exponent does not grow with |z|.  Beyond |z| = 200 the result stays infinity or zero.
-__device__ __forceinline__ float exp_neg(float z) {
-    z = __builtin_amdgcn_fmed3f(z, -200.f, 200.f);
-    constexpr float kL = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;  // log2(e), high and low
-    const float p = -z * kL;
-    const float e = __builtin_fmaf(-z, kL, -p) + -z * kLo;
-    return __builtin_amdgcn_exp2f(p) * __builtin_fmaf(e, 0.6931471805599453f, 1.f);
 }
 
 // Norm per value head (V values, V/8 neighbouring threads), times weight and silu(gate), and

@@ -178,12 +178,19 @@ def _on(stream, call, *args):
         outs = call(*args)
     finally:
         torch.cuda.set_stream(here)
-    for group, user in ((args, there), ((outs,), here)):
-        for t in group:
-            for u in t if isinstance(t, (tuple, list)) else (t,):
-                if isinstance(u, torch.Tensor):
-                    u.record_stream(user)
+    for group, user in ((args, there), (outs, here)):
+        for t in _tensors(group):
+            t.record_stream(user)
     return outs
+
+
+def _tensors(t):
+    """The tensors among t and what it holds, sequences in sequences too."""
+    if isinstance(t, torch.Tensor):
+        yield t
+    elif isinstance(t, (tuple, list)):
+        for u in t:
+            yield from _tensors(u)
 
 
 def _rows(t, name, tail=1):
