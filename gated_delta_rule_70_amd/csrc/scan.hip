@@ -1,6 +1,15 @@
 // Selective scan: the recurrence with a diagonal transition that depends on the input
 // (gdr_selective_scan, gdr_selective_scan_step).
+//
+//   h[n] <- exp(step A[n]) h[n] + step x B[n],   y = sum_n C[n] h[n]
+//
+// for every channel.  A differs from channel to channel and state to state, so there is no matrix
+// product in it: an exponential, three multiplications and two additions for each token, channel and
+// state, on the vector ALU.
 #include "layer_launch.h"
+
+#include <type_traits>
+#include <utility>
 
 #include "row_device.h"
 
@@ -16,82 +25,451 @@ __device__ __forceinline__ void store1(bf16_t* p, float v) { *reinterpret_cast<_
 
 // Sixteen lanes for each channel, S state values in each: lane l has values l, l + 16, ...
 template <typename TX, typename TDT, int S>
-__global__ __launch_bounds__(kThreads) void scan_kernel(ScanArgs a, int tiles, int64_t block0) {
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int tiles, int64_t block0) {
     const int64_t b = block0 + blockIdx.x;
     const int seq = (int)(b / tiles), lane = threadIdx.x & 15;
     const int d = (int)(b % tiles) * (kThreads / 16) + threadIdx.x / 16;
     if (d >= a.D) return;  // whole rows of 16 lanes
     const int N = a.N, g = d / (a.D / a.G);
-    int64_t first = (int64_t)seq * a.T;
-    int len = a.T;
-    if (a.cu) {
-        const Span s = packed_span(a.cu, seq, a.T);
-        first = s.first, len = s.count;
-    }
+    const int64_t first = seq;
     float A[S], h[S];
     const int64_t at = ((int64_t)seq * a.D + d) * N;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const int n = lane + 16 * s;
-        A[s] = n < N && len > 0 ? a.A[(int64_t)d * N + n] * kLog2e : 0.f;
+        A[s] = n < N ? a.A[(int64_t)d * N + n] * kLog2e : 0.f;
         h[s] = n < N && a.h0 ? a.h0[at + n] : 0.f;
     }
     const float skip = a.skip ? a.skip[d] : 0.f, bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    const TX* x = static_cast<const TX*>(a.x) + first * a.x_stride + d;
-    const TDT* dt = static_cast<const TDT*>(a.dt) + first * a.dt_stride + d;
-    const TX* z = a.z ? static_cast<const TX*>(a.z) + first * a.z_stride + d : nullptr;
     const TX* B = static_cast<const TX*>(a.b) + first * a.b_stride + (int64_t)g * N;
     const TX* C = static_cast<const TX*>(a.c) + first * a.c_stride + (int64_t)g * N;
-    TX* out = static_cast<TX*>(a.out) + first * a.out_stride + d;
-    for (int t = 0; t < len; ++t) {
-        const float xv = to_f32(x[t * a.x_stride]);
-        float step = to_f32(dt[t * a.dt_stride]) + bias;
-        if (a.softplus) step = softplus(step);
-        const float in = step * xv;
-        float y = 0.f;
+    const float xv = to_f32(static_cast<const TX*>(a.x)[first * a.x_stride + d]);
+    float step = to_f32(static_cast<const TDT*>(a.dt)[first * a.dt_stride + d]) + bias;
+    if (a.softplus) step = softplus(step);
+    const float in = step * xv;
+    float y = 0.f;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int n = lane + 16 * s;
-            const float bv = n < N ? to_f32(B[t * a.b_stride + n]) : 0.f, cv = n < N ? to_f32(C[t * a.c_stride + n]) : 0.f;
-            h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * A[s]), h[s], in * bv);
-            y = __builtin_fmaf(cv, h[s], y);
-        }
-        y = row_sum(y);
-        y = __builtin_fmaf(skip, xv, y);
-        if (z) y *= silu(to_f32(z[t * a.z_stride]));
-        if (lane == 0) store1(out + t * a.out_stride, y);
+    for (int s = 0; s < S; ++s) {
+        const int n = lane + 16 * s;
+        const float bv = n < N ? to_f32(B[n]) : 0.f, cv = n < N ? to_f32(C[n]) : 0.f;
+        h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * A[s]), h[s], in * bv);
+        y = __builtin_fmaf(cv, h[s], y);
     }
+    y = row_sum(y);
+    y = __builtin_fmaf(skip, xv, y);
+    if (a.z) y *= silu(to_f32(static_cast<const TX*>(a.z)[first * a.z_stride + d]));
+    if (lane == 0) store1(static_cast<TX*>(a.out) + first * a.out_stride + d, y);
     if (a.ht)
 #pragma unroll
         for (int s = 0; s < S; ++s)
             if (lane + 16 * s < N) a.ht[at + lane + 16 * s] = h[s];
 }
 
+// ---- prompts -------------------------------------------------------------------------------------
+
+// Four values as loaded, turned to fp32 where they are used, so that the load stays in flight.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    f32x4 v;
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+};
+template <>
+struct Raw4<bf16_t> {
+    u32x2 v;
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i % 2 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+    }
+};
+// Values 0 .. 3 at p, zeros from n on; any alignment.
+template <typename T>
+__device__ __forceinline__ Raw4<T> load4(const T* p, int n) {
+    Raw4<T> r{};
+    if (n >= 4) {
+        __builtin_memcpy(&r, p, sizeof(r));
+    } else if (n > 0) {
+        T t[4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) t[i] = p[i];
+        __builtin_memcpy(&r, t, sizeof(r));
+    }
+    return r;
+}
+__device__ __forceinline__ void store4(float* p, int n, f32x4 v) {
+    if (n >= 4) {
+        __builtin_memcpy(p, &v, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+__device__ __forceinline__ void store4(bf16_t* p, int n, f32x4 v) {
+    const u32x2 u = bf16x4_bits(v);
+    if (n >= 4) {
+        __builtin_memcpy(p, &u, 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i].bits = (uint16_t)(u[i / 2] >> (i % 2 * 16));
+    }
+}
+
+// silu(z) for an fp32 output, and for a bf16 one, where the exponent's error of |z| 2^-24 does not show.
+__device__ __forceinline__ float gate(float z, const float*) { return silu(z); }
+__device__ __forceinline__ float gate(float z, const bf16_t*) {
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * z));
+}
+
+// Lane J's value in all L lanes that share a channel.
+template <int L, int J>
+__device__ __forceinline__ float broadcast(float x) {
+    static_assert(L == 16 || L == 4, "a row of lanes, or a quad");
+    return dpp_mov<L == 16 ? 0x150 + J : J * 0x55>(x);  // row_newbcast, quad_perm
+}
+
+// The sums over L lanes of L values each, lane j having the j-th: lanes exchange halves of what they
+// hold, opposite ones first.
+template <int L>
+__device__ __forceinline__ float sum_scatter(float (&p)[L], int lane) {
+    if constexpr (L == 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float keep = lane & 8 ? p[i + 8] : p[i], send = lane & 8 ? p[i] : p[i + 8];
+            p[i] = keep + dpp_mov<0x140>(send);  // row_mirror
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float keep = lane & 4 ? p[i + 4] : p[i], send = lane & 4 ? p[i] : p[i + 4];
+            p[i] = keep + dpp_mov<0x141>(send);  // row_half_mirror
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float keep = lane & 2 ? p[i + 2] : p[i], send = lane & 2 ? p[i] : p[i + 2];
+        p[i] = keep + dpp_mov<0x1B>(send);  // quad_perm [3,2,1,0]
+    }
+    const float keep = lane & 1 ? p[1] : p[0], send = lane & 1 ? p[0] : p[1];
+    return keep + dpp_mov<0xB1>(send);  // quad_perm [1,0,3,2]
+}
+
+template <int... J, typename F>
+__device__ __forceinline__ void unrolled(std::integer_sequence<int, J...>, F f) {
+    (f(std::integral_constant<int, J>{}), ...);
+}
+
+// A workgroup runs CT channels of one sequence from its first token to its last, TT tokens a tile.
+// L lanes share a channel, S state values in each, in registers throughout.  A tile's step and x lie
+// in LDS as [token][channel], B and C as [state][token] (L = 16) or [token][state] (L = 4), the next
+// tile's are on their way in registers meanwhile.  In a chunk of L tokens lane j reads the j-th
+// token's step and x and hands them to the others (DPP), and each lane sums its own states' part of
+// y for every token; sum_scatter leaves the j-th token's y in lane j.
+template <int L, int S>
+struct Tile {
+    static constexpr int CT = kThreads / L;
+    static constexpr int TT = L == 4 ? 32 : S == 1 ? 64 : S <= 4 ? 32 : 16;  // for 64 KB of LDS at most
+    static constexpr int NP = L * S;                                         // states, padded with zeros
+    static constexpr int bc = L == 16 ? NP * (TT + 4) : TT * NP;
+    static constexpr int groups = (TT * CT / 4 + kThreads - 1) / kThreads;   // of four channels, for a thread to bring
+    static constexpr int bc_groups = (TT * NP / 4 + kThreads - 1) / kThreads;  // of four states
+    // Where token t's channel c lies: channels are exchanged in fours so that the lanes of a wave,
+    // on L tokens of 64 / L channels, meet no bank twice.
+    static __device__ __forceinline__ int at(int t, int c) {
+        return t * CT + (c ^ (L == 16 ? (t >> 2 & 3) << 2 : (t & 3) << 4));
+    }
+};
+
+template <typename TX, typename TDT, int L, int S>
+__global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, int tiles, int64_t block0) {
+    using K = Tile<L, S>;
+    constexpr int CT = K::CT, TT = K::TT, NP = K::NP;
+    __shared__ float sDt[2][TT * CT], sX[2][TT * CT], sY[2][TT * CT];
+    __shared__ float sB[2][K::bc], sC[2][K::bc];
+
+    const int64_t b = block0 + blockIdx.x;
+    const int seq = (int)(b / (tiles * a.G)), gt = (int)(b % (tiles * a.G));
+    const int g = gt / tiles, per = a.D / a.G, c0 = gt % tiles * CT;  // first channel in the group
+    const int d0 = g * per + c0, left = per - c0;                     // in all; channels from there on
+    int64_t first = (int64_t)seq * a.T;
+    int len = a.T;
+    if (a.cu) {
+        const Span s = packed_span(a.cu, seq, a.T);
+        first = s.first, len = s.count;
+    }
+    const int tid = threadIdx.x % kThreads, N = a.N;
+
+    if (threadIdx.x >= kThreads) {
+        // What this thread brings of a tile: groups of four channels, of tokens rowsApart from each other,
+        // and of four states of B and C.
+        constexpr int rowsApart = kThreads / (CT / 4), bcApart = kThreads / (NP / 4);
+        const int gc = tid % (CT / 4) * 4, gt0 = tid / (CT / 4), gn = left - gc;
+        const TX* x = static_cast<const TX*>(a.x) + (first + gt0) * a.x_stride + d0 + gc;
+        const TDT* dt = static_cast<const TDT*>(a.dt) + (first + gt0) * a.dt_stride + d0 + gc;
+        const TX* z = a.z ? static_cast<const TX*>(a.z) + (first + gt0) * a.z_stride + d0 + gc : nullptr;
+        TX* out = static_cast<TX*>(a.out) + (first + gt0) * a.out_stride + d0 + gc;
+        const int bt = tid / (NP / 4), bn = tid % (NP / 4) * 4;
+        const TX* B = static_cast<const TX*>(a.b) + (first + bt) * a.b_stride + (int64_t)g * N + bn;
+        const TX* C = static_cast<const TX*>(a.c) + (first + bt) * a.c_stride + (int64_t)g * N + bn;
+        Raw4<TX> rx[K::groups], rz[K::groups], rb[K::bc_groups], rc[K::bc_groups];
+        Raw4<TDT> rdt[K::groups];
+        float bias[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias[i] = a.dt_bias && i < gn ? a.dt_bias[d0 + gc + i] : 0.f;
+
+        // Tiles of nothing but whole groups are loaded and stored without looking at their ends: a branch
+        // around a load makes the next instructions wait for it.
+        const bool whole = left >= CT && N % 4 == 0;
+        auto bring = [&](int t0) {  // the tile at t0, on which the pointers stand
+            if (whole && t0 + TT <= len) {
+#pragma unroll
+                for (int i = 0; i < K::groups; ++i)
+                    if (rowsApart * K::groups == TT || gt0 < TT) {
+                        rx[i] = load4(x + i * rowsApart * a.x_stride, 4);
+                        rdt[i] = load4(dt + i * rowsApart * a.dt_stride, 4);
+                    }
+#pragma unroll
+                for (int i = 0; i < K::bc_groups; ++i) {
+                    rb[i] = rc[i] = Raw4<TX>{};
+                    if ((bcApart * K::bc_groups == TT || bt < TT) && bn < N) {
+                        rb[i] = load4(B + i * bcApart * a.b_stride, 4);
+                        rc[i] = load4(C + i * bcApart * a.c_stride, 4);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < K::groups; ++i) {
+                    const int t = gt0 + i * rowsApart, n = t < TT && t0 + t < len ? gn : 0;
+                    rx[i] = load4(x + i * rowsApart * a.x_stride, n);
+                    rdt[i] = load4(dt + i * rowsApart * a.dt_stride, n);
+                }
+#pragma unroll
+                for (int i = 0; i < K::bc_groups; ++i) {
+                    const int t = bt + i * bcApart, n = t < TT && t0 + t < len ? N - bn : 0;
+                    rb[i] = load4(B + i * bcApart * a.b_stride, n);
+                    rc[i] = load4(C + i * bcApart * a.c_stride, n);
+                }
+            }
+            x += TT * a.x_stride;
+            dt += TT * a.dt_stride;
+            B += TT * a.b_stride;
+            C += TT * a.c_stride;
+        };
+        auto stage = [&](int t0, int buf) {
+#pragma unroll
+            for (int i = 0; i < K::groups; ++i) {
+                const int t = gt0 + i * rowsApart;
+                if (t >= TT) break;
+                f32x4 sv, xv;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sv[j] = rdt[i].get(j) + bias[j];
+                    xv[j] = rx[i].get(j);
+                }
+                if (a.softplus)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sv[j] = softplus(sv[j]);
+                if (t0 + t >= len) sv = f32x4{0.f, 0.f, 0.f, 0.f};  // tokens past the end leave the state as it is
+                *reinterpret_cast<f32x4*>(&sDt[buf][K::at(t, gc)]) = sv;
+                *reinterpret_cast<f32x4*>(&sX[buf][K::at(t, gc)]) = xv;
+            }
+#pragma unroll
+            for (int i = 0; i < K::bc_groups; ++i) {
+                const int t = bt + i * bcApart;
+                if (t >= TT) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int to = L == 16 ? (bn + j) * (TT + 4) + t : t * NP + bn + j;
+                    sB[buf][to] = rb[i].get(j);
+                    sC[buf][to] = rc[i].get(j);
+                }
+            }
+        };
+        auto bring_gate = [&](int t0) {
+            if (!z) return;
+#pragma unroll
+            for (int i = 0; i < K::groups; ++i) {
+                const int t = gt0 + i * rowsApart;
+                if (whole && t0 + TT <= len) {
+                    if (rowsApart * K::groups == TT || gt0 < TT) rz[i] = load4(z + i * rowsApart * a.z_stride, 4);
+                } else {
+                    rz[i] = load4(z + i * rowsApart * a.z_stride, t < TT && t0 + t < len ? gn : 0);
+                }
+            }
+            z += TT * a.z_stride;
+        };
+        auto store = [&](int t0, int buf) {
+#pragma unroll
+            for (int i = 0; i < K::groups; ++i) {
+                const int t = gt0 + i * rowsApart;
+                if (t >= TT) break;
+                f32x4 y = *reinterpret_cast<const f32x4*>(&sY[buf][K::at(t, gc)]);
+                if (z)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] *= gate(rz[i].get(j), out);
+                if (whole && t0 + TT <= len)
+                    store4(out + i * rowsApart * a.out_stride, 4, y);
+                else if (t0 + t < len)
+                    store4(out + i * rowsApart * a.out_stride, gn, y);
+            }
+            out += TT * a.out_stride;
+        };
+
+        if (len > 0) {
+            bring(0);
+            stage(0, 0);
+            if (TT < len) bring(TT);
+        }
+        lds_barrier();
+#pragma unroll 1
+        for (int t0 = 0, buf = 0; t0 < len; t0 += TT, buf ^= 1) {
+            if (t0 > 0) store(t0 - TT, buf ^ 1);
+            bring_gate(t0);
+            if (t0 + TT < len) {
+                stage(t0 + TT, buf ^ 1);
+                if (t0 + 2 * TT < len) bring(t0 + 2 * TT);
+            }
+            lds_barrier();
+        }
+        if (len > 0) store((len - 1) / TT * TT, (len - 1) / TT & 1);
+        return;
+    }
+
+    const int lane = tid % L, c = tid / L;
+    const bool mine = c < left;
+    float A[S], h[S];
+    const int64_t state = ((int64_t)seq * a.D + d0 + c) * N + lane * S;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const bool there = mine && lane * S + s < N;
+        A[s] = there && len > 0 ? a.A[(int64_t)(d0 + c) * N + lane * S + s] * kLog2e : 0.f;
+        h[s] = there && a.h0 ? a.h0[state + s] : 0.f;
+    }
+    const float skip = mine && a.skip ? a.skip[d0 + c] : 0.f;
+    // What was loaded so far is waited for here: left to its first use in the loop, the wait would be
+    // there in every pass.
+#pragma unroll
+    for (int s = 0; s < S; ++s) asm volatile("" : "+v"(A[s]), "+v"(h[s]));
+
+    // B and C of four tokens for this lane's states
+    struct Four {
+        f32x4 b[S], c[S];
+    };
+    auto four = [&](int buf, int t, Four& f) {
+        if constexpr (L == 16) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                f.b[s] = *reinterpret_cast<const f32x4*>(&sB[buf][(lane * S + s) * (TT + 4) + t]);
+                f.c[s] = *reinterpret_cast<const f32x4*>(&sC[buf][(lane * S + s) * (TT + 4) + t]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float b[S], cc[S];
+                __builtin_memcpy(b, __builtin_assume_aligned(&sB[buf][(t + i) * NP + lane * S], 4 * S), sizeof(b));
+                __builtin_memcpy(cc, __builtin_assume_aligned(&sC[buf][(t + i) * NP + lane * S], 4 * S), sizeof(cc));
+#pragma unroll
+                for (int s = 0; s < S; ++s) f.b[s][i] = b[s], f.c[s][i] = cc[s];
+            }
+        }
+    };
+    auto compute = [&](int buf) {
+        // operands from LDS are read one group of four tokens (step and x one chunk) ahead, into two
+        // sets of registers in turn
+        constexpr int chunks = L == 16 ? 1 : 2;  // of a pass, so that it has an even number of groups
+        Four f[2];
+        four(buf, 0, f[0]);
+        float step = sDt[buf][K::at(lane, c)], xv = sX[buf][K::at(lane, c)];
+#pragma unroll 1
+        for (int t0 = 0; t0 < TT; t0 += chunks * L) {
+#pragma unroll
+            for (int k = 0; k < chunks; ++k) {
+                const int here = t0 + k * L;
+                const int after = here + L < TT ? here + L : 0;  // nothing is done with what is read behind the last chunk
+                const float step1 = sDt[buf][K::at(after + lane, c)], xv1 = sX[buf][K::at(after + lane, c)];
+                const float in = step * xv;
+                float p[L];
+                unrolled(std::make_integer_sequence<int, L>{}, [&](auto j) {
+                    constexpr int J = decltype(j)::value;
+                    Four &now = f[(k * (L / 4) + J / 4) % 2], &next = f[(k * (L / 4) + J / 4 + 1) % 2];
+                    if constexpr (J % 4 == 0) four(buf, J + 4 < L ? here + J + 4 : after, next);
+                    const float sj = broadcast<L, J>(step), ij = broadcast<L, J>(in);
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(sj * A[s]), h[s], ij * now.b[s][J % 4]);
+                        p[J] = s ? __builtin_fmaf(now.c[s][J % 4], h[s], p[J]) : now.c[s][J % 4] * h[s];
+                    }
+                });
+                sY[buf][K::at(here + lane, c)] = __builtin_fmaf(skip, xv, sum_scatter<L>(p, lane));
+                step = step1, xv = xv1;
+            }
+        }
+    };
+
+    lds_barrier();
+#pragma unroll 1
+    for (int t0 = 0, buf = 0; t0 < len; t0 += TT, buf ^= 1) {
+        compute(buf);
+        lds_barrier();
+    }
+    if (a.ht && mine)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (lane * S + s < N) a.ht[state + s] = h[s];
+}
+
+bool valid(const ScanArgs& a) {
+    return a.B >= 1 && a.D >= 1 && a.N >= 1 && a.N <= GDR_SCAN_MAX_STATES && a.G >= 1 && a.D % a.G == 0;
+}
+
 template <typename TX, typename TDT>
-hipError_t launch(const ScanArgs& a) {
+hipError_t launch_step(const ScanArgs& a) {
     const int tiles = (a.D + kThreads / 16 - 1) / (kThreads / 16);
     return by_blocks((int64_t)a.B * tiles, kThreads, [&](int64_t first, unsigned count) {
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, a.stream, a, tiles, first); };
         if (a.N <= 16)
-            go(scan_kernel<TX, TDT, 1>);
+            go(scan_step_kernel<TX, TDT, 1>);
         else if (a.N <= 32)
-            go(scan_kernel<TX, TDT, 2>);
+            go(scan_step_kernel<TX, TDT, 2>);
         else if (a.N <= 64)
-            go(scan_kernel<TX, TDT, 4>);
+            go(scan_step_kernel<TX, TDT, 4>);
         else
-            go(scan_kernel<TX, TDT, 8>);
+            go(scan_step_kernel<TX, TDT, 8>);
     });
 }
 
-hipError_t typed(const ScanArgs& a) {
-    if (a.B < 1 || a.D < 1 || a.N < 1 || a.N > GDR_SCAN_MAX_STATES || a.G < 1 || a.D % a.G) return hipErrorInvalidValue;
-    if (!a.bf16) return launch<float, float>(a);
-    return a.dt_bf16 ? launch<bf16_t, bf16_t>(a) : launch<bf16_t, float>(a);
+template <typename TX, typename TDT, int L, int S>
+hipError_t launch_tiles(const ScanArgs& a) {
+    constexpr int CT = Tile<L, S>::CT;
+    const int tiles = (a.D / a.G + CT - 1) / CT;
+    return by_blocks((int64_t)a.B * a.G * tiles, 2 * kThreads, [&](int64_t first, unsigned count) {
+        hipLaunchKernelGGL((scan_kernel<TX, TDT, L, S>), dim3(count), dim3(2 * kThreads), 0, a.stream, a, tiles, first);
+    });
+}
+
+template <typename TX, typename TDT>
+hipError_t launch(const ScanArgs& a) {
+    if (a.N <= 16 && (int64_t)a.B * a.D >= 32768)
+        return a.N <= 8 ? launch_tiles<TX, TDT, 4, 2>(a) : launch_tiles<TX, TDT, 4, 4>(a);
+    if (a.N <= 16) return launch_tiles<TX, TDT, 16, 1>(a);
+    if (a.N <= 32) return launch_tiles<TX, TDT, 16, 2>(a);
+    if (a.N <= 64) return launch_tiles<TX, TDT, 16, 4>(a);
+    return launch_tiles<TX, TDT, 16, 8>(a);
 }
 
 }  // namespace
 
-hipError_t launch_selective_scan(const ScanArgs& a) { return typed(a); }
-hipError_t launch_selective_scan_step(const ScanArgs& a) { return typed(a); }
+hipError_t launch_selective_scan(const ScanArgs& a) {
+    if (!valid(a)) return hipErrorInvalidValue;
+    if (!a.bf16) return launch<float, float>(a);
+    return a.dt_bf16 ? launch<bf16_t, bf16_t>(a) : launch<bf16_t, float>(a);
+}
+
+hipError_t launch_selective_scan_step(const ScanArgs& a) {
+    if (!valid(a)) return hipErrorInvalidValue;
+    if (!a.bf16) return launch_step<float, float>(a);
+    return a.dt_bf16 ? launch_step<bf16_t, bf16_t>(a) : launch_step<bf16_t, float>(a);
+}
 
 }  // namespace gdr

@@ -72,7 +72,7 @@ _NONE = (0,) * CONV_MAX_OUT
 def bind(L):
     """Argument types of the entry points of gdr_layer.h on the loaded library."""
     for name, n in (("gdr_causal_conv", 9), ("gdr_qk_norm_rope", 11), ("gdr_selective_scan", 14),
-                    ("gdr_selective_scan_step", 12)):
+                    ("gdr_selective_scan_step", 13)):
         fn = getattr(L, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [_VP] * n

@@ -156,7 +156,7 @@ def test_prompt_scan_refusals(L, want, kw):
 @pytest.mark.parametrize("T", [0, 2])
 def test_step_takes_one_token(L, T):
     assert scan(L, True, T=T) == ESHAPE
-    assert L.gdr_selective_scan_step(None, *[None] * 11) == ENULL
+    assert L.gdr_selective_scan_step(None, *[None] * 12) == ENULL
 
 
 # ---- the Python binding ----------------------------------------------------------------------
@@ -249,3 +249,9 @@ def test_rope_table():
     for bad in (dict(length=0, rotated=6), dict(length=3, rotated=5), dict(length=3, rotated=0)):
         with pytest.raises(ValueError):
             gdr.rope_table(**bad)
+
+
+def test_bound_arguments_match_the_header(L):
+    """As many of them as the header declares: one more would be passed as a C int, a stream's handle cut."""
+    for name, args in re.findall(r"^\s*int\s+(gdr_\w+)\s*\(([^)]*)\)", open(HEADER).read(), re.M):
+        assert len(getattr(L, name).argtypes) == args.count(",") + 1, name
