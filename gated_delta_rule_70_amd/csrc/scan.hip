@@ -23,50 +23,6 @@ constexpr float kLog2e = 1.44269504088896341f;
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(bf16_t* p, float v) { *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(v); }
 
-// Sixteen lanes for each channel, S state values in each: lane l has values l, l + 16, ...
-template <typename TX, typename TDT, int S>
-__global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int tiles, int64_t block0) {
-    const int64_t b = block0 + blockIdx.x;
-    const int seq = (int)(b / tiles), lane = threadIdx.x & 15;
-    const int d = (int)(b % tiles) * (kThreads / 16) + threadIdx.x / 16;
-    if (d >= a.D) return;  // whole rows of 16 lanes
-    const int N = a.N, g = d / (a.D / a.G);
-    const int64_t first = seq;
-    float A[S], h[S];
-    const int64_t at = ((int64_t)seq * a.D + d) * N;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int n = lane + 16 * s;
-        A[s] = n < N ? a.A[(int64_t)d * N + n] * kLog2e : 0.f;
-        h[s] = n < N && a.h0 ? a.h0[at + n] : 0.f;
-    }
-    const float skip = a.skip ? a.skip[d] : 0.f, bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    const TX* B = static_cast<const TX*>(a.b) + first * a.b_stride + (int64_t)g * N;
-    const TX* C = static_cast<const TX*>(a.c) + first * a.c_stride + (int64_t)g * N;
-    const float xv = to_f32(static_cast<const TX*>(a.x)[first * a.x_stride + d]);
-    float step = to_f32(static_cast<const TDT*>(a.dt)[first * a.dt_stride + d]) + bias;
-    if (a.softplus) step = softplus(step);
-    const float in = step * xv;
-    float y = 0.f;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int n = lane + 16 * s;
-        const float bv = n < N ? to_f32(B[n]) : 0.f, cv = n < N ? to_f32(C[n]) : 0.f;
-        h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * A[s]), h[s], in * bv);
-        y = __builtin_fmaf(cv, h[s], y);
-    }
-    y = row_sum(y);
-    y = __builtin_fmaf(skip, xv, y);
-    if (a.z) y *= silu(to_f32(static_cast<const TX*>(a.z)[first * a.z_stride + d]));
-    if (lane == 0) store1(static_cast<TX*>(a.out) + first * a.out_stride + d, y);
-    if (a.ht)
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (lane + 16 * s < N) a.ht[at + lane + 16 * s] = h[s];
-}
-
-// ---- prompts -------------------------------------------------------------------------------------
-
 // Four values as loaded, turned to fp32 where they are used, so that the load stays in flight.
 template <typename T>
 struct Raw4;
@@ -122,6 +78,111 @@ __device__ __forceinline__ float gate(float z, const float*) { return silu(z); }
 __device__ __forceinline__ float gate(float z, const bf16_t*) {
     return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * z));
 }
+
+// ---- single tokens -------------------------------------------------------------------------------
+
+// One token of each sequence, any N: sixteen lanes for each channel, S state values in each, lane l
+// has values l, l + 16, ...
+template <typename TX, typename TDT, int S>
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int tiles, int64_t block0) {
+    const int64_t b = block0 + blockIdx.x;
+    const int64_t seq = b / tiles;
+    const int lane = threadIdx.x & 15;
+    const int d = (int)(b % tiles) * (kThreads / 16) + threadIdx.x / 16;
+    if (d >= a.D) return;  // whole rows of 16 lanes
+    const int N = a.N, g = d / (a.D / a.G);
+    float A[S], h[S];
+    const int64_t at = (seq * a.D + d) * N;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int n = lane + 16 * s;
+        A[s] = n < N ? a.A[(int64_t)d * N + n] * kLog2e : 0.f;
+        h[s] = n < N && a.h0 ? a.h0[at + n] : 0.f;
+    }
+    const TX* B = static_cast<const TX*>(a.b) + seq * a.b_stride + (int64_t)g * N;
+    const TX* C = static_cast<const TX*>(a.c) + seq * a.c_stride + (int64_t)g * N;
+    const float xv = to_f32(static_cast<const TX*>(a.x)[seq * a.x_stride + d]);
+    float step = to_f32(static_cast<const TDT*>(a.dt)[seq * a.dt_stride + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
+    if (a.softplus) step = softplus(step);
+    const float in = step * xv;
+    float y = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int n = lane + 16 * s;
+        const float bv = n < N ? to_f32(B[n]) : 0.f, cv = n < N ? to_f32(C[n]) : 0.f;
+        h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * A[s]), h[s], in * bv);
+        y = __builtin_fmaf(cv, h[s], y);
+    }
+    y = row_sum(y);
+    y = __builtin_fmaf(a.skip ? a.skip[d] : 0.f, xv, y);
+    TX* out = static_cast<TX*>(a.out) + seq * a.out_stride + d;
+    if (a.z) y *= gate(to_f32(static_cast<const TX*>(a.z)[seq * a.z_stride + d]), out);
+    if (lane == 0) store1(out, y);
+    if (a.ht)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (lane + 16 * s < N) a.ht[at + lane + 16 * s] = h[s];
+}
+
+// The same for N a multiple of four: P lanes for each channel (a power of two, at least N / 4), four
+// state values in each, and Q sequences one after the other, whose loads are all on their way at
+// once.  Bound by the states' bytes.
+template <typename TX, typename TDT, int P, int Q>
+__global__ __launch_bounds__(kThreads) void scan_step4_kernel(ScanArgs a, int tiles, int64_t block0) {
+    const int64_t b = block0 + blockIdx.x;
+    const int64_t seq0 = b / tiles * Q;
+    const int lane = threadIdx.x % P;
+    const int d = (int)(b % tiles) * (kThreads / P) + threadIdx.x / P;
+    if (d >= a.D) return;  // all lanes of a channel
+    const int N = a.N, n = 4 * lane, g = a.G == 1 ? 0 : d / (a.D / a.G);
+    const bool mine = n < N;
+    Raw4<float> h[Q], A{};
+    Raw4<TX> B[Q], C[Q];
+    TX x[Q], z[Q];
+    TDT dt[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int64_t seq = seq0 + q < a.B ? seq0 + q : a.B - 1;  // past the last one: loaded again, not stored
+        h[q] = Raw4<float>{};
+        B[q] = C[q] = Raw4<TX>{};
+        if (mine) {
+            if (a.h0) h[q] = load4(a.h0 + (seq * a.D + d) * N + n, 4);
+            B[q] = load4(static_cast<const TX*>(a.b) + seq * a.b_stride + (int64_t)g * N + n, 4);
+            C[q] = load4(static_cast<const TX*>(a.c) + seq * a.c_stride + (int64_t)g * N + n, 4);
+        }
+        x[q] = static_cast<const TX*>(a.x)[seq * a.x_stride + d];
+        dt[q] = static_cast<const TDT*>(a.dt)[seq * a.dt_stride + d];
+        z[q] = a.z ? static_cast<const TX*>(a.z)[seq * a.z_stride + d] : TX{};
+    }
+    if (mine) A = load4(a.A + (int64_t)d * N + n, 4);
+    const float skip = a.skip ? a.skip[d] : 0.f, bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        if (seq0 + q >= a.B) return;
+        float step = to_f32(dt[q]) + bias;
+        if (a.softplus) step = softplus(step);
+        const float xv = to_f32(x[q]), in = step * xv;
+        f32x4 v;
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * (A.get(i) * kLog2e)), h[q].get(i), in * B[q].get(i));
+            y = __builtin_fmaf(C[q].get(i), v[i], y);
+        }
+        if (mine && a.ht) store4(a.ht + ((seq0 + q) * a.D + d) * N + n, 4, v);
+        if constexpr (P > 1) y += dpp_mov<0xB1>(y);   // quad_perm [1,0,3,2]
+        if constexpr (P > 2) y += dpp_mov<0x4E>(y);   // quad_perm [2,3,0,1]
+        if constexpr (P > 4) y += dpp_mov<0x141>(y);  // row_half_mirror
+        if constexpr (P > 8) y += dpp_mov<0x140>(y);  // row_mirror
+        if constexpr (P > 16) y += __shfl_xor(y, 16);
+        y = __builtin_fmaf(skip, xv, y);
+        TX* out = static_cast<TX*>(a.out) + (seq0 + q) * a.out_stride + d;
+        if (a.z) y *= gate(to_f32(z[q]), out);
+        if (lane == 0) store1(out, y);
+    }
+}
+
+// ---- prompts -------------------------------------------------------------------------------------
 
 // Lane J's value in all L lanes that share a channel.
 template <int L, int J>
@@ -423,8 +484,28 @@ bool valid(const ScanArgs& a) {
     return a.B >= 1 && a.D >= 1 && a.N >= 1 && a.N <= GDR_SCAN_MAX_STATES && a.G >= 1 && a.D % a.G == 0;
 }
 
+template <typename TX, typename TDT, int P>
+hipError_t launch_step4(const ScanArgs& a) {
+    constexpr int channels = kThreads / P;
+    const int tiles = (a.D + channels - 1) / channels;
+    auto go = [&](auto kernel, int q) {
+        return by_blocks(((int64_t)a.B + q - 1) / q * tiles, kThreads, [&](int64_t first, unsigned count) {
+            hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, a.stream, a, tiles, first);
+        });
+    };
+    return (int64_t)a.B * tiles >= 8192 ? go(scan_step4_kernel<TX, TDT, P, 4>, 4) : go(scan_step4_kernel<TX, TDT, P, 1>, 1);
+}
+
 template <typename TX, typename TDT>
 hipError_t launch_step(const ScanArgs& a) {
+    if (a.N % 4 == 0) {
+        if (a.N <= 4) return launch_step4<TX, TDT, 1>(a);
+        if (a.N <= 8) return launch_step4<TX, TDT, 2>(a);
+        if (a.N <= 16) return launch_step4<TX, TDT, 4>(a);
+        if (a.N <= 32) return launch_step4<TX, TDT, 8>(a);
+        if (a.N <= 64) return launch_step4<TX, TDT, 16>(a);
+        return launch_step4<TX, TDT, 32>(a);
+    }
     const int tiles = (a.D + kThreads / 16 - 1) / (kThreads / 16);
     return by_blocks((int64_t)a.B * tiles, kThreads, [&](int64_t first, unsigned count) {
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, a.stream, a, tiles, first); };
