@@ -19,13 +19,13 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 16;  // rows of a tile, at most 64
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 4;  // rows that a thread loads at once
+constexpr int kXcds = 8;   // workgroups go round them in turn
 
 struct ConvGroups {
     int groups;                           // of eight channels; an output's last one may have fewer
     int first[GDR_CONV_MAX_OUT + 1];      // first group of each output
-    int64_t head_blocks, block0, col_waves;  // col_waves: waves across the channels
+    int64_t head_blocks, tile_blocks, block0, col_waves;  // col_waves: waves across the channels
 };
 
 // A thread's channels: the output, their place in it, and in x.
@@ -68,7 +68,7 @@ struct Taps {
             float s = bias[i];
 #pragma unroll
             for (int j = 0; j < W; ++j) s = __builtin_fmaf(w[j][i], f[j][i], s);
-            y[i] = a.silu ? silu(s) : s;
+            y[i] = a.silu ? silu_for(s, static_cast<const TX*>(nullptr)) : s;
         }
         store8<PART>(static_cast<TX*>(a.out[c.out]) + row * a.out_stride[c.out] + c.at, c.n, y);
     }
@@ -124,11 +124,18 @@ __device__ __forceinline__ void head(const ConvArgs& a, const ConvGroups& c, int
         if (t < len) taps.store(a, col, first + t, f + t, static_cast<const TX*>(nullptr));
 }
 
+// Work item of block b of n, so that each XCD (block b is on XCD b % 8) has a contiguous range: the
+// rows that neighbouring tiles share are then in its L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
+    const int64_t q = n / kXcds, r = n % kXcds, x = b % kXcds;
+    return x * q + (x < r ? x : r) + b / kXcds;
+}
+
 // Which of the tile's rows have their whole window in their own sequence.
-template <int W>
+template <int W, int TILE>
 __device__ __forceinline__ uint64_t whole_windows(const ConvArgs& a, int r0) {
     const int lane = threadIdx.x & 63, r = r0 + lane;
-    bool ok = lane < kTile && r < a.rows;
+    bool ok = lane < TILE && r < a.rows;
     if (ok && !a.cu) {
         ok = r % a.T >= W - 1;
     } else if (ok) {
@@ -146,13 +153,13 @@ __device__ __forceinline__ uint64_t whole_windows(const ConvArgs& a, int r0) {
     return __ballot(ok);
 }
 
-template <typename TX, typename TW, int W, bool PART>
+template <typename TX, typename TW, int W, int TILE, bool PART>
 __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int64_t wave) {
     const int64_t t = wave / c.col_waves;
-    const int64_t row0 = t * kTile;
+    const int64_t row0 = t * TILE;
     if (row0 >= a.rows) return;
     const int r0 = (int)row0;
-    const uint64_t whole = whole_windows<W>(a, r0);
+    const uint64_t whole = whole_windows<W, TILE>(a, r0);
     const int g = (int)(wave % c.col_waves) * 64 + (threadIdx.x & 63);
     if (whole == 0 || g >= c.groups) return;
     const Cols col = cols_of(a, c, g);
@@ -160,20 +167,20 @@ __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int
     taps.load(a, col);
     const TX* x = static_cast<const TX*>(a.x) + col.channel;
     float f[W - 1 + kUnroll][8];
-    auto load = [&](int r, float(&v)[8]) {
-        if (r >= 0 && r < a.rows) {
-            load8<PART>(x + r * a.x_stride, col.n, v);
-        } else {
+    Raw8<TX> next[kUnroll];
+    auto raw = [&](int r) { return r >= 0 && r < a.rows ? load8_raw<PART>(x + r * a.x_stride, col.n) : Raw8<TX>{}; };
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        }
-    };
+    for (int j = 0; j < W - 1; ++j) raw(r0 - (W - 1) + j).get(f[j]);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load(r0 - (W - 1) + j, f[j]);
+    for (int u = 0; u < kUnroll; ++u) next[u] = raw(r0 + u);
 #pragma unroll 1
-    for (int k = 0; k < kTile; k += kUnroll) {
+    for (int k = 0; k < TILE; k += kUnroll) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) load(r0 + k + u, f[W - 1 + u]);
+        for (int u = 0; u < kUnroll; ++u) next[u].get(f[W - 1 + u]);
+        if (k + kUnroll < TILE) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) next[u] = raw(r0 + k + kUnroll + u);
+        }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             if (whole >> (k + u) & 1) taps.store(a, col, (int64_t)r0 + k + u, f + u, static_cast<const TX*>(nullptr));
@@ -184,13 +191,14 @@ __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int
     }
 }
 
-template <typename TX, typename TW, int W, bool PART>
+template <typename TX, typename TW, int W, int TILE, bool PART>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvArgs a, ConvGroups c) {
     const int64_t b = c.block0 + blockIdx.x;
     if (b < c.head_blocks)
         head<TX, TW, W, PART>(a, c, b * kThreads + threadIdx.x);
     else
-        tile<TX, TW, W, PART>(a, c, (b - c.head_blocks) * (kThreads / 64) + threadIdx.x / 64);
+        tile<TX, TW, W, TILE, PART>(a, c, xcd_order(b - c.head_blocks, c.tile_blocks) * (kThreads / 64) +
+                                              __builtin_amdgcn_readfirstlane(threadIdx.x / 64));
 }
 
 template <typename TX, typename TW, int W>
@@ -207,15 +215,24 @@ hipError_t launch(const ConvArgs& a) {
     c.col_waves = (c.groups + 63) / 64;
     c.head_blocks = ((int64_t)a.B * c.groups + kThreads - 1) / kThreads;
     const bool tiles = a.rows > 0 && a.T >= W;  // some sequence may be longer than its head
-    const int64_t waves = tiles ? ((int64_t)a.rows + kTile - 1) / kTile * c.col_waves : 0;
-    const int64_t blocks = c.head_blocks + (waves + kThreads / 64 - 1) / (kThreads / 64);
-    return by_blocks(blocks, kThreads, [&](int64_t first, unsigned count) {
-        c.block0 = first;
-        if (part)
-            hipLaunchKernelGGL((causal_conv_kernel<TX, TW, W, true>), dim3(count), dim3(kThreads), 0, a.stream, a, c);
-        else
-            hipLaunchKernelGGL((causal_conv_kernel<TX, TW, W, false>), dim3(count), dim3(kThreads), 0, a.stream, a, c);
-    });
+    auto go = [&](auto rows, auto kernel) {
+        constexpr int TILE = decltype(rows)::value;
+        const int64_t waves = tiles ? ((int64_t)a.rows + TILE - 1) / TILE * c.col_waves : 0;
+        c.tile_blocks = (waves + kThreads / 64 - 1) / (kThreads / 64);
+        return by_blocks(c.head_blocks + c.tile_blocks, kThreads, [&](int64_t first, unsigned count) {
+            c.block0 = first;
+            hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, a.stream, a, c);
+        });
+    };
+    // Tiles of 16 rows where they make eight waves for each CU, of 4 rows below: more waves count for
+    // more than rows read again.  us at 16 / 4 rows: 32768 x 8192 213 / 232, 4096 x 4096 16.2 / 17.8,
+    // 300 x 2048 7.9 / 4.5, 2999 x 1001 fp32 17.9 / 10.2.
+    using std::integral_constant;
+    if ((int64_t)a.rows / 16 * c.col_waves >= 2048)
+        return part ? go(integral_constant<int, 16>{}, causal_conv_kernel<TX, TW, W, 16, true>)
+                    : go(integral_constant<int, 16>{}, causal_conv_kernel<TX, TW, W, 16, false>);
+    return part ? go(integral_constant<int, 4>{}, causal_conv_kernel<TX, TW, W, 4, true>)
+                : go(integral_constant<int, 4>{}, causal_conv_kernel<TX, TW, W, 4, false>);
 }
 
 }  // namespace

@@ -60,6 +60,40 @@ __device__ __forceinline__ void store8(bf16_t* p, int n, const float (&v)[8]) {
     }
 }
 
+// Eight values as loaded, turned to fp32 where they are used, so that the load stays in flight.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    f32x4 v[2];
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = v[i / 4][i % 4];
+    }
+};
+template <>
+struct Raw8<bf16_t> {
+    u32x4 v;
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(i % 2 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+    }
+};
+template <bool PART, typename T>
+__device__ __forceinline__ Raw8<T> load8_raw(const T* p, int n) {
+    Raw8<T> r{};
+    if (!PART || n >= 8) {
+        __builtin_memcpy(&r, p, sizeof(r));
+    } else {
+        T t[8] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) t[i] = p[i];
+        __builtin_memcpy(&r, t, sizeof(r));
+    }
+    return r;
+}
+
 // Sum over the V / 8 neighbouring lanes (4, 8 or 16) that hold a head's V values, in all of them.
 template <int CTRL>
 __device__ __forceinline__ double dpp_mov64(double x) {
@@ -95,6 +129,14 @@ __device__ __forceinline__ float exp_neg(float z) {
 
 // z / (1 + exp(-z))
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + exp_neg(z)); }
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+// silu(z) for an fp32 output, and for a bf16 one, where the exponent's error of |z| 2^-24 does not show.
+__device__ __forceinline__ float silu_for(float z, const float*) { return silu(z); }
+__device__ __forceinline__ float silu_for(float z, const bf16_t*) {
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * z));
+}
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), to a few ulp of the result at any v: far
 // below zero it is exp(v), for which 1 + exp(v) has no bits.  log1p(e) = 2 artanh(s) with

@@ -18,7 +18,6 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(bf16_t* p, float v) { *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(v); }
@@ -73,12 +72,6 @@ __device__ __forceinline__ void store4(bf16_t* p, int n, f32x4 v) {
     }
 }
 
-// silu(z) for an fp32 output, and for a bf16 one, where the exponent's error of |z| 2^-24 does not show.
-__device__ __forceinline__ float gate(float z, const float*) { return silu(z); }
-__device__ __forceinline__ float gate(float z, const bf16_t*) {
-    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * z));
-}
-
 // ---- single tokens -------------------------------------------------------------------------------
 
 // One token of each sequence, any N: sixteen lanes for each channel, S state values in each, lane l
@@ -116,7 +109,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int til
     y = row_sum(y);
     y = __builtin_fmaf(a.skip ? a.skip[d] : 0.f, xv, y);
     TX* out = static_cast<TX*>(a.out) + seq * a.out_stride + d;
-    if (a.z) y *= gate(to_f32(static_cast<const TX*>(a.z)[seq * a.z_stride + d]), out);
+    if (a.z) y *= silu_for(to_f32(static_cast<const TX*>(a.z)[seq * a.z_stride + d]), out);
     if (lane == 0) store1(out, y);
     if (a.ht)
 #pragma unroll
@@ -177,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void scan_step4_kernel(ScanArgs a, int ti
         if constexpr (P > 16) y += __shfl_xor(y, 16);
         y = __builtin_fmaf(skip, xv, y);
         TX* out = static_cast<TX*>(a.out) + (seq0 + q) * a.out_stride + d;
-        if (a.z) y *= gate(to_f32(z[q]), out);
+        if (a.z) y *= silu_for(to_f32(z[q]), out);
         if (lane == 0) store1(out, y);
     }
 }
@@ -368,7 +361,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 f32x4 y = *reinterpret_cast<const f32x4*>(&sY[buf][K::at(t, gc)]);
                 if (z)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] *= gate(rz[i].get(j), out);
+                    for (int j = 0; j < 4; ++j) y[j] *= silu_for(rz[i].get(j), out);
                 if (whole && t0 + TT <= len)
                     store4(out + i * rowsApart * a.out_stride, 4, y);
                 else if (t0 + t < len)
