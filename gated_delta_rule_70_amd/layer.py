@@ -154,7 +154,14 @@ def causal_conv(x, weight, bias=None, state=None, cu_seqlens=None, activation="s
     ``(y, out_state)``, y a tuple for a sequence; ``out_state`` (which may be ``state`` itself) holds
     the rows that a later call continues from, and is None if not given and not wanted.
     """
-    if stream is not None and (not _given(out) or out_state is None and want_state) and _elsewhere(stream, x):
+    if stream is None:
+        status = (_qz._B or _qz._binding()).causal_conv(x, weight, bias, state, cu_seqlens, activation, out, out_state, want_state,
+                                                        False)
+        if status is not None:
+            if status:
+                _fail(status)
+            return (out if isinstance(out, torch.Tensor) else tuple(out)), out_state
+    elif (not _given(out) or out_state is None and want_state) and _elsewhere(stream, x):
         return _on(stream, causal_conv, x, weight, bias, state, cu_seqlens, activation, out, out_state, want_state)
     return _conv(x, weight, bias, state, cu_seqlens, activation, out, out_state, want_state, stream,
                  *_batch(x, cu_seqlens))
@@ -164,10 +171,16 @@ def causal_conv_step(x, weight, state, bias=None, activation="silu", out=None, o
     """One new token of every sequence through :func:`causal_conv`: ``x`` is ``[B, D]``.  Updates
     ``state`` in place unless ``out_state`` is given.  Returns y (a tuple for a sequence ``out``).
     ``state`` may be None (zeros; ``out_state`` then receives the new state if given)."""
-    if stream is not None and not _given(out) and _elsewhere(stream, x):
+    end = state if out_state is None else out_state
+    if stream is None:
+        status = (_qz._B or _qz._binding()).causal_conv(x, weight, bias, state, None, activation, out, end, False, True)
+        if status is not None:
+            if status:
+                _fail(status)
+            return out if isinstance(out, torch.Tensor) else tuple(out)
+    elif not _given(out) and _elsewhere(stream, x):
         return _on(stream, causal_conv_step, x, weight, state, bias, activation, out, out_state)
-    return _conv(x, weight, bias, state, None, activation, out, state if out_state is None else out_state, False, stream,
-                 *_tokens(x))[0]
+    return _conv(x, weight, bias, state, None, activation, out, end, False, stream, *_tokens(x))[0]
 
 
 def _given(out):
@@ -252,7 +265,13 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
 
     Returns ``(out_q, out_k)`` of q's and k's shapes; they may be ``q`` and ``k`` themselves.
     """
-    if stream is not None and (out_q is None or out_k is None) and _elsewhere(stream, q):
+    if stream is None:
+        status = (_qz._B or _qz._binding()).qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, out_q, out_k)
+        if status is not None:
+            if status:
+                _fail(status)
+            return out_q, out_k
+    elif (out_q is None or out_k is None) and _elsewhere(stream, q):
         return _on(stream, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, out_q, out_k)
     if q.dim() < 2 or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
         raise ValueError(f"q must be [..., HQ, d] and k [..., HK, d], got {list(q.shape)} and {list(k.shape)}")
@@ -317,7 +336,14 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     ``A`` ``[D, N]``, ``D`` and ``dt_bias`` ``[D]`` fp32, states ``[B, D, N]`` fp32.  Returns ``(y, ht)``, y of
     x's type; ``ht`` may be ``h0`` itself, and is None if not given and not wanted.
     """
-    if stream is not None and (out is None or ht is None and want_state) and _elsewhere(stream, x):
+    if stream is None:
+        status = (_qz._B or _qz._binding()).selective_scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht,
+                                                           want_state, False)
+        if status is not None:
+            if status:
+                _fail(status)
+            return out, ht
+    elif (out is None or ht is None and want_state) and _elsewhere(stream, x):
         return _on(stream, selective_scan, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht, want_state)
     return _scan("gdr_selective_scan", x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht, want_state,
                  stream, *_batch(x, cu_seqlens))
@@ -329,10 +355,18 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     ``dt``, ``z`` are ``[B, D]``, ``B`` and ``C`` ``[B, N]`` or ``[B, G, N]``.  Updates ``state`` in place unless
     ``out_state`` is given.  Returns y.  ``state`` may be None (zeros; ``out_state`` then receives the new
     state if given)."""
-    if stream is not None and out is None and _elsewhere(stream, x):
+    end = state if out_state is None else out_state
+    if stream is None:
+        status = (_qz._B or _qz._binding()).selective_scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, state, None, out, end, False,
+                                                           True)
+        if status is not None:
+            if status:
+                _fail(status)
+            return out
+    elif out is None and _elsewhere(stream, x):
         return _on(stream, selective_scan_step, x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, out, out_state)
-    return _scan("gdr_selective_scan_step", x, dt, A, B, C, D, z, dt_bias, dt_softplus, state, None, out,
-                 state if out_state is None else out_state, False, stream, *_tokens(x))[0]
+    return _scan("gdr_selective_scan_step", x, dt, A, B, C, D, z, dt_bias, dt_softplus, state, None, out, end, False, stream,
+                 *_tokens(x))[0]
 
 
 def _scan(entry, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu, out, ht, want_state, stream, seqs, T, lead):

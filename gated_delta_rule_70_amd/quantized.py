@@ -81,13 +81,14 @@ def _lib():
 
 
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
-BINDING_VERSION = 1
+BINDING_VERSION = 2
 _B = None
 
 
 class _NoBinding:
     """In the extension's place where it is not built: every call goes through Python."""
     add_rmsnorm = gated_rmsnorm = matmul = staticmethod(lambda *a: None)
+    causal_conv = qk_norm_rope = selective_scan = staticmethod(lambda *a: None)
 
 
 def _binding():
@@ -96,7 +97,7 @@ def _binding():
     if _B is None:
         L = _lib()
         if not os.path.exists(BINDING_PATH):
-            warnings.warn(f"{BINDING_PATH} is not built: calls of the 8-bit operators take 3 to 5 us longer", RuntimeWarning,
+            warnings.warn(f"{BINDING_PATH} is not built: calls of the 8-bit and the layer operators take 3 to 10 us longer", RuntimeWarning,
                           stacklevel=3)
             _B = _NoBinding
             return _B
@@ -107,6 +108,8 @@ def _binding():
             raise RuntimeError(f"{BINDING_PATH} is of another version; rebuild it")
         m.bind(*(ctypes.cast(f, _VP).value for f in (L.gdr_add_rmsnorm_i8, L.gdr_gated_rmsnorm_i8, L.gdr_matmul_i8)),
                _current_device, _raw_stream)
+        m.bind_layer(*(ctypes.cast(f, _VP).value for f in (L.gdr_causal_conv, L.gdr_qk_norm_rope, L.gdr_selective_scan,
+                                                           L.gdr_selective_scan_step)))
         _B = m
     return _B
 
