@@ -29,7 +29,7 @@ import torch
 
 from . import layer, quantized
 from .layer import (causal_conv, causal_conv_step, qk_norm_rope, rope_table, selective_scan,
-                    selective_scan_step)
+                    selective_scan_step, selective_scan_workspace_bytes)
 from .quantized import add_rmsnorm_i8, gated_rmsnorm_i8, matmul_i8, quantize_rows_i8
 
 __all__ = ["decode_step", "fused_recurrent", "chunk_prefill", "chunk_prefill_noalloc", "forward",
@@ -39,7 +39,7 @@ __all__ = ["decode_step", "fused_recurrent", "chunk_prefill", "chunk_prefill_noa
            "RECURRENT_MAX_T", "TREE_MAX_T", "O_BF16",
            "add_rmsnorm_i8", "gated_rmsnorm_i8", "matmul_i8", "quantize_rows_i8",
            "causal_conv", "causal_conv_step", "qk_norm_rope", "rope_table", "selective_scan",
-           "selective_scan_step"]
+           "selective_scan_step", "selective_scan_workspace_bytes"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdr.so")
 ABI_VERSION = 8

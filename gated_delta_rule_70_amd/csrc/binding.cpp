@@ -68,7 +68,7 @@ bool stream_of(int dev, void** stream) {
 }
 
 PyObject* result(int status) {
-    if (status >= GDR_ERR_NULL && status <= GDR_ERR_ALIAS) Py_RETURN_NONE;  // nothing was enqueued
+    if (status >= GDR_ERR_NULL && status <= GDR_ERR_WORKSPACE) Py_RETURN_NONE;  // nothing was enqueued
     return PyLong_FromLong(status);
 }
 
@@ -352,14 +352,15 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
-// (x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht, want_state, step)
+// (x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht, want_state, step, workspace)
 PyObject* selective_scan(PyObject*, PyObject* const* v, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        if (n != 15 || !g_scan || !g_scan_step) return nullptr;
+        if (n != 16 || !g_scan || !g_scan_step) return nullptr;
         const at::Tensor *x = strided(v[0]), *dt = strided(v[1]), *A = dense(v[2]), *b = strided(v[3]), *c = strided(v[4]);
-        const at::Tensor *o = strided(v[11]), *skip, *z, *bias, *h0, *cu, *ht;
+        const at::Tensor *o = strided(v[11]), *skip, *z, *bias, *h0, *cu, *ht, *ws;
         if (!x || !dt || !A || !b || !c || !o || !optional(v[5], &skip) || !optional(v[6], &z, true) || !optional(v[7], &bias) ||
-            !optional(v[9], &h0) || !optional(v[10], &cu) || !optional(v[12], &ht))
+            !optional(v[9], &h0) || !optional(v[10], &cu) || !optional(v[12], &ht) ||
+            !optional(v[15], &ws))
             return nullptr;
         const int softplus = PyObject_IsTrue(v[8]);
         const bool step = v[14] == Py_True;
@@ -385,12 +386,13 @@ PyObject* selective_scan(PyObject*, PyObject* const* v, Py_ssize_t n) {
         if (!stream_of(dev.index(), &stream)) return nullptr;
         d.B = (int32_t)S, d.T = (int32_t)T, d.D = (int32_t)D, d.N = (int32_t)N, d.G = (int32_t)G;
         d.dtype = code(*x), d.dt_dtype = code(*dt), d.flags = softplus ? GDR_SCAN_DT_SOFTPLUS : 0;
+        if (ws && (ws->scalar_type() != at::kByte || ws->device() != dev)) return nullptr;
         auto f = [](const at::Tensor* t) { return static_cast<float*>(data(t)); };
         int st;
         Py_BEGIN_ALLOW_THREADS;
         st = step ? g_scan_step(&d, data(x), data(dt), f(A), data(b), data(c), f(skip), data(z), f(bias), f(h0), data(o), f(ht), stream)
                   : g_scan(&d, static_cast<const int32_t*>(data(cu)), data(x), data(dt), f(A), data(b), data(c), f(skip), data(z),
-                           f(bias), f(h0), data(o), f(ht), stream);
+                           f(bias), f(h0), data(o), f(ht), data(ws), ws ? ws->numel() : 0, stream);
         Py_END_ALLOW_THREADS;
         return result(st);
     });

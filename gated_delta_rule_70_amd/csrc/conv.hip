@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows that a thread loads at once
-constexpr int kXcds = 8;   // workgroups go round them in turn
 
 struct ConvGroups {
     int groups;                           // of eight channels; an output's last one may have fewer
@@ -122,13 +121,6 @@ __device__ __forceinline__ void head(const ConvArgs& a, const ConvGroups& c, int
 #pragma unroll
     for (int t = 0; t < P; ++t)
         if (t < len) taps.store(a, col, first + t, f + t, static_cast<const TX*>(nullptr));
-}
-
-// Work item of block b of n, so that each XCD (block b is on XCD b % 8) has a contiguous range: the
-// rows that neighbouring tiles share are then in its L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
-    const int64_t q = n / kXcds, r = n % kXcds, x = b % kXcds;
-    return x * q + (x < r ? x : r) + b / kXcds;
 }
 
 // Which of the tile's rows have their whole window in their own sequence.

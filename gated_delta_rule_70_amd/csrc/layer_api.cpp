@@ -44,15 +44,25 @@ int batch_rows(int32_t B, int32_t T, const int32_t* cu, int64_t* rows) {
     return aligned(cu, 4) ? GDR_OK : GDR_ERR_ALIGN;
 }
 
+int scan_rows(const gdr_scan_dims& d, const int32_t* cu, int64_t* rows) {
+    const int st = batch_rows(d.B, d.T, cu, rows);
+    if (st != GDR_OK) return st;
+    return d.D < 1 || d.D > GDR_LAYER_MAX_CHANNELS || d.N < 1 || d.G < 1 || d.D % d.G ? GDR_ERR_SHAPE : GDR_OK;
+}
+
+// Values of workspace.
+int64_t scan_workspace(const gdr_scan_dims& d, const ScanCut& cut) {
+    return cut.segs > 1 ? (int64_t)d.B * cut.segs * d.D * (d.N + 1) : 0;
+}
+
 int scan(const gdr_scan_dims* dims, const int32_t* cu, bool step, const void* x, const void* dt, const float* A,
          const void* B, const void* C, const float* skip, const void* z, const float* dt_bias, const float* h0,
-         void* out, float* ht, void* stream) {
+         void* out, float* ht, void* workspace, size_t workspace_bytes, void* stream) {
     if (!dims) return GDR_ERR_NULL;
     const gdr_scan_dims& d = *dims;
     int64_t rows;
-    const int st = batch_rows(d.B, d.T, cu, &rows);
+    const int st = scan_rows(d, cu, &rows);
     if (st != GDR_OK) return st;
-    if (d.D < 1 || d.D > GDR_LAYER_MAX_CHANNELS || d.N < 1 || d.G < 1 || d.D % d.G) return GDR_ERR_SHAPE;
     if (step && d.T != 1) return GDR_ERR_SHAPE;
     if (d.N > GDR_SCAN_MAX_STATES || !known_dtype(d.dtype) || (d.flags & ~GDR_SCAN_DT_SOFTPLUS) ||
         (d.dt_dtype != d.dtype && d.dt_dtype != GDR_F32))
@@ -62,7 +72,9 @@ int scan(const gdr_scan_dims* dims, const int32_t* cu, bool step, const void* x,
         return GDR_ERR_SHAPE;
     if (d.B == 0) return GDR_OK;
     const int64_t e = elt_of(d.dtype), some = rows > 0, gn = (int64_t)d.G * d.N, dn = (int64_t)d.D * d.N;
-    enum { X, DT, BB, CC, Z, AA, SKIP, BIAS, H0, OUT, HT, CU };
+    const ScanCut cut = step || rows == 0 ? ScanCut{1, 0} : scan_cut(d.B, d.T, d.D, d.G, cu != nullptr);
+    const int64_t need = scan_workspace(d, cut);
+    enum { X, DT, BB, CC, Z, AA, SKIP, BIAS, H0, OUT, HT, CU, WORK };
     Operand o[] = {{x, rows, d.D, d.x_stride, e, some != 0, {}},
                    {dt, rows, d.D, d.dt_stride, elt_of(d.dt_dtype), some != 0, {}},
                    {B, rows, gn, d.b_stride, e, some != 0, {}},
@@ -74,9 +86,13 @@ int scan(const gdr_scan_dims* dims, const int32_t* cu, bool step, const void* x,
                    {h0, d.B, dn, dn, 4, false, {}},
                    {out, rows, d.D, d.out_stride, e, some != 0, {}},
                    {ht, d.B, dn, dn, 4, false, {}},
-                   {cu, 1, (int64_t)d.B + 1, 0, 4, false, {}}};
+                   {cu, 1, (int64_t)d.B + 1, 0, 4, false, {}},
+                   {need ? workspace : nullptr, 1, need, 0, 4, false, {}}};
     const int bad = check(o);
     if (bad != GDR_OK) return bad;
+    if (need && (!workspace || workspace_bytes / 4 < (uint64_t)need)) return GDR_ERR_WORKSPACE;
+    for (int i = X; i < WORK; ++i)
+        if (overlap(o[WORK].range, o[i].range)) return GDR_ERR_ALIAS;
     for (int i : {X, DT, BB, CC, Z, AA, SKIP, BIAS, CU})
         if (overlap(o[OUT].range, o[i].range) || overlap(o[HT].range, o[i].range)) return GDR_ERR_ALIAS;
     if (overlap(o[OUT].range, o[H0].range) || overlap(o[OUT].range, o[HT].range)) return GDR_ERR_ALIAS;
@@ -94,6 +110,8 @@ int scan(const gdr_scan_dims* dims, const int32_t* cu, bool step, const void* x,
     a.A = A, a.skip = skip, a.dt_bias = dt_bias, a.h0 = h0;
     a.out = out;
     a.ht = ht;
+    a.segs = cut.segs, a.seg_len = cut.seg_len;
+    a.workspace = static_cast<float*>(workspace);
     a.stream = static_cast<hipStream_t>(stream);
     return (step ? launch_selective_scan_step(a) : launch_selective_scan(a)) == hipSuccess ? GDR_OK : GDR_ERR_HIP;
 }
@@ -224,16 +242,24 @@ int gdr_qk_norm_rope(const gdr_qk_dims* dims, const void* q, const void* k, cons
     return launch_qk_norm_rope(a) == hipSuccess ? GDR_OK : GDR_ERR_HIP;
 }
 
+size_t gdr_selective_scan_workspace_bytes(const gdr_scan_dims* dims, int packed) {
+    int64_t rows;
+    static const int32_t some = 0;
+    if (!dims || scan_rows(*dims, packed ? &some : nullptr, &rows) != GDR_OK || dims->N > GDR_SCAN_MAX_STATES || rows == 0) return 0;
+    return 4 * static_cast<size_t>(scan_workspace(*dims, scan_cut(dims->B, dims->T, dims->D, dims->G, packed != 0)));
+}
+
 int gdr_selective_scan(const gdr_scan_dims* dims, const int32_t* cu_seqlens, const void* x, const void* dt,
                        const float* A, const void* B, const void* C, const float* Dskip, const void* z,
-                       const float* dt_bias, const float* h0, void* out, float* ht, void* stream) {
-    return scan(dims, cu_seqlens, false, x, dt, A, B, C, Dskip, z, dt_bias, h0, out, ht, stream);
+                       const float* dt_bias, const float* h0, void* out, float* ht, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    return scan(dims, cu_seqlens, false, x, dt, A, B, C, Dskip, z, dt_bias, h0, out, ht, workspace, workspace_bytes, stream);
 }
 
 int gdr_selective_scan_step(const gdr_scan_dims* dims, const void* x, const void* dt, const float* A, const void* B,
                             const void* C, const float* Dskip, const void* z, const float* dt_bias,
                             const float* h0, void* out, float* ht, void* stream) {
-    return scan(dims, nullptr, true, x, dt, A, B, C, Dskip, z, dt_bias, h0, out, ht, stream);
+    return scan(dims, nullptr, true, x, dt, A, B, C, Dskip, z, dt_bias, h0, out, ht, nullptr, 0, stream);
 }
 
 }  // extern "C"

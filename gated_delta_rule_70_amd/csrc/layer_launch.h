@@ -45,8 +45,31 @@ struct ScanArgs {
     const float *A, *skip, *dt_bias, *h0;
     void* out;
     float* ht;
+    int segs, seg_len;  // segments of a sequence (1: it is run whole), and their tokens
+    float* workspace;   // segs > 1: B * segs * D * (N + 1) values
     hipStream_t stream;
 };
+
+// Segments that the sequences of a scan are cut into, by the sizes alone.
+//
+// A scan runs a token after the other in workgroups of 16 channels, 25 ns a token for one workgroup on
+// a CU and 42 for two.  Where they leave half the CUs idle, segments run side by side: first the states
+// behind each from zero, 55 % of a run's work, then each segment from its start.  Two workgroups a CU,
+// at 1.55 * 42 ns for each segment's tokens, pay from three segments on, if a sequence is long enough to
+// win back the second launch, and segments of 64 tokens or more.  In a packed batch any sequence may
+// have all rows, so each has workgroups for all of them, most of which find nothing to do: that is
+// limited.
+struct ScanCut {
+    int segs, seg_len;
+};
+inline ScanCut scan_cut(int64_t B, int64_t T, int64_t D, int64_t G, bool packed) {
+    const int64_t groups = G * ((D / G + 15) / 16), blocks = B * groups;
+    const int64_t n = 512 / blocks, mean = packed ? T / B : T;
+    if (n < 3 || mean < 512) return {1, 0};
+    const int64_t len = ((mean + n - 1) / n + 63) / 64 * 64, segs = (T + len - 1) / len;
+    if (segs < 2 || (packed && segs * blocks > 8192)) return {1, 0};
+    return {static_cast<int>(segs), static_cast<int>(len)};
+}
 
 hipError_t launch_causal_conv(const ConvArgs& a);
 hipError_t launch_qk_norm_rope(const QkArgs& a);

@@ -163,6 +163,15 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+constexpr int kXcds = 8;
+
+// Work item of block b of n, so that each XCD (block b is on XCD b % 8) has a contiguous range: what
+// neighbouring items share is then in its L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
+    const int64_t q = n / kXcds, r = n % kXcds, x = b % kXcds;
+    return x * q + (x < r ? x : r) + b / kXcds;
+}
+
 // A sequence's rows in a packed batch of T rows: clamped, so that no entry leads outside.
 struct Span {
     int first, count;

@@ -235,15 +235,21 @@ struct Tile {
     }
 };
 
-template <typename TX, typename TDT, int L, int S>
+// What a launch does: whole sequences, or sequences cut into segments of a.seg_len tokens, the
+// states behind each first (from zero, without outputs), then each segment from its start.
+enum { kWhole, kEnds, kSegments };
+
+template <typename TX, typename TDT, int L, int S, int MODE>
 __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, int tiles, int64_t block0) {
     using K = Tile<L, S>;
     constexpr int CT = K::CT, TT = K::TT, NP = K::NP;
     __shared__ float sDt[2][TT * CT], sX[2][TT * CT], sY[2][TT * CT];
     __shared__ float sB[2][K::bc], sC[2][K::bc];
 
-    const int64_t b = block0 + blockIdx.x;
-    const int seq = (int)(b / (tiles * a.G)), gt = (int)(b % (tiles * a.G));
+    const int64_t b = block0 + xcd_order(blockIdx.x, gridDim.x);
+    const int gt = (int)(b % (tiles * a.G));
+    const int64_t slot = b / (tiles * a.G);  // sequence, and segment
+    const int seq = (int)(MODE == kWhole ? slot : slot / a.segs), seg = (int)(MODE == kWhole ? 0 : slot % a.segs);
     const int g = gt / tiles, per = a.D / a.G, c0 = gt % tiles * CT;  // first channel in the group
     const int d0 = g * per + c0, left = per - c0;                     // in all; channels from there on
     int64_t first = (int64_t)seq * a.T;
@@ -251,6 +257,15 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     if (a.cu) {
         const Span s = packed_span(a.cu, seq, a.T);
         first = s.first, len = s.count;
+    }
+    bool last = true;  // segment of the sequence
+    if constexpr (MODE != kWhole) {
+        const int64_t behind = (int64_t)seg * a.seg_len;
+        if (seg > 0 && behind >= len) return;
+        last = behind + a.seg_len >= len;
+        if (MODE == kEnds && last) return;  // no segment starts from it
+        first += behind;
+        len = last ? len - (int)behind : a.seg_len;
     }
     const int tid = threadIdx.x % kThreads, N = a.N;
 
@@ -261,7 +276,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         const int gc = tid % (CT / 4) * 4, gt0 = tid / (CT / 4), gn = left - gc;
         const TX* x = static_cast<const TX*>(a.x) + (first + gt0) * a.x_stride + d0 + gc;
         const TDT* dt = static_cast<const TDT*>(a.dt) + (first + gt0) * a.dt_stride + d0 + gc;
-        const TX* z = a.z ? static_cast<const TX*>(a.z) + (first + gt0) * a.z_stride + d0 + gc : nullptr;
+        const TX* z = a.z && MODE != kEnds ? static_cast<const TX*>(a.z) + (first + gt0) * a.z_stride + d0 + gc : nullptr;
         TX* out = static_cast<TX*>(a.out) + (first + gt0) * a.out_stride + d0 + gc;
         const int bt = tid / (NP / 4), bn = tid % (NP / 4) * 4;
         const TX* B = static_cast<const TX*>(a.b) + (first + bt) * a.b_stride + (int64_t)g * N + bn;
@@ -288,7 +303,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                     rb[i] = rc[i] = Raw4<TX>{};
                     if ((bcApart * K::bc_groups == TT || bt < TT) && bn < N) {
                         rb[i] = load4(B + i * bcApart * a.b_stride, 4);
-                        rc[i] = load4(C + i * bcApart * a.c_stride, 4);
+                        if constexpr (MODE != kEnds) rc[i] = load4(C + i * bcApart * a.c_stride, 4);
                     }
                 }
             } else {
@@ -302,7 +317,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 for (int i = 0; i < K::bc_groups; ++i) {
                     const int t = bt + i * bcApart, n = t < TT && t0 + t < len ? N - bn : 0;
                     rb[i] = load4(B + i * bcApart * a.b_stride, n);
-                    rc[i] = load4(C + i * bcApart * a.c_stride, n);
+                    if constexpr (MODE != kEnds) rc[i] = load4(C + i * bcApart * a.c_stride, n);
                 }
             }
             x += TT * a.x_stride;
@@ -336,7 +351,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 for (int j = 0; j < 4; ++j) {
                     const int to = L == 16 ? (bn + j) * (TT + 4) + t : t * NP + bn + j;
                     sB[buf][to] = rb[i].get(j);
-                    sC[buf][to] = rc[i].get(j);
+                    if constexpr (MODE != kEnds) sC[buf][to] = rc[i].get(j);
                 }
             }
         };
@@ -378,7 +393,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         lds_barrier();
 #pragma unroll 1
         for (int t0 = 0, buf = 0; t0 < len; t0 += TT, buf ^= 1) {
-            if (t0 > 0) store(t0 - TT, buf ^ 1);
+            if (MODE != kEnds && t0 > 0) store(t0 - TT, buf ^ 1);
             bring_gate(t0);
             if (t0 + TT < len) {
                 stage(t0 + TT, buf ^ 1);
@@ -386,7 +401,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             }
             lds_barrier();
         }
-        if (len > 0) store((len - 1) / TT * TT, (len - 1) / TT & 1);
+        if (MODE != kEnds && len > 0) store((len - 1) / TT * TT, (len - 1) / TT & 1);
         return;
     }
 
@@ -398,9 +413,23 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     for (int s = 0; s < S; ++s) {
         const bool there = mine && lane * S + s < N;
         A[s] = there && len > 0 ? a.A[(int64_t)(d0 + c) * N + lane * S + s] * kLog2e : 0.f;
-        h[s] = there && a.h0 ? a.h0[state + s] : 0.f;
+        h[s] = there && a.h0 && MODE != kEnds ? a.h0[state + s] : 0.f;
     }
-    const float skip = mine && a.skip ? a.skip[d0 + c] : 0.f;
+    const float skip = mine && a.skip && MODE != kEnds ? a.skip[d0 + c] : 0.f;
+    // The state behind a segment, from zero, and its sum of steps lie in the workspace, [slot][D][N] and
+    // [slot][D]: with them the state before this segment follows from the sequence's first one.
+    float* const ends = a.workspace;
+    float* const steps = ends + (int64_t)a.B * a.segs * a.D * N;
+    if constexpr (MODE == kSegments) {
+        if (mine)
+            for (int64_t e = slot - seg; e < slot; ++e) {
+                const float sum = steps[e * a.D + d0 + c];
+                const float* end = ends + (e * a.D + d0 + c) * N + lane * S;
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(sum * A[s]), h[s], lane * S + s < N ? end[s] : 0.f);
+            }
+    }
     // What was loaded so far is waited for here: left to its first use in the loop, the wait would be
     // there in every pass.
 #pragma unroll
@@ -415,19 +444,23 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 f.b[s] = *reinterpret_cast<const f32x4*>(&sB[buf][(lane * S + s) * (TT + 4) + t]);
-                f.c[s] = *reinterpret_cast<const f32x4*>(&sC[buf][(lane * S + s) * (TT + 4) + t]);
+                if constexpr (MODE != kEnds) f.c[s] = *reinterpret_cast<const f32x4*>(&sC[buf][(lane * S + s) * (TT + 4) + t]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float b[S], cc[S];
                 __builtin_memcpy(b, __builtin_assume_aligned(&sB[buf][(t + i) * NP + lane * S], 4 * S), sizeof(b));
-                __builtin_memcpy(cc, __builtin_assume_aligned(&sC[buf][(t + i) * NP + lane * S], 4 * S), sizeof(cc));
+                if constexpr (MODE != kEnds) __builtin_memcpy(cc, __builtin_assume_aligned(&sC[buf][(t + i) * NP + lane * S], 4 * S), sizeof(cc));
 #pragma unroll
-                for (int s = 0; s < S; ++s) f.b[s][i] = b[s], f.c[s][i] = cc[s];
+                for (int s = 0; s < S; ++s) {
+                    f.b[s][i] = b[s];
+                    if constexpr (MODE != kEnds) f.c[s][i] = cc[s];
+                }
             }
         }
     };
+    float sum = 0.f;  // of this lane's steps
     auto compute = [&](int buf) {
         // operands from LDS are read one group of four tokens (step and x one chunk) ahead, into two
         // sets of registers in turn
@@ -443,6 +476,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 const int after = here + L < TT ? here + L : 0;  // nothing is done with what is read behind the last chunk
                 const float step1 = sDt[buf][K::at(after + lane, c)], xv1 = sX[buf][K::at(after + lane, c)];
                 const float in = step * xv;
+                if constexpr (MODE == kEnds) sum += step;
                 float p[L];
                 unrolled(std::make_integer_sequence<int, L>{}, [&](auto j) {
                     constexpr int J = decltype(j)::value;
@@ -452,10 +486,10 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
                         h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(sj * A[s]), h[s], ij * now.b[s][J % 4]);
-                        p[J] = s ? __builtin_fmaf(now.c[s][J % 4], h[s], p[J]) : now.c[s][J % 4] * h[s];
+                        if constexpr (MODE != kEnds) p[J] = s ? __builtin_fmaf(now.c[s][J % 4], h[s], p[J]) : now.c[s][J % 4] * h[s];
                     }
                 });
-                sY[buf][K::at(here + lane, c)] = __builtin_fmaf(skip, xv, sum_scatter<L>(p, lane));
+                if constexpr (MODE != kEnds) sY[buf][K::at(here + lane, c)] = __builtin_fmaf(skip, xv, sum_scatter<L>(p, lane));
                 step = step1, xv = xv1;
             }
         }
@@ -467,10 +501,25 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         compute(buf);
         lds_barrier();
     }
-    if (a.ht && mine)
+    if constexpr (MODE == kEnds) {
+        sum += dpp_mov<0xB1>(sum);  // quad_perm [1,0,3,2]
+        sum += dpp_mov<0x4E>(sum);  // quad_perm [2,3,0,1]
+        if constexpr (L == 16) {
+            sum += dpp_mov<0x141>(sum);  // row_half_mirror
+            sum += dpp_mov<0x140>(sum);  // row_mirror
+        }
+        if (mine) {
+            if (lane == 0) steps[slot * a.D + d0 + c] = sum;
+            float* end = ends + (slot * a.D + d0 + c) * N + lane * S;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (lane * S + s < N) end[s] = h[s];
+        }
+    } else if (a.ht && mine && last) {
 #pragma unroll
         for (int s = 0; s < S; ++s)
             if (lane * S + s < N) a.ht[state + s] = h[s];
+    }
 }
 
 bool valid(const ScanArgs& a) {
@@ -517,15 +566,36 @@ template <typename TX, typename TDT, int L, int S>
 hipError_t launch_tiles(const ScanArgs& a) {
     constexpr int CT = Tile<L, S>::CT;
     const int tiles = (a.D / a.G + CT - 1) / CT;
-    return by_blocks((int64_t)a.B * a.G * tiles, 2 * kThreads, [&](int64_t first, unsigned count) {
-        hipLaunchKernelGGL((scan_kernel<TX, TDT, L, S>), dim3(count), dim3(2 * kThreads), 0, a.stream, a, tiles, first);
-    });
+    auto go = [&](int64_t slots, auto kernel) {
+        return by_blocks(slots * a.G * tiles, 2 * kThreads, [&](int64_t first, unsigned count) {
+            hipLaunchKernelGGL(kernel, dim3(count), dim3(2 * kThreads), 0, a.stream, a, tiles, first);
+        });
+    };
+    if constexpr (L == 16) {
+        if (a.segs > 1) {
+            const hipError_t e = go((int64_t)a.B * a.segs, scan_kernel<TX, TDT, L, S, kEnds>);
+            return e != hipSuccess ? e : go((int64_t)a.B * a.segs, scan_kernel<TX, TDT, L, S, kSegments>);
+        }
+    }
+    return go(a.B, scan_kernel<TX, TDT, L, S, kWhole>);
+}
+
+// Lanes for a channel.  ns a token, by workgroups for each CU (each of the dense batch's sequences as
+// long; 256 CUs): 16 lanes, workgroups of 16 channels: 25, 42, 60, 78, 116 for 1, 2, 3, 4, 6; 4 lanes, workgroups
+// of 64 channels, N = 16: 74, 135, 270 for 1, 2, 4, N = 8: 103 for 2.  So 4 lanes take less where they
+// fill the CUs evenly: 4 x 2048 x 4096 152 us (16 lanes 161), 6 x 1024 x 4096 133 (119), 8 x 512 x 4096
+// 69 (81).  Sequences of a packed batch end at different times: there only from four workgroups a CU on.
+bool few_lanes(const ScanArgs& a) {
+    if (a.N > 16 || a.segs > 1) return false;
+    const int64_t per = a.D / a.G, wide = a.B * a.G * ((per + 63) / 64), narrow = a.B * a.G * ((per + 15) / 16);
+    if (a.cu) return wide >= 1024;
+    const int64_t rounds4 = (wide + 255) / 256, rounds16 = (narrow + 255) / 256;
+    return rounds4 * (a.N > 8 ? 67 : 51) < rounds16 * 19;
 }
 
 template <typename TX, typename TDT>
 hipError_t launch(const ScanArgs& a) {
-    if (a.N <= 16 && (int64_t)a.B * a.D >= 32768)
-        return a.N <= 8 ? launch_tiles<TX, TDT, 4, 2>(a) : launch_tiles<TX, TDT, 4, 4>(a);
+    if (few_lanes(a)) return a.N <= 8 ? launch_tiles<TX, TDT, 4, 2>(a) : launch_tiles<TX, TDT, 4, 4>(a);
     if (a.N <= 16) return launch_tiles<TX, TDT, 16, 1>(a);
     if (a.N <= 32) return launch_tiles<TX, TDT, 16, 2>(a);
     if (a.N <= 64) return launch_tiles<TX, TDT, 16, 4>(a);
@@ -535,7 +605,7 @@ hipError_t launch(const ScanArgs& a) {
 }  // namespace
 
 hipError_t launch_selective_scan(const ScanArgs& a) {
-    if (!valid(a)) return hipErrorInvalidValue;
+    if (!valid(a) || a.segs < 1 || (a.segs > 1 && (!a.workspace || a.seg_len < 1))) return hipErrorInvalidValue;
     if (!a.bf16) return launch<float, float>(a);
     return a.dt_bf16 ? launch<bf16_t, bf16_t>(a) : launch<bf16_t, float>(a);
 }

@@ -31,7 +31,7 @@ from . import quantized as _qz
 from .quantized import _code, _elsewhere, _eps, _fail, _on, _rows, _stream
 
 __all__ = ["causal_conv", "causal_conv_step", "qk_norm_rope", "rope_table", "selective_scan", "selective_scan_step",
-           "CONV_MAX_OUT", "SCAN_MAX_STATES", "QK_MAX_DIM"]
+           "selective_scan_workspace_bytes",           "CONV_MAX_OUT", "SCAN_MAX_STATES", "QK_MAX_DIM"]
 
 CONV_MAX_OUT = 8        # most separate outputs of one convolution
 SCAN_MAX_STATES = 128   # most state values of a channel
@@ -71,11 +71,13 @@ _NONE = (0,) * CONV_MAX_OUT
 
 def bind(L):
     """Argument types of the entry points of gdr_layer.h on the loaded library."""
-    for name, n in (("gdr_causal_conv", 9), ("gdr_qk_norm_rope", 11), ("gdr_selective_scan", 14),
+    for name, n in (("gdr_causal_conv", 9), ("gdr_qk_norm_rope", 11), ("gdr_selective_scan", 16),
                     ("gdr_selective_scan_step", 13)):
         fn = getattr(L, name)
         fn.restype = ctypes.c_int
-        fn.argtypes = [_VP] * n
+        fn.argtypes = [ctypes.c_size_t if (name, i) == ("gdr_selective_scan", 14) else _VP for i in range(n)]
+    L.gdr_selective_scan_workspace_bytes.restype = ctypes.c_size_t
+    L.gdr_selective_scan_workspace_bytes.argtypes = [_VP, ctypes.c_int]
 
 
 def _ptr(t):
@@ -325,7 +327,7 @@ _QK_NAMES = ("q", "k", "q_weight", "k_weight", "cos", "sin", "positions", "out_q
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False, h0=None, cu_seqlens=None,
-                   out=None, ht=None, want_state: bool = True, stream=None):
+                   out=None, ht=None, want_state: bool = True, stream=None, workspace=None):
     """The recurrence with a diagonal, input-dependent transition over prompts (gdr_selective_scan).
 
     With ``step = dt + dt_bias`` (softplus of it with ``dt_softplus``), for every channel and its state
@@ -335,18 +337,30 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     ``[B, T, N]`` or ``[B, T, G, N]`` of x's type (groups of D / G channels share them; N at most 128),
     ``A`` ``[D, N]``, ``D`` and ``dt_bias`` ``[D]`` fp32, states ``[B, D, N]`` fp32.  Returns ``(y, ht)``, y of
     x's type; ``ht`` may be ``h0`` itself, and is None if not given and not wanted.
+
+    Long sequences of few channels need a workspace (see :func:`selective_scan_workspace_bytes`), a contiguous
+    uint8 tensor on x's GPU; one is allocated if it is None.  Calls that overlap in time, or graphs
+    replayed so, need one each.
     """
     if stream is None:
         status = (_qz._B or _qz._binding()).selective_scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht,
-                                                           want_state, False)
+                                                           want_state, False, workspace)
         if status is not None:
             if status:
                 _fail(status)
             return out, ht
     elif (out is None or ht is None and want_state) and _elsewhere(stream, x):
-        return _on(stream, selective_scan, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht, want_state)
+        return _on(stream, selective_scan, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht, want_state,
+                   None, workspace)
     return _scan("gdr_selective_scan", x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht, want_state,
-                 stream, *_batch(x, cu_seqlens))
+                 stream, workspace, *_batch(x, cu_seqlens))
+
+
+def selective_scan_workspace_bytes(B, T, D, N, groups: int = 1, packed: bool = False) -> int:
+    """Bytes of workspace that :func:`selective_scan` needs for B sequences of T tokens (``packed``: T rows in
+    all), D channels and N state values; 0 for most sizes."""
+    dims = _SCAN.pack(B, T, D, N, groups, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    return int(_qz._lib().gdr_selective_scan_workspace_bytes(dims, 1 if packed else 0))
 
 
 def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus: bool = False, out=None,
@@ -358,7 +372,7 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     end = state if out_state is None else out_state
     if stream is None:
         status = (_qz._B or _qz._binding()).selective_scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, state, None, out, end, False,
-                                                           True)
+                                                           True, None)
         if status is not None:
             if status:
                 _fail(status)
@@ -366,10 +380,10 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     elif out is None and _elsewhere(stream, x):
         return _on(stream, selective_scan_step, x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, out, out_state)
     return _scan("gdr_selective_scan_step", x, dt, A, B, C, D, z, dt_bias, dt_softplus, state, None, out, end, False, stream,
-                 *_tokens(x))[0]
+                 None, *_tokens(x))[0]
 
 
-def _scan(entry, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu, out, ht, want_state, stream, seqs, T, lead):
+def _scan(entry, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu, out, ht, want_state, stream, workspace, seqs, T, lead):
     shape, dtype = x.shape, x.dtype
     ch = shape[-1]
     xc = _code(x, "x")
@@ -401,13 +415,32 @@ def _scan(entry, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu, out, ht, wa
     tail = len(gshape) - len(lead)
     dims = _SCAN.pack(seqs, T, ch, N, G, xc, _code(dt, "dt"), 1 if dt_softplus else 0, _stride(x, "x"), _stride(dt, "dt"),
                       0 if z is None else _stride(z, "z"), _stride(B, "B", tail), _stride(C, "C", tail), _stride(out, "out"))
-    s = _stream(stream, x.get_device(), _SCAN_NAMES, (x, dt, A, B, C, D, z, dt_bias, h0, cu, out, ht))
-    head = (dims,) if entry == "gdr_selective_scan_step" else (dims, _ptr(cu))
-    status = getattr(_qz._lib(), entry)(*head, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                                        _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), out.data_ptr(), _ptr(ht), s)
+    step = entry == "gdr_selective_scan_step"
+    need = 0 if step else _qz._lib().gdr_selective_scan_workspace_bytes(dims, cu is not None)
+    if workspace is None and need:
+        workspace = _workspace(need, x, stream)
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8:
+            raise TypeError(f"workspace must be torch.uint8, got {workspace.dtype}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    s = _stream(stream, x.get_device(), _SCAN_NAMES, (x, dt, A, B, C, D, z, dt_bias, h0, cu, out, ht, workspace))
+    ptrs = [_ptr(t) for t in (x, dt, A, B, C, D, z, dt_bias, h0, out, ht)]
+    if step:
+        status = _qz._lib().gdr_selective_scan_step(dims, *ptrs, s)
+    else:
+        status = _qz._lib().gdr_selective_scan(dims, _ptr(cu), *ptrs, _ptr(workspace),
+                                               0 if workspace is None else workspace.numel(), s)
     if status:
         _fail(status)
     return out, ht
 
 
-_SCAN_NAMES = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0", "cu_seqlens", "out", "ht")
+def _workspace(need, x, stream):
+    """Memory of the stream that writes it."""
+    def make():
+        return torch.empty(need, dtype=torch.uint8, device=x.device)
+    return make() if stream is None or not _elsewhere(stream, x) else _on(stream, make)
+
+
+_SCAN_NAMES = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0", "cu_seqlens", "out", "ht", "workspace")

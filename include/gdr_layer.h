@@ -132,7 +132,16 @@ typedef struct {
  */
 int gdr_selective_scan(const gdr_scan_dims* dims, const int32_t* cu_seqlens, const void* x, const void* dt,
                        const float* A, const void* B, const void* C, const float* Dskip, const void* z,
-                       const float* dt_bias, const float* h0, void* out, float* ht, void* stream);
+                       const float* dt_bias, const float* h0, void* out, float* ht, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of device workspace gdr_selective_scan needs for these dims, `packed` saying whether the call
+ * has cu_seqlens (0 for most dims, and for invalid ones; then `workspace` may be NULL).  Long sequences
+ * of few channels are cut into segments that run side by side; the workspace, 4-byte aligned, holds the
+ * state behind each.  Its contents on entry are ignored; calls that overlap in time need one each.
+ */
+size_t gdr_selective_scan_workspace_bytes(const gdr_scan_dims* dims, int packed);
 
 /* One token for each of B sequences (T must be 1): the same formulas, each state value read once
  * and written once.  Normally called in place (ht == h0). */

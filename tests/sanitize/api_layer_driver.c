@@ -32,7 +32,7 @@ static int64_t pick(const int64_t* v, int n) { return v[rnd() % (uint64_t)n]; }
 #define CHANNELS PICK(1, 64, 64, 96, 4096, 1 << 24, (1 << 24) + 1, INT32_MAX, 0, -1)
 #define MAYBE(p) (rnd() % 4 ? (p) : NULL)
 
-static int known(int s) { return (s >= GDR_OK && s <= GDR_ERR_ALIAS) || s == GDR_ERR_HIP; }
+static int known(int s) { return s >= GDR_OK && s <= GDR_ERR_HIP; }
 
 int main(void) {
     int reached[4] = {0, 0, 0, 0};
@@ -75,8 +75,11 @@ int main(void) {
             const void *x = MAYBE(P(0)), *dt = MAYBE(P(1)), *B = MAYBE(P(3)), *C = MAYBE(P(4)), *z = MAYBE(P(6));
             const float *A = MAYBE(P(2)), *skip = MAYBE(P(5)), *bias = MAYBE(P(7));
             void* out = MAYBE(P(PICK(10, 10, 6)));
+            void* ws = MAYBE(P(PICK(12, 12, 3)));
+            (void)gdr_selective_scan_workspace_bytes(&c, step);
             const int u = step ? gdr_selective_scan_step(&c, x, dt, A, B, C, skip, z, bias, h0, out, ht, NULL)
-                               : gdr_selective_scan(&c, rnd() % 3 ? NULL : P(11), x, dt, A, B, C, skip, z, bias, h0, out, ht, NULL);
+                               : gdr_selective_scan(&c, rnd() % 3 ? NULL : P(11), x, dt, A, B, C, skip, z, bias, h0, out, ht, ws,
+                                                    (size_t)PICK(0, 1 << 20, INT64_MAX), NULL);
             CHECK(known(u));
             reached[2 + step] += u == GDR_ERR_HIP;
         }

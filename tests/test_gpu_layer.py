@@ -267,6 +267,14 @@ def test_qk_magnitudes(dtype, d):
         check_qk(got, qr, k, qw, kw, cos, sin, pos, eps, False)
 
 
+@pytest.mark.parametrize("rows,HQ,HK,d", [(11000, 3, 1, 512), (2100, 5, 3, 16)])
+def test_qk_many_heads(rows, HQ, HK, d):
+    """Enough heads for two groups a lane, the last one with fewer."""
+    note(f"qk_norm_rope {rows}x{HQ}+{HK}x{d}")
+    q, k, qw, kw, cos, sin, pos = qk_inputs((rows,), HQ, HK, d, 16, BF, F32, I32, seed=5)
+    check_qk(gdr.qk_norm_rope(q, k, qw, kw, cos, sin, positions=pos), q, k, qw, kw, cos, sin, pos, 1e-6, False)
+
+
 def test_qk_length_one():
     """Keys of length one, as the delta rule takes them."""
     q, k, _, _, _, _, _ = qk_inputs((31,), 4, 4, 64, 0, F32, None, None, seed=4)
@@ -346,6 +354,66 @@ def test_scan_packed(lens, xt, D, N, G):
     assert (y[:front] == SENTINEL).all() and (y[front + T:] == SENTINEL).all()
 
 
+SEGMENTS = [
+    # B, T, D, N, G, x
+    (1, 1000, 40, 16, 1, BF),
+    (1, 4099, 24, 5, 3, F32),
+    (3, 513, 70, 40, 1, F32),
+    (2, 700, 17, 128, 1, BF),
+    (1, 576, 33, 64, 1, F32),
+]
+
+
+@pytest.mark.parametrize("B,T,D,N,G,xt", SEGMENTS)
+def test_scan_in_segments(B, T, D, N, G, xt):
+    """Long sequences of few channels, that are cut; the workspace is given, or made, and may hold anything."""
+    note(f"selective_scan in segments {B}x{T}x{D} N={N} G={G} {xt}")
+    need = gdr.selective_scan_workspace_bytes(B, T, D, N, groups=G)
+    assert need > 0
+    a = scan_inputs((B, T), B, D, N, G, xt, F32, True, True, True, True, True, seed=9)
+    a["dt_bias"] -= 2  # states that last for segments
+    want, bound, end, end_bound = scan_reference(a)
+    y, ht = gdr.selective_scan(**a)
+    ref.close(y, want, bound)
+    ref.close(ht, end, end_bound)
+    room = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    y2, ht2 = gdr.selective_scan(**a, workspace=room[32:need + 32], ht=a["h0"])
+    assert torch.equal(y2, y) and torch.equal(ht2, ht) and (room[:32] == 255).all() and (room[need + 32:] == 255).all()
+    a["h0"] = None
+    want, bound, end, end_bound = scan_reference(a)
+    y, ht = gdr.selective_scan(**a)
+    ref.close(y, want, bound)
+    ref.close(ht, end, end_bound)
+
+
+@pytest.mark.parametrize("lens", [[0, 1500, 3, 64, 700, 0], [2400], [800, 801, 799], [1, 1, 2300]])
+@pytest.mark.parametrize("xt,D,N,G", [(BF, 40, 16, 1), (F32, 24, 5, 3)])
+def test_scan_packed_in_segments(lens, xt, D, N, G):
+    note(f"packed selective_scan in segments {lens} {xt} D={D} N={N}")
+    front, back, T = 3, 900, sum(lens)
+    assert gdr.selective_scan_workspace_bytes(len(lens), front + T + back, D, N, groups=G, packed=True) > 0
+    a = scan_inputs((front + T + back,), len(lens), D, N, G, xt, xt, True, True, True, True, True, seed=10)
+    a["dt_bias"] -= 2
+    out = torch.full_like(a["x"], SENTINEL)
+    y, ht = gdr.selective_scan(**a, cu_seqlens=cu_of(lens, front), out=out)
+    cut = {k: v[front:front + T] if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+    want, bound, end, end_bound = scan_reference(cut, lens)
+    ref.close(y[front:front + T], want, bound)
+    ref.close(ht, end, end_bound)
+    assert (y[:front] == SENTINEL).all() and (y[front + T:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("B,T,D,N,xt", [(17, 40, 1000, 16, BF), (64, 21, 520, 7, F32), (30, 35, 1090, 12, BF)])
+def test_scan_of_many_channels(B, T, D, N, xt):
+    """Four lanes for a channel."""
+    note(f"selective_scan {B}x{T}x{D} N={N} {xt}")
+    a = scan_inputs((B, T), B, D, N, 1, xt, xt, True, True, True, True, True, seed=11)
+    want, bound, end, end_bound = scan_reference(a)
+    y, ht = gdr.selective_scan(**a)
+    ref.close(y, want, bound)
+    ref.close(ht, end, end_bound)
+
+
 def test_scan_strided_and_in_place():
     """Inputs as column ranges of wider arrays, the output into one, the state in place."""
     note("strided selective_scan")
@@ -364,7 +432,8 @@ def test_scan_strided_and_in_place():
 
 
 @pytest.mark.parametrize("B,D,N,G,xt,dtt", [(1, 4096, 16, 1, BF, BF), (33, 72, 16, 2, BF, F32), (5, 37, 10, 1, F32, F32),
-                                            (70, 64, 64, 1, BF, BF), (3, 20, 128, 4, F32, F32), (2, 9, 1, 1, BF, BF), (17, 130, 7, 1, BF, BF)])
+                                            (70, 64, 64, 1, BF, BF), (3, 20, 128, 4, F32, F32), (2, 9, 1, 1, BF, BF), (17, 130, 7, 1, BF, BF),
+                                            (8195, 5, 8, 1, BF, BF), (9, 40, 4, 1, F32, F32), (6, 30, 28, 2, BF, BF)])
 def test_scan_step(B, D, N, G, xt, dtt):
     """Token by token within the whole sequence's bounds, the state in place."""
     note(f"selective_scan_step {B}x{D} N={N} G={G} {xt}")

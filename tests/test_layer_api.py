@@ -14,7 +14,7 @@ from gated_delta_rule_70_amd import layer
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "gdr_layer.h")
-OK, ENULL, ESHAPE, EUNSUP, EALIGN, EALIAS = range(6)
+OK, ENULL, ESHAPE, EUNSUP, EALIGN, EALIAS, EWS = range(7)
 BASE, SLOT = 1 << 40, 1 << 34
 BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 
@@ -116,13 +116,13 @@ def scan(L, step=False, **kw):
     d = dict(B=2, T=1 if step else 5, D=64, N=16, G=2, dtype=0, dt_dtype=0, flags=1, x_stride=64, dt_stride=64, z_stride=64, b_stride=32,
              c_stride=32, out_stride=64)
     p = dict(cu=None, x=addr(0), dt=addr(1), A=addr(2), B_=addr(3), C=addr(4), skip=addr(5), z=addr(6), bias=addr(7), h0=addr(8),
-             out=addr(9), ht=addr(10))
+             out=addr(9), ht=addr(10), ws=None, ws_bytes=0)
     p.update(split(kw, d))
     dims = layer.ScanDims(**d)
     rest = [p[n] for n in ("x", "dt", "A", "B_", "C", "skip", "z", "bias", "h0", "out", "ht")]
     if step:
         return L.gdr_selective_scan_step(ctypes.addressof(dims), *rest, None)
-    return L.gdr_selective_scan(ctypes.addressof(dims), p["cu"], *rest, None)
+    return L.gdr_selective_scan(ctypes.addressof(dims), p["cu"], *rest, p["ws"], p["ws_bytes"], None)
 
 
 BOTH = [
@@ -150,7 +150,37 @@ def test_scan_refusals(L, step, want, kw):
 ])
 def test_prompt_scan_refusals(L, want, kw):
     assert scan(L, **kw) == want
-    assert L.gdr_selective_scan(None, *[None] * 13) == ENULL
+    assert L.gdr_selective_scan(None, *[None] * 13, 0, None) == ENULL
+
+
+LONG = dict(B=1, T=4096, N=16, D=64, G=1, b_stride=16, c_stride=16)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (EWS, dict(ws=None)), (EWS, dict(ws=addr(12), ws_bytes=-1)), (EALIGN, dict(ws=addr(12, 2))), (EALIAS, dict(ws=addr(0))),
+    (EALIAS, dict(ws=addr(9))), (EALIAS, dict(ws=addr(8))), (EALIAS, dict(ws=addr(10))),
+])
+def test_scan_workspace_refusals(L, want, kw):
+    need = gdr.selective_scan_workspace_bytes(1, 4096, 64, 16)
+    assert need > 0
+    kw = {"ws_bytes": need, **kw}
+    if kw["ws_bytes"] < 0:
+        kw["ws_bytes"] += need
+    assert scan(L, **LONG, **kw) == want
+
+
+def test_scan_workspace():
+    """Only where channels are few and sequences long; what is needed never passes what the entries of
+    cu_seqlens could ask for."""
+    size = gdr.selective_scan_workspace_bytes
+    assert size(1, 4097, 4096, 16) == 0 and size(8, 512, 4096, 16) == 0 and size(1, 64, 64, 16) == 0
+    assert size(0, 100, 64, 16) == 0 and size(1, 100, 63, 16, groups=2) == 0 and size(1, 4096, 64, 129) == 0
+    for B, T, D, N, G, packed in ((1, 4096, 64, 16, 1, False), (2, 100000, 300, 5, 3, False), (4, 8192, 128, 16, 1, True)):
+        n = size(B, T, D, N, groups=G, packed=packed)
+        assert n > 0 and n % (4 * B * D * (N + 1)) == 0
+        segs = n // (4 * B * D * (N + 1))
+        assert 2 <= segs <= T // 64 + 1
+    assert size(4096, 1 << 20, 64, 16, packed=True) == 0
 
 
 @pytest.mark.parametrize("T", [0, 2])
