@@ -189,16 +189,41 @@ __device__ __forceinline__ float broadcast(float x) {
 template <int L>
 __device__ __forceinline__ float sum_scatter(float (&p)[L], int lane) {
     if constexpr (L == 16) {
+        // The halves are lanes of four banks each, so an addition to some banks only makes the choice: two
+        // instructions for a value instead of three.  s_nop: a DPP operand must be two cycles old.
+        float r[8], q[4];
+        asm("s_nop 1\n"
+            "v_add_f32_dpp %0, %8, %8 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %0, %16, %16 row_mirror row_mask:0xf bank_mask:0xc\n"
+            "v_add_f32_dpp %1, %9, %9 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %1, %17, %17 row_mirror row_mask:0xf bank_mask:0xc\n"
+            "v_add_f32_dpp %2, %10, %10 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %2, %18, %18 row_mirror row_mask:0xf bank_mask:0xc\n"
+            "v_add_f32_dpp %3, %11, %11 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %3, %19, %19 row_mirror row_mask:0xf bank_mask:0xc\n"
+            "v_add_f32_dpp %4, %12, %12 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %4, %20, %20 row_mirror row_mask:0xf bank_mask:0xc\n"
+            "v_add_f32_dpp %5, %13, %13 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %5, %21, %21 row_mirror row_mask:0xf bank_mask:0xc\n"
+            "v_add_f32_dpp %6, %14, %14 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %6, %22, %22 row_mirror row_mask:0xf bank_mask:0xc\n"
+            "v_add_f32_dpp %7, %15, %15 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %7, %23, %23 row_mirror row_mask:0xf bank_mask:0xc\n"
+            : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+            : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(p[4]), "v"(p[5]), "v"(p[6]), "v"(p[7]), "v"(p[8]), "v"(p[9]), "v"(p[10]), "v"(p[11]), "v"(p[12]), "v"(p[13]), "v"(p[14]), "v"(p[15]));
+        asm("s_nop 1\n"
+            "v_add_f32_dpp %0, %4, %4 row_half_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %0, %8, %8 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+            "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %1, %9, %9 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+            "v_add_f32_dpp %2, %6, %6 row_half_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %2, %10, %10 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+            "v_add_f32_dpp %3, %7, %7 row_half_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %3, %11, %11 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+            : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3])
+            : "v"(r[0]), "v"(r[1]), "v"(r[2]), "v"(r[3]), "v"(r[4]), "v"(r[5]), "v"(r[6]), "v"(r[7]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float keep = lane & 8 ? p[i + 8] : p[i], send = lane & 8 ? p[i] : p[i + 8];
-            p[i] = keep + dpp_mov<0x140>(send);  // row_mirror
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float keep = lane & 4 ? p[i + 4] : p[i], send = lane & 4 ? p[i] : p[i + 4];
-            p[i] = keep + dpp_mov<0x141>(send);  // row_half_mirror
-        }
+        for (int i = 0; i < 4; ++i) p[i] = q[i];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -223,11 +248,16 @@ __device__ __forceinline__ void unrolled(std::integer_sequence<int, J...>, F f) 
 template <int L, int S>
 struct Tile {
     static constexpr int CT = kThreads / L;
-    static constexpr int TT = L == 4 ? 32 : S == 1 ? 64 : S <= 4 ? 32 : 16;  // for 64 KB of LDS at most
+    static constexpr int TT = L == 4 ? 32 : S <= 2 ? 64 : S == 4 ? 48 : 16;  // two workgroups share a CU's LDS
     static constexpr int NP = L * S;                                         // states, padded with zeros
     static constexpr int bc = L == 16 ? NP * (TT + 4) : TT * NP;
     static constexpr int groups = (TT * CT / 4 + kThreads - 1) / kThreads;   // of four channels, for a thread to bring
     static constexpr int bc_groups = (TT * NP / 4 + kThreads - 1) / kThreads;  // of four states
+    // Where token t's state n lies (L = 16: the states of neighbouring lanes in neighbouring rows, which
+    // are four words apart in their banks).
+    static __device__ __forceinline__ int at_state(int t, int n) {
+        return L == 16 ? (n % S * 16 + n / S) * (TT + 4) + t : t * NP + n;
+    }
     // Where token t's channel c lies: channels are exchanged in fours so that the lanes of a wave,
     // on L tokens of 64 / L channels, meet no bank twice.
     static __device__ __forceinline__ int at(int t, int c) {
@@ -281,8 +311,11 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         const int bt = tid / (NP / 4), bn = tid % (NP / 4) * 4;
         const TX* B = static_cast<const TX*>(a.b) + (first + bt) * a.b_stride + (int64_t)g * N + bn;
         const TX* C = static_cast<const TX*>(a.c) + (first + bt) * a.c_stride + (int64_t)g * N + bn;
-        Raw4<TX> rx[K::groups], rz[K::groups], rb[K::bc_groups], rc[K::bc_groups];
-        Raw4<TDT> rdt[K::groups];
+        struct Held {  // of a tile, on its way
+            Raw4<TX> x[K::groups], b[K::bc_groups], c[K::bc_groups];
+            Raw4<TDT> dt[K::groups];
+        } held[2];
+        Raw4<TX> gates[2][K::groups];
         float bias[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) bias[i] = a.dt_bias && i < gn ? a.dt_bias[d0 + gc + i] : 0.f;
@@ -290,34 +323,35 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         // Tiles of nothing but whole groups are loaded and stored without looking at their ends: a branch
         // around a load makes the next instructions wait for it.
         const bool whole = left >= CT && N % 4 == 0;
-        auto bring = [&](int t0) {  // the tile at t0, on which the pointers stand
+        auto bring = [&](int t0, Held& r) {  // the tile at t0, on which the pointers stand
+            if (t0 >= len) return;
             if (whole && t0 + TT <= len) {
 #pragma unroll
                 for (int i = 0; i < K::groups; ++i)
                     if (rowsApart * K::groups == TT || gt0 < TT) {
-                        rx[i] = load4(x + i * rowsApart * a.x_stride, 4);
-                        rdt[i] = load4(dt + i * rowsApart * a.dt_stride, 4);
+                        r.x[i] = load4(x + i * rowsApart * a.x_stride, 4);
+                        r.dt[i] = load4(dt + i * rowsApart * a.dt_stride, 4);
                     }
 #pragma unroll
                 for (int i = 0; i < K::bc_groups; ++i) {
-                    rb[i] = rc[i] = Raw4<TX>{};
+                    r.b[i] = r.c[i] = Raw4<TX>{};
                     if ((bcApart * K::bc_groups == TT || bt < TT) && bn < N) {
-                        rb[i] = load4(B + i * bcApart * a.b_stride, 4);
-                        if constexpr (MODE != kEnds) rc[i] = load4(C + i * bcApart * a.c_stride, 4);
+                        r.b[i] = load4(B + i * bcApart * a.b_stride, 4);
+                        if constexpr (MODE != kEnds) r.c[i] = load4(C + i * bcApart * a.c_stride, 4);
                     }
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < K::groups; ++i) {
                     const int t = gt0 + i * rowsApart, n = t < TT && t0 + t < len ? gn : 0;
-                    rx[i] = load4(x + i * rowsApart * a.x_stride, n);
-                    rdt[i] = load4(dt + i * rowsApart * a.dt_stride, n);
+                    r.x[i] = load4(x + i * rowsApart * a.x_stride, n);
+                    r.dt[i] = load4(dt + i * rowsApart * a.dt_stride, n);
                 }
 #pragma unroll
                 for (int i = 0; i < K::bc_groups; ++i) {
                     const int t = bt + i * bcApart, n = t < TT && t0 + t < len ? N - bn : 0;
-                    rb[i] = load4(B + i * bcApart * a.b_stride, n);
-                    if constexpr (MODE != kEnds) rc[i] = load4(C + i * bcApart * a.c_stride, n);
+                    r.b[i] = load4(B + i * bcApart * a.b_stride, n);
+                    if constexpr (MODE != kEnds) r.c[i] = load4(C + i * bcApart * a.c_stride, n);
                 }
             }
             x += TT * a.x_stride;
@@ -325,7 +359,8 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             B += TT * a.b_stride;
             C += TT * a.c_stride;
         };
-        auto stage = [&](int t0, int buf) {
+        auto stage = [&](int t0, int buf, const Held& r) {
+            if (t0 >= len) return;
 #pragma unroll
             for (int i = 0; i < K::groups; ++i) {
                 const int t = gt0 + i * rowsApart;
@@ -333,8 +368,8 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 f32x4 sv, xv;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    sv[j] = rdt[i].get(j) + bias[j];
-                    xv[j] = rx[i].get(j);
+                    sv[j] = r.dt[i].get(j) + bias[j];
+                    xv[j] = r.x[i].get(j);
                 }
                 if (a.softplus)
 #pragma unroll
@@ -349,14 +384,14 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 if (t >= TT) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int to = L == 16 ? (bn + j) * (TT + 4) + t : t * NP + bn + j;
-                    sB[buf][to] = rb[i].get(j);
-                    if constexpr (MODE != kEnds) sC[buf][to] = rc[i].get(j);
+                    const int to = K::at_state(t, bn + j);
+                    sB[buf][to] = r.b[i].get(j);
+                    if constexpr (MODE != kEnds) sC[buf][to] = r.c[i].get(j);
                 }
             }
         };
-        auto bring_gate = [&](int t0) {
-            if (!z) return;
+        auto bring_gate = [&](int t0, Raw4<TX>(&rz)[K::groups]) {
+            if (!z || t0 >= len) return;
 #pragma unroll
             for (int i = 0; i < K::groups; ++i) {
                 const int t = gt0 + i * rowsApart;
@@ -368,7 +403,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             }
             z += TT * a.z_stride;
         };
-        auto store = [&](int t0, int buf) {
+        auto store = [&](int t0, int buf, const Raw4<TX>(&rz)[K::groups]) {
 #pragma unroll
             for (int i = 0; i < K::groups; ++i) {
                 const int t = gt0 + i * rowsApart;
@@ -385,23 +420,34 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             out += TT * a.out_stride;
         };
 
-        if (len > 0) {
-            bring(0);
-            stage(0, 0);
-            if (TT < len) bring(TT);
-        }
+        // Two tiles are on their way while one is computed: at 25 ns a token a tile of 64 takes 1.6 us, not
+        // much more than memory's latency.
+        bring(0, held[0]);
+        stage(0, 0, held[0]);
+        bring(TT, held[1]);
+        bring(2 * TT, held[0]);
+        bring_gate(0, gates[0]);
         lds_barrier();
-#pragma unroll 1
-        for (int t0 = 0, buf = 0; t0 < len; t0 += TT, buf ^= 1) {
-            if (MODE != kEnds && t0 > 0) store(t0 - TT, buf ^ 1);
-            bring_gate(t0);
-            if (t0 + TT < len) {
-                stage(t0 + TT, buf ^ 1);
-                if (t0 + 2 * TT < len) bring(t0 + 2 * TT);
-            }
+        auto pass = [&](int t0, auto parity) {
+            constexpr int P = decltype(parity)::value;
+            if (MODE != kEnds && t0 > 0) store(t0 - TT, P ^ 1, gates[P ^ 1]);
+            bring_gate(t0 + TT, gates[P ^ 1]);
+            stage(t0 + TT, P ^ 1, held[P ^ 1]);
+            bring(t0 + 3 * TT, held[P ^ 1]);
             lds_barrier();
+        };
+#pragma unroll 1
+        for (int t0 = 0; t0 < len; t0 += 2 * TT) {
+            pass(t0, std::integral_constant<int, 0>{});
+            if (t0 + TT < len) pass(t0 + TT, std::integral_constant<int, 1>{});
         }
-        if (MODE != kEnds && len > 0) store((len - 1) / TT * TT, (len - 1) / TT & 1);
+        if (MODE != kEnds && len > 0) {
+            const int end = (len - 1) / TT;
+            if (end & 1)
+                store(end * TT, 1, gates[1]);
+            else
+                store(end * TT, 0, gates[0]);
+        }
         return;
     }
 
@@ -443,8 +489,8 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         if constexpr (L == 16) {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                f.b[s] = *reinterpret_cast<const f32x4*>(&sB[buf][(lane * S + s) * (TT + 4) + t]);
-                if constexpr (MODE != kEnds) f.c[s] = *reinterpret_cast<const f32x4*>(&sC[buf][(lane * S + s) * (TT + 4) + t]);
+                f.b[s] = *reinterpret_cast<const f32x4*>(&sB[buf][(s * 16 + lane) * (TT + 4) + t]);
+                if constexpr (MODE != kEnds) f.c[s] = *reinterpret_cast<const f32x4*>(&sC[buf][(s * 16 + lane) * (TT + 4) + t]);
             }
         } else {
 #pragma unroll
