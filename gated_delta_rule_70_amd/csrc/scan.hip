@@ -276,9 +276,10 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     __shared__ float sDt[2][TT * CT], sX[2][TT * CT], sY[2][TT * CT];
     __shared__ float sB[2][K::bc], sC[2][K::bc];
 
-    const int64_t b = block0 + xcd_order(blockIdx.x, gridDim.x);
-    const int gt = (int)(b % (tiles * a.G));
+    const int64_t b = block0 + blockIdx.x;
     const int64_t slot = b / (tiles * a.G);  // sequence, and segment
+    // each sequence on all XCDs, neighbouring channels, whose values share lines, on one
+    const int gt = (int)xcd_order(b % (tiles * a.G), tiles * a.G);
     const int seq = (int)(MODE == kWhole ? slot : slot / a.segs), seg = (int)(MODE == kWhole ? 0 : slot % a.segs);
     const int g = gt / tiles, per = a.D / a.G, c0 = gt % tiles * CT;  // first channel in the group
     const int d0 = g * per + c0, left = per - c0;                     // in all; channels from there on
