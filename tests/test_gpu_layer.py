@@ -184,6 +184,15 @@ QK = [
     ((12,), 1, 1, 512, 512, BF, F32, False, I32),
     ((12,), 2, 2, 400, 272, BF, F32, True, I32),
     ((9,), 3, 2, 1, 0, BF, BF, False, None),
+    ((7,), 3, 2, 512, 8, BF, BF, False, I32),
+    ((7,), 2, 2, 501, 98, F32, F32, True, I32),
+    ((7,), 2, 2, 500, 500, F32, F32, False, I32),
+    ((7,), 5, 2, 90, 90, BF, BF, False, I32),
+    ((7,), 5, 2, 90, 90, BF, F32, True, I32),
+    ((70,), 9, 2, 65, 34, BF, BF, False, I64),
+    ((70,), 20, 2, 33, 18, BF, BF, True, I64),
+    ((70,), 20, 2, 17, 2, F32, F32, True, I64),
+    ((70,), 20, 2, 128, 66, BF, BF, False, I64),
     ((301,), 16, 4, 128, 0, BF, BF, False, None),
     ((5,), 2, 2, 16, 16, BF, BF, False, I32),
     ((130,), 6, 2, 112, 32, F32, F32, False, I32),
@@ -269,7 +278,7 @@ def test_qk_magnitudes(dtype, d):
 
 @pytest.mark.parametrize("rows,HQ,HK,d", [(11000, 3, 1, 512), (2100, 5, 3, 16)])
 def test_qk_many_heads(rows, HQ, HK, d):
-    """Enough heads for two groups a lane, the last one with fewer."""
+    """More workgroups than the GPU holds at once, the last waves of a row with fewer heads."""
     note(f"qk_norm_rope {rows}x{HQ}+{HK}x{d}")
     q, k, qw, kw, cos, sin, pos = qk_inputs((rows,), HQ, HK, d, 16, BF, F32, I32, seed=5)
     check_qk(gdr.qk_norm_rope(q, k, qw, kw, cos, sin, positions=pos), q, k, qw, kw, cos, sin, pos, 1e-6, False)
