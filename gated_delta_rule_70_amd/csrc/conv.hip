@@ -1,8 +1,12 @@
 // Short causal convolution of each channel over time (gdr_causal_conv).
 //
-// y[t][d] = act(bias[d] + sum_j w[d][j] x[t - (W - 1) + j][d]).  Each thread holds eight channels'
-// taps and the window of the last W - 1 rows in registers and walks down the rows, so x is read once
-// (and W - 1 rows again for each tile of rows) and y written once: bound by memory.
+// y[t][d] = act(bias[d] + sum_j w[d][j] x[t - (W - 1) + j][d]).  Each thread takes a tile of rows of eight
+// channels: it loads them and the W - 1 rows before, all at once, and its taps, and slides over them in
+// registers.  So x is read from memory once (the W - 1 rows again from L2) and y written once: bound by
+// memory.  4097 x 8192 bf16 27.2 us from one call to the next (4.9 TB/s), 36.2 with inputs from memory (3.7; a
+// copy of as much 26.3), 32768 x 8192 208 (5.2).  Walking down 16 rows with four on their way took 39
+// from memory.  Stores that bypass the caches made that 36 and 21 us of 4096 x 4096 15, but what reads q,
+// k and v next then waits longer: the convolution and a copy of its outputs 66 us instead of 57.
 //
 // The first W - 1 tokens of a sequence, whose windows reach into its state, and the new state are one
 // thread's work for each sequence and channel group ("heads"); all other rows need nothing but x
@@ -18,8 +22,7 @@ namespace gdr {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // rows that a thread loads at once
+constexpr int kThreads = 128;  // 32768 x 8192 208 us, 223 with 256
 
 struct ConvGroups {
     int groups;                           // of eight channels; an output's last one may have fewer
@@ -155,31 +158,22 @@ __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int
     const int g = (int)(wave % c.col_waves) * 64 + (threadIdx.x & 63);
     if (whole == 0 || g >= c.groups) return;
     const Cols col = cols_of(a, c, g);
+    const TX* x = static_cast<const TX*>(a.x) + col.channel;
+    Raw8<TX> raw[W - 1 + TILE];  // all on their way before the first is used
+#pragma unroll
+    for (int j = 0; j < W - 1 + TILE; ++j) {
+        const int r = r0 - (W - 1) + j;
+        raw[j] = r >= 0 && r < a.rows ? load8_raw<PART>(x + r * a.x_stride, col.n) : Raw8<TX>{};
+    }
     Taps<TW, W, PART> taps;
     taps.load(a, col);
-    const TX* x = static_cast<const TX*>(a.x) + col.channel;
-    float f[W - 1 + kUnroll][8];
-    Raw8<TX> next[kUnroll];
-    auto raw = [&](int r) { return r >= 0 && r < a.rows ? load8_raw<PART>(x + r * a.x_stride, col.n) : Raw8<TX>{}; };
+    float f[W - 1 + TILE][8];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) raw(r0 - (W - 1) + j).get(f[j]);
+    for (int j = 0; j < W - 1; ++j) raw[j].get(f[j]);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) next[u] = raw(r0 + u);
-#pragma unroll 1
-    for (int k = 0; k < TILE; k += kUnroll) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) next[u].get(f[W - 1 + u]);
-        if (k + kUnroll < TILE) {
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) next[u] = raw(r0 + k + kUnroll + u);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (whole >> (k + u) & 1) taps.store(a, col, (int64_t)r0 + k + u, f + u, static_cast<const TX*>(nullptr));
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[j][i] = f[kUnroll + j][i];
+    for (int u = 0; u < TILE; ++u) {
+        raw[W - 1 + u].get(f[W - 1 + u]);
+        if (whole >> u & 1) taps.store(a, col, (int64_t)r0 + u, f + u, static_cast<const TX*>(nullptr));
     }
 }
 
@@ -216,13 +210,13 @@ hipError_t launch(const ConvArgs& a) {
             hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, a.stream, a, c);
         });
     };
-    // Tiles of 16 rows where they make eight waves for each CU, of 4 rows below: more waves count for
-    // more than rows read again.  us at 16 / 4 rows: 32768 x 8192 213 / 232, 4096 x 4096 16.2 / 17.8,
-    // 300 x 2048 7.9 / 4.5, 2999 x 1001 fp32 17.9 / 10.2.
+    // Tiles of 8 rows where they make sixteen waves for each CU, of 4 rows below: more waves count for more
+    // than rows read again.  us at 8 / 4 rows, inputs from memory: 32768 x 8192 bf16 208 / 236, 4097 x 8192
+    // 36.2 / 38.4, 4097 x 4096 20.4 / 20.2, 3000 x 3000 11.9 / 12.2; 300 x 2048 4.3 at 4, 5.1 at 8.
     using std::integral_constant;
-    if ((int64_t)a.rows / 16 * c.col_waves >= 2048)
-        return part ? go(integral_constant<int, 16>{}, causal_conv_kernel<TX, TW, W, 16, true>)
-                    : go(integral_constant<int, 16>{}, causal_conv_kernel<TX, TW, W, 16, false>);
+    if ((int64_t)a.rows / 8 * c.col_waves >= 4096)
+        return part ? go(integral_constant<int, 8>{}, causal_conv_kernel<TX, TW, W, 8, true>)
+                    : go(integral_constant<int, 8>{}, causal_conv_kernel<TX, TW, W, 8, false>);
     return part ? go(integral_constant<int, 4>{}, causal_conv_kernel<TX, TW, W, 4, true>)
                 : go(integral_constant<int, 4>{}, causal_conv_kernel<TX, TW, W, 4, false>);
 }
