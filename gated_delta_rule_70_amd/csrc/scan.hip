@@ -72,6 +72,13 @@ __device__ __forceinline__ void store4(bf16_t* p, int n, f32x4 v) {
     }
 }
 
+// A in units of log2.  -infinity becomes the lowest finite value: the same for every step but zero,
+// which tokens past a sequence's end have.
+__device__ __forceinline__ float rate(float a) {
+    a *= kLog2e;
+    return a < -3.402823466e38f ? -3.402823466e38f : a;
+}
+
 // ---- single tokens -------------------------------------------------------------------------------
 
 // One token of each sequence, any N: sixteen lanes for each channel, S state values in each, lane l
@@ -89,7 +96,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int til
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const int n = lane + 16 * s;
-        A[s] = n < N ? a.A[(int64_t)d * N + n] * kLog2e : 0.f;
+        A[s] = n < N ? rate(a.A[(int64_t)d * N + n]) : 0.f;
         h[s] = n < N && a.h0 ? a.h0[at + n] : 0.f;
     }
     const TX* B = static_cast<const TX*>(a.b) + seq * a.b_stride + (int64_t)g * N;
@@ -159,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void scan_step4_kernel(ScanArgs a, int ti
         float y = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * (A.get(i) * kLog2e)), h[q].get(i), in * B[q].get(i));
+            v[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * rate(A.get(i))), h[q].get(i), in * B[q].get(i));
             y = __builtin_fmaf(C[q].get(i), v[i], y);
         }
         if (mine && a.ht) store4(a.ht + ((seq0 + q) * a.D + d) * N + n, 4, v);
@@ -273,8 +280,9 @@ template <typename TX, typename TDT, int L, int S, int MODE>
 __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, int tiles, int64_t block0) {
     using K = Tile<L, S>;
     constexpr int CT = K::CT, TT = K::TT, NP = K::NP;
-    __shared__ float sDt[2][TT * CT], sX[2][TT * CT], sY[2][TT * CT];
-    __shared__ float sB[2][K::bc], sC[2][K::bc];
+    __shared__ __align__(16) float sDt[2][TT * CT], sX[2][TT * CT], sY[2][TT * CT];
+    __shared__ __align__(16) float sB[2][K::bc], sC[2][K::bc];
+    static_assert(K::bc % 4 == 0);
 
     const int64_t b = block0 + blockIdx.x;
     const int64_t slot = b / (tiles * a.G);  // sequence, and segment
@@ -459,7 +467,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const bool there = mine && lane * S + s < N;
-        A[s] = there && len > 0 ? a.A[(int64_t)(d0 + c) * N + lane * S + s] * kLog2e : 0.f;
+        A[s] = there && len > 0 ? rate(a.A[(int64_t)(d0 + c) * N + lane * S + s]) : 0.f;
         h[s] = there && a.h0 && MODE != kEnds ? a.h0[state + s] : 0.f;
     }
     const float skip = mine && a.skip && MODE != kEnds ? a.skip[d0 + c] : 0.f;
@@ -634,7 +642,7 @@ hipError_t launch_tiles(const ScanArgs& a) {
 // 69 (81).  Sequences of a packed batch end at different times: there only from four workgroups a CU on.
 bool few_lanes(const ScanArgs& a) {
     if (a.N > 16 || a.segs > 1) return false;
-    const int64_t per = a.D / a.G, wide = a.B * a.G * ((per + 63) / 64), narrow = a.B * a.G * ((per + 15) / 16);
+    const int64_t per = a.D / a.G, parts = (int64_t)a.B * a.G, wide = parts * ((per + 63) / 64), narrow = parts * ((per + 15) / 16);
     if (a.cu) return wide >= 1024;
     const int64_t rounds4 = (wide + 255) / 256, rounds16 = (narrow + 255) / 256;
     return rounds4 * (a.N > 8 ? 67 : 51) < rounds16 * 19;

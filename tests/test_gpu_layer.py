@@ -412,15 +412,61 @@ def test_scan_packed_in_segments(lens, xt, D, N, G):
     assert (y[:front] == SENTINEL).all() and (y[front + T:] == SENTINEL).all()
 
 
-@pytest.mark.parametrize("B,T,D,N,xt", [(17, 40, 1000, 16, BF), (64, 21, 520, 7, F32), (30, 35, 1090, 12, BF)])
+@pytest.mark.parametrize("B,T,D,N,xt", [(17, 40, 1000, 16, BF), (64, 21, 520, 7, F32), (16, 35, 1024, 16, BF), (32, 21, 500, 13, F32)])
 def test_scan_of_many_channels(B, T, D, N, xt):
-    """Four lanes for a channel."""
+    """Enough for four lanes a channel in some, sixteen in others."""
     note(f"selective_scan {B}x{T}x{D} N={N} {xt}")
     a = scan_inputs((B, T), B, D, N, 1, xt, xt, True, True, True, True, True, seed=11)
     want, bound, end, end_bound = scan_reference(a)
     y, ht = gdr.selective_scan(**a)
     ref.close(y, want, bound)
     ref.close(ht, end, end_bound)
+
+
+def test_scan_packed_many_sequences():
+    """Four lanes for a channel in a packed batch, sequences that end inside a tile."""
+    note("packed selective_scan of 70 sequences")
+    lens = [int(n) for n in torch.randint(0, 19, (70,), generator=gen(12))]
+    D, T = 1000, sum(lens)
+    a = scan_inputs((T + 5,), len(lens), D, 16, 1, BF, BF, True, True, True, True, True, seed=12)
+    out = torch.full_like(a["x"], SENTINEL)
+    y, ht = gdr.selective_scan(**a, cu_seqlens=cu_of(lens), out=out)
+    cut = {k: v[:T] if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+    want, bound, end, end_bound = scan_reference(cut, lens)
+    ref.close(y[:T], want, bound)
+    ref.close(ht, end, end_bound)
+    assert (y[T:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("T,D", [(1, 40), (21, 40), (1100, 40), (21, 1024)])
+def test_scan_without_memory(T, D):
+    """A of -infinity: the state is the last token's input alone, whatever comes behind the sequence's end in
+    a tile; in every form of the kernel."""
+    B = 16 if D > 40 else 1
+    a = scan_inputs((B, T), B, D, 16, 1, F32, F32, True, False, True, True, True, seed=13)
+    a["A"][::2] = -float("inf")
+    y, ht = gdr.selective_scan(**a)
+    v = ref.wide(a["dt"]) + ref.wide(a["dt_bias"])
+    step = torch.nn.functional.softplus(v)
+    last = (step * ref.wide(a["x"]))[:, -1, ::2, None] * ref.wide(a["B"])[:, -1]
+    # softplus (16 u), its argument's rounding (|v| u of a small value), two products
+    bound = (18 + v.abs()[:, -1, ::2, None]) * ref.U * last.abs()
+    assert not y.isnan().any() and not ht.isnan().any()
+    ref.close(ht[:, ::2], last, bound)
+    one = {k: v[:, -1] if k in ("x", "dt", "B", "C") else v for k, v in a.items() if k not in ("h0", "z")}
+    end = torch.empty_like(ht)
+    gdr.selective_scan_step(**one, state=a["h0"], out_state=end)
+    ref.close(end[:, ::2], last, bound)
+
+
+def test_packed_batch_of_nothing():
+    a = scan_inputs((0,), 3, 24, 16, 1, BF, BF, True, True, True, True, True, seed=14)
+    cu = torch.zeros(4, dtype=I32, device="cuda")
+    y, ht = gdr.selective_scan(**a, cu_seqlens=cu)
+    assert y.shape == (0, 24) and torch.equal(ht, a["h0"])
+    x, w, b, s = conv_inputs(3, 0, 24, 4, BF, BF, True, True)
+    y, end = gdr.causal_conv(x[0], w, bias=b, state=s, cu_seqlens=cu)
+    assert y.shape == (0, 24) and torch.equal(end, s)
 
 
 def test_scan_strided_and_in_place():
