@@ -24,6 +24,14 @@ namespace {
 
 constexpr int kThreads = 128;  // 32768 x 8192 208 us, 223 with 256
 
+// How an output's channels go into groups of eight.
+enum {
+    kWhole,    // without rest
+    kOverlap,  // a tile's last group begins earlier, so that it is whole: some channels are computed twice.
+               // Not in a head, where the second to come would find the state replaced
+    kPart      // an output has fewer than eight channels: its group goes value by value
+};
+
 struct ConvGroups {
     int groups;                           // of eight channels; an output's last one may have fewer
     int first[GDR_CONV_MAX_OUT + 1];      // first group of each output
@@ -148,8 +156,9 @@ __device__ __forceinline__ uint64_t whole_windows(const ConvArgs& a, int r0) {
     return __ballot(ok);
 }
 
-template <typename TX, typename TW, int W, int TILE, bool PART>
+template <typename TX, typename TW, int W, int TILE, int FORM>
 __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int64_t wave) {
+    constexpr bool PART = FORM == kPart;
     const int64_t t = wave / c.col_waves;
     const int64_t row0 = t * TILE;
     if (row0 >= a.rows) return;
@@ -157,7 +166,11 @@ __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int
     const uint64_t whole = whole_windows<W, TILE>(a, r0);
     const int g = (int)(wave % c.col_waves) * 64 + (threadIdx.x & 63);
     if (whole == 0 || g >= c.groups) return;
-    const Cols col = cols_of(a, c, g);
+    Cols col = cols_of(a, c, g);
+    if (FORM == kOverlap && col.n < 8) {
+        const int back = 8 - col.n;
+        col.at -= back, col.channel -= back;
+    }
     const TX* x = static_cast<const TX*>(a.x) + col.channel;
     Raw8<TX> raw[W - 1 + TILE];  // all on their way before the first is used
 #pragma unroll
@@ -177,23 +190,23 @@ __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int
     }
 }
 
-template <typename TX, typename TW, int W, int TILE, bool PART>
+template <typename TX, typename TW, int W, int TILE, int FORM>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvArgs a, ConvGroups c) {
     const int64_t b = c.block0 + blockIdx.x;
     if (b < c.head_blocks)
-        head<TX, TW, W, PART>(a, c, b * kThreads + threadIdx.x);
+        head<TX, TW, W, FORM != kWhole>(a, c, b * kThreads + threadIdx.x);
     else
-        tile<TX, TW, W, TILE, PART>(a, c, xcd_order(b - c.head_blocks, c.tile_blocks) * (kThreads / 64) +
+        tile<TX, TW, W, TILE, FORM>(a, c, xcd_order(b - c.head_blocks, c.tile_blocks) * (kThreads / 64) +
                                               __builtin_amdgcn_readfirstlane(threadIdx.x / 64));
 }
 
 template <typename TX, typename TW, int W>
 hipError_t launch(const ConvArgs& a) {
     ConvGroups c{};
-    bool part = false;
+    int form = kWhole;
     for (int i = 0; i < a.n_out; ++i) {
         const int n = a.begin[i + 1] - a.begin[i];
-        part |= n % 8 != 0;
+        if (n % 8 != 0 && form != kPart) form = n < 8 ? kPart : kOverlap;
         c.first[i] = c.groups;
         c.groups += (n + 7) / 8;
     }
@@ -214,11 +227,13 @@ hipError_t launch(const ConvArgs& a) {
     // than rows read again.  us at 8 / 4 rows, inputs from memory: 32768 x 8192 bf16 208 / 236, 4097 x 8192
     // 36.2 / 38.4, 4097 x 4096 20.4 / 20.2, 3000 x 3000 11.9 / 12.2; 300 x 2048 4.3 at 4, 5.1 at 8.
     using std::integral_constant;
-    if ((int64_t)a.rows / 8 * c.col_waves >= 4096)
-        return part ? go(integral_constant<int, 8>{}, causal_conv_kernel<TX, TW, W, 8, true>)
-                    : go(integral_constant<int, 8>{}, causal_conv_kernel<TX, TW, W, 8, false>);
-    return part ? go(integral_constant<int, 4>{}, causal_conv_kernel<TX, TW, W, 4, true>)
-                : go(integral_constant<int, 4>{}, causal_conv_kernel<TX, TW, W, 4, false>);
+    auto rows = [&](auto n) {
+        constexpr int TILE = decltype(n)::value;
+        return form == kWhole     ? go(n, causal_conv_kernel<TX, TW, W, TILE, kWhole>)
+               : form == kOverlap ? go(n, causal_conv_kernel<TX, TW, W, TILE, kOverlap>)
+                                  : go(n, causal_conv_kernel<TX, TW, W, TILE, kPart>);
+    };
+    return (int64_t)a.rows / 8 * c.col_waves >= 4096 ? rows(integral_constant<int, 8>{}) : rows(integral_constant<int, 4>{});
 }
 
 }  // namespace
