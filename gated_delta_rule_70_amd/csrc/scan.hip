@@ -308,6 +308,10 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     }
     const int tid = threadIdx.x % kThreads, N = a.N;
 
+    for (int i = threadIdx.x; i < K::bc; i += 2 * kThreads)  // the states past N stay zero
+        sB[0][i] = sB[1][i] = sC[0][i] = sC[1][i] = 0.f;
+    lds_barrier();
+
     if (threadIdx.x >= kThreads) {
         // What this thread brings of a tile: groups of four channels, of tokens rowsApart from each other,
         // and of four states of B and C.
@@ -317,7 +321,9 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         const TDT* dt = static_cast<const TDT*>(a.dt) + (first + gt0) * a.dt_stride + d0 + gc;
         const TX* z = a.z && MODE != kEnds ? static_cast<const TX*>(a.z) + (first + gt0) * a.z_stride + d0 + gc : nullptr;
         TX* out = static_cast<TX*>(a.out) + (first + gt0) * a.out_stride + d0 + gc;
-        const int bt = tid / (NP / 4), bn = tid % (NP / 4) * 4;
+        // the last four states where N is no multiple of four: some are then brought twice
+        const int bt = tid / (NP / 4), group = tid % (NP / 4) * 4, bn = N < 4 ? group : min(group, N - 4);
+        const bool brings = group < N;
         const TX* B = static_cast<const TX*>(a.b) + (first + bt) * a.b_stride + (int64_t)g * N + bn;
         const TX* C = static_cast<const TX*>(a.c) + (first + bt) * a.c_stride + (int64_t)g * N + bn;
         struct Held {  // of a tile, on its way
@@ -331,7 +337,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 
         // Tiles of nothing but whole groups are loaded and stored without looking at their ends: a branch
         // around a load makes the next instructions wait for it.
-        const bool whole = left >= CT && N % 4 == 0;
+        const bool whole = left >= CT && N >= 4;
         auto bring = [&](int t0, Held& r) {  // the tile at t0, on which the pointers stand
             if (t0 >= len) return;
             if (whole && t0 + TT <= len) {
@@ -344,7 +350,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 #pragma unroll
                 for (int i = 0; i < K::bc_groups; ++i) {
                     r.b[i] = r.c[i] = Raw4<TX>{};
-                    if ((bcApart * K::bc_groups == TT || bt < TT) && bn < N) {
+                    if ((bcApart * K::bc_groups == TT || bt < TT) && brings) {
                         r.b[i] = load4(B + i * bcApart * a.b_stride, 4);
                         if constexpr (MODE != kEnds) r.c[i] = load4(C + i * bcApart * a.c_stride, 4);
                     }
@@ -358,7 +364,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 }
 #pragma unroll
                 for (int i = 0; i < K::bc_groups; ++i) {
-                    const int t = bt + i * bcApart, n = t < TT && t0 + t < len ? N - bn : 0;
+                    const int t = bt + i * bcApart, n = brings && t < TT && t0 + t < len ? N - bn : 0;
                     r.b[i] = load4(B + i * bcApart * a.b_stride, n);
                     if constexpr (MODE != kEnds) r.c[i] = load4(C + i * bcApart * a.c_stride, n);
                 }
@@ -390,7 +396,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 #pragma unroll
             for (int i = 0; i < K::bc_groups; ++i) {
                 const int t = bt + i * bcApart;
-                if (t >= TT) break;
+                if (t >= TT || !brings) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int to = K::at_state(t, bn + j);
