@@ -38,11 +38,14 @@ def close(got, want, bound):
                                  f"{want[ok][worst]:.6e} at {ok.nonzero()[worst].tolist()}")
 
 
-def silu(s, err):
+def silu(s, err, out):
     """silu(s) and its error, for s within err: |silu'| <= 1.1; the exponential's argument is taken in two
-    parts (2 u, and 2 u of the exponential, 2 u of its correction), one addition, a reciprocal, a product."""
+    parts (2 u, and 2 u of the exponential, 2 u of its correction), one addition, a reciprocal, a product.
+    For a bf16 output it is one product with log2(e), itself rounded: the exponent is off by 1.3 u of
+    itself at most, and e^-s / (1 + e^-s) of that, relative, is left in the result."""
     y = s * torch.sigmoid(s)
-    return y, 1.1 * err + 12 * U * y.abs() + FLUSH
+    one = 1.3 * U * s.abs() * y.abs() if out == torch.bfloat16 else 0.0
+    return y, 1.1 * err + 12 * U * y.abs() + one + FLUSH
 
 
 def softplus(v, err):
@@ -75,7 +78,7 @@ def conv(x, weight, bias, state, act, lens=None):
             s, mag = s + bias, mag + bias.abs()
         err = (W + 1) * U * mag
         if act:
-            s, err = silu(s, err)
+            s, err = silu(s, err, out)
         ys.append(s)
         bounds.append(1.01 * err + rounding(out) * s.abs() + FLUSH)
         ends.append(whole[rows.shape[0]:])
@@ -149,7 +152,7 @@ def scan(x, dt, A, B, C, D, z, dt_bias, softplus_dt, h0, lens=None):
                 y, err = y + D * xs[t], err + 2 * U * (D * xs[t]).abs() + U * y.abs()
             if z is not None:
                 zt = take(z, s)[t]
-                g, gerr = silu(zt, torch.zeros_like(zt))
+                g, gerr = silu(zt, torch.zeros_like(zt), out)
                 y, err = y * g, err * g.abs() + y.abs() * gerr + U * (y * g).abs()
             yo[t], bo[t] = y, 1.01 * err + rounding(out) * y.abs() + FLUSH
         ys.append(yo)

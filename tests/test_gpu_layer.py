@@ -87,6 +87,56 @@ def test_conv_packed(lens, xt, D, W):
     assert (y[:front] == SENTINEL).all() and (y[front + T:] == SENTINEL).all()
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("xt,W,out", [(BF, 4, (24,)), (F32, 3, (29, 8)), (BF, 2, (5, 32)), (BF, 4, (17, 9, 3))])
+def test_conv_long(packed, xt, W, out):
+    """Tiles of eight rows, outputs of whole groups of channels, with a rest, and of fewer than eight."""
+    note(f"long causal_conv {xt} W={W} {out} packed={packed}")
+    D, lens = sum(out), [11000, 3, 0, 8, 21999]
+    x, w, b, s = conv_inputs(len(lens) if packed else 3, 1, D, W, xt, xt, True, True, seed=8)
+    g = gen(9)
+    if packed:
+        x = randn(g, sum(lens), D, dtype=xt)
+        y, end = gdr.causal_conv(x, w, bias=b, state=s, cu_seqlens=cu_of(lens), out=out)
+    else:
+        x = randn(g, 3, 11003, D, dtype=xt)
+        y, end = gdr.causal_conv(x, w, bias=b, state=s, out=out)
+    want, bound, last = ref.conv(x, w, b, s, True, lens if packed else None)
+    ref.close(torch.cat(y, -1), want, bound)
+    assert torch.equal(ref.wide(end), last)
+
+
+def test_rows_far_apart():
+    """Rows 2^30 values apart: the third begins past 2^31 values, 2^32 bytes."""
+    note("rows far apart")
+    far, T = 2 ** 30 + 8, 3
+
+    def spaced(*tail):
+        n = torch.Size(tail).numel()
+        return torch.empty((T - 1) * far + n, dtype=BF, device="cuda").as_strided((T, *tail), (far, *[torch.Size(tail[i + 1:]).numel() for i in range(len(tail))]))
+
+    x, w, b, s = conv_inputs(1, T, 72, 4, BF, BF, True, True, seed=10)
+    a_x, a_out = spaced(72), spaced(72)
+    a_x.copy_(x[0])
+    y, end = gdr.causal_conv(a_x[None], w, bias=b, state=s, out=a_out[None])
+    want, bound, last = ref.conv(x, w, b, s, True)
+    ref.close(y, want, bound)
+    assert torch.equal(ref.wide(end), last)
+    a = scan_inputs((1, T), 1, 72, 16, 1, BF, BF, True, True, True, True, True, seed=11)
+    a_x.copy_(a["x"][0])
+    want, bound, end, end_bound = scan_reference(a)
+    y, ht = gdr.selective_scan(**{**a, "x": a_x[None]}, out=a_out[None])
+    ref.close(y, want, bound)
+    ref.close(ht, end, end_bound)
+    q, k, qw, kw, cos, sin, pos = qk_inputs((T,), 2, 2, 32, 32, BF, BF, I32, seed=12)
+    a_q, a_oq = a_x.as_strided((T, 2, 32), (far, 32, 1)), a_out.as_strided((T, 2, 32), (far, 32, 1))
+    a_q.copy_(q)
+    got = gdr.qk_norm_rope(a_q, k, qw, kw, cos, sin, positions=pos, out_q=a_oq)
+    check_qk(got, q, k, qw, kw, cos, sin, pos, 1e-6, False)
+    rows = [t.clone() for t in gdr.qk_norm_rope(q[0], k[0], qw, kw, cos, sin, positions=pos[0])]  # one token, without a dimension of tokens
+    assert torch.equal(rows[0], got[0][0]) and torch.equal(rows[1], got[1][0])
+
+
 def test_conv_strided_and_in_place():
     """A column range of a wider projection in, column ranges of one array out, the state in place."""
     note("strided causal_conv")
