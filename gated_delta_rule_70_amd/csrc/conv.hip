@@ -27,8 +27,7 @@ constexpr int kThreads = 128;  // 32768 x 8192 208 us, 223 with 256
 // How an output's channels go into groups of eight.
 enum {
     kWhole,    // without rest
-    kOverlap,  // a tile's last group begins earlier, so that it is whole: some channels are computed twice.
-               // Not in a head, where the second to come would find the state replaced
+    kOverlap,  // an output's last group begins earlier, so that it is whole: some channels are computed twice
     kPart      // an output has fewer than eight channels: its group goes value by value
 };
 
@@ -38,15 +37,37 @@ struct ConvGroups {
     int64_t head_blocks, tile_blocks, block0, col_waves;  // col_waves: waves across the channels
 };
 
-// A thread's channels: the output, their place in it, and in x.
+// A thread's channels: the output, their place in it, and in x; how many there are; and how many of the
+// first are another thread's to store.
 struct Cols {
-    int out, at, channel, n;
+    int out, at, channel, n, others;
 };
 __device__ __forceinline__ Cols cols_of(const ConvArgs& a, const ConvGroups& c, int g) {
     int i = 0;
     while (i + 1 < a.n_out && g >= c.first[i + 1]) ++i;
     const int at = (g - c.first[i]) * 8;
-    return Cols{i, at, a.begin[i] + at, a.begin[i + 1] - a.begin[i] - at};
+    return Cols{i, at, a.begin[i] + at, a.begin[i + 1] - a.begin[i] - at, 0};
+}
+
+// The same with the last group of an output begun earlier.
+__device__ __forceinline__ Cols whole_cols_of(const ConvArgs& a, const ConvGroups& c, int g) {
+    Cols col = cols_of(a, c, g);
+    if (col.n < 8) {
+        col.others = 8 - col.n;
+        col.at -= col.others, col.channel -= col.others;
+    }
+    return col;
+}
+
+template <bool PART, typename T>
+__device__ __forceinline__ void store_own(T* p, const Cols& c, const float (&v)[8]) {
+    if (c.others == 0) {
+        store8<PART>(p, c.n, v);
+    } else {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            if (i >= c.others) p[i] = rounded(v[i], p);
+    }
 }
 
 template <typename TW, int W, bool PART>
@@ -80,15 +101,19 @@ struct Taps {
             for (int j = 0; j < W; ++j) s = __builtin_fmaf(w[j][i], f[j][i], s);
             y[i] = a.silu ? silu_for(s, static_cast<const TX*>(nullptr)) : s;
         }
-        store8<PART>(static_cast<TX*>(a.out[c.out]) + row * a.out_stride[c.out] + c.at, c.n, y);
+        store_own<PART>(static_cast<TX*>(a.out[c.out]) + row * a.out_stride[c.out] + c.at, c, y);
     }
 };
 
-template <typename TX, typename TW, int W, bool PART>
+// What an overlapping group computes of another thread's channels is not stored: their state may be
+// replaced already.
+template <typename TX, typename TW, int W, int FORM>
 __device__ __forceinline__ void head(const ConvArgs& a, const ConvGroups& c, int64_t item) {
+    constexpr bool PART = FORM == kPart;
     if (item >= (int64_t)a.B * c.groups) return;
     const int seq = (int)(item / c.groups);
-    const Cols col = cols_of(a, c, (int)(item % c.groups));
+    const int g = (int)(item % c.groups);
+    const Cols col = FORM == kOverlap ? whole_cols_of(a, c, g) : cols_of(a, c, g);
     int64_t first = (int64_t)seq * a.T;
     int len = a.T;
     if (a.cu) {
@@ -123,7 +148,7 @@ __device__ __forceinline__ void head(const ConvArgs& a, const ConvGroups& c, int
                         if (len == l) v[i] = f[j + l][i];
                 }
             }
-            store8<PART>(static_cast<TX*>(a.out_state) + ((int64_t)seq * P + j) * a.D + col.channel, col.n, v);
+            store_own<PART>(static_cast<TX*>(a.out_state) + ((int64_t)seq * P + j) * a.D + col.channel, col, v);
         }
     }
     if (len < 1) return;
@@ -166,11 +191,8 @@ __device__ __forceinline__ void tile(const ConvArgs& a, const ConvGroups& c, int
     const uint64_t whole = whole_windows<W, TILE>(a, r0);
     const int g = (int)(wave % c.col_waves) * 64 + (threadIdx.x & 63);
     if (whole == 0 || g >= c.groups) return;
-    Cols col = cols_of(a, c, g);
-    if (FORM == kOverlap && col.n < 8) {
-        const int back = 8 - col.n;
-        col.at -= back, col.channel -= back;
-    }
+    Cols col = FORM == kOverlap ? whole_cols_of(a, c, g) : cols_of(a, c, g);
+    col.others = 0;  // the same values twice: one store for all is quicker
     const TX* x = static_cast<const TX*>(a.x) + col.channel;
     Raw8<TX> raw[W - 1 + TILE];  // all on their way before the first is used
 #pragma unroll
@@ -194,7 +216,7 @@ template <typename TX, typename TW, int W, int TILE, int FORM>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvArgs a, ConvGroups c) {
     const int64_t b = c.block0 + blockIdx.x;
     if (b < c.head_blocks)
-        head<TX, TW, W, FORM != kWhole>(a, c, b * kThreads + threadIdx.x);
+        head<TX, TW, W, FORM>(a, c, b * kThreads + threadIdx.x);
     else
         tile<TX, TW, W, TILE, FORM>(a, c, xcd_order(b - c.head_blocks, c.tile_blocks) * (kThreads / 64) +
                                               __builtin_amdgcn_readfirstlane(threadIdx.x / 64));

@@ -37,6 +37,11 @@ __device__ __forceinline__ float round_to(float x, const float*) { return x; }
 __device__ __forceinline__ float round_to(float x, const bf16_t*) {
     return static_cast<float>(static_cast<__bf16>(x));
 }
+// x as it is stored, in the type of what p points to.
+__device__ __forceinline__ float rounded(float x, const float*) { return x; }
+__device__ __forceinline__ bf16_t rounded(float x, const bf16_t*) {
+    return bf16_t{__builtin_bit_cast(uint16_t, static_cast<__bf16>(x))};
+}
 template <bool PART>
 __device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
     if (!PART || n >= 8) {
