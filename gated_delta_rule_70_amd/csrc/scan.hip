@@ -13,7 +13,7 @@
 // outputs would take 27; 8 sequences of 512 70 (76); 4097 x 1024 48 (50); 32768 x 4096 840.  At 8 x 4096 x 4096 the ALU
 // issued in 93 % of the cycles.  fp32 matrix instructions do not run beside the ALU here: one of 4 x 4 x 1
 // takes as long as 3.6 additions, so neither step x B nor the sums over states gain by them.  Single tokens are
-// bound by the states' bytes: 256 sequences of 4096 x 16 24 us (32 from memory, 4.5 TB/s).
+// bound by the states' bytes: 256 sequences of 4096 x 16 27 us (31 from memory, 4.6 TB/s).
 #include "layer_launch.h"
 
 #include <type_traits>
@@ -89,61 +89,21 @@ __device__ __forceinline__ float rate(float a) {
 
 // ---- single tokens -------------------------------------------------------------------------------
 
-// One token of each sequence, any N: sixteen lanes for each channel, S state values in each, lane l
-// has values l, l + 16, ...
-template <typename TX, typename TDT, int S>
+// P lanes for each channel (a power of two, at least N / 4), four state values in each, and Q sequences one
+// after the other, whose loads are all on their way at once.  Where N is no multiple of four the last
+// lane has the last four values, some of them twice: the lanes of a channel are in one wave, so all have read
+// before any writes.  (FOURS: N is a multiple; looking at N around the loads costs 256 x 4096 x 16 from memory
+// 35 us instead of 31.)  Bound by the states' bytes.
+template <typename TX, typename TDT, int P, int Q, bool FOURS>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int tiles, int64_t block0) {
-    const int64_t b = block0 + blockIdx.x;
-    const int64_t seq = b / tiles;
-    const int lane = threadIdx.x & 15;
-    const int d = (int)(b % tiles) * (kThreads / 16) + threadIdx.x / 16;
-    if (d >= a.D) return;  // whole rows of 16 lanes
-    const int N = a.N, g = d / (a.D / a.G);
-    float A[S], h[S];
-    const int64_t at = (seq * a.D + d) * N;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int n = lane + 16 * s;
-        A[s] = n < N ? rate(a.A[(int64_t)d * N + n]) : 0.f;
-        h[s] = n < N && a.h0 ? a.h0[at + n] : 0.f;
-    }
-    const TX* B = static_cast<const TX*>(a.b) + seq * a.b_stride + (int64_t)g * N;
-    const TX* C = static_cast<const TX*>(a.c) + seq * a.c_stride + (int64_t)g * N;
-    const float xv = to_f32(static_cast<const TX*>(a.x)[seq * a.x_stride + d]);
-    float step = to_f32(static_cast<const TDT*>(a.dt)[seq * a.dt_stride + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
-    if (a.softplus) step = softplus(step);
-    const float in = step * xv;
-    float y = 0.f;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int n = lane + 16 * s;
-        const float bv = n < N ? to_f32(B[n]) : 0.f, cv = n < N ? to_f32(C[n]) : 0.f;
-        h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * A[s]), h[s], in * bv);
-        y = __builtin_fmaf(cv, h[s], y);
-    }
-    y = row_sum(y);
-    y = __builtin_fmaf(a.skip ? a.skip[d] : 0.f, xv, y);
-    TX* out = static_cast<TX*>(a.out) + seq * a.out_stride + d;
-    if (a.z) y *= silu_for(to_f32(static_cast<const TX*>(a.z)[seq * a.z_stride + d]), out);
-    if (lane == 0) store1(out, y);
-    if (a.ht)
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (lane + 16 * s < N) a.ht[at + lane + 16 * s] = h[s];
-}
-
-// The same for N a multiple of four: P lanes for each channel (a power of two, at least N / 4), four
-// state values in each, and Q sequences one after the other, whose loads are all on their way at
-// once.  Bound by the states' bytes.
-template <typename TX, typename TDT, int P, int Q>
-__global__ __launch_bounds__(kThreads) void scan_step4_kernel(ScanArgs a, int tiles, int64_t block0) {
     const int64_t b = block0 + blockIdx.x;
     const int64_t seq0 = b / tiles * Q;
     const int lane = threadIdx.x % P;
     const int d = (int)(b % tiles) * (kThreads / P) + threadIdx.x / P;
     if (d >= a.D) return;  // all lanes of a channel
-    const int N = a.N, n = 4 * lane, g = a.G == 1 ? 0 : d / (a.D / a.G);
-    const bool mine = n < N;
+    const int N = a.N, most = FOURS ? 4 : N;
+    const int n = FOURS ? 4 * lane : N < 4 ? 0 : min(4 * lane, N - 4), twice = 4 * lane - n, g = a.G == 1 ? 0 : d / (a.D / a.G);
+    const bool mine = 4 * lane < N;
     Raw4<float> h[Q], A{};
     Raw4<TX> B[Q], C[Q];
     TX x[Q], z[Q];
@@ -154,15 +114,15 @@ __global__ __launch_bounds__(kThreads) void scan_step4_kernel(ScanArgs a, int ti
         h[q] = Raw4<float>{};
         B[q] = C[q] = Raw4<TX>{};
         if (mine) {
-            if (a.h0) h[q] = load4(a.h0 + (seq * a.D + d) * N + n, 4);
-            B[q] = load4(static_cast<const TX*>(a.b) + seq * a.b_stride + (int64_t)g * N + n, 4);
-            C[q] = load4(static_cast<const TX*>(a.c) + seq * a.c_stride + (int64_t)g * N + n, 4);
+            if (a.h0) h[q] = load4(a.h0 + (seq * a.D + d) * N + n, most);
+            B[q] = load4(static_cast<const TX*>(a.b) + seq * a.b_stride + (int64_t)g * N + n, most);
+            C[q] = load4(static_cast<const TX*>(a.c) + seq * a.c_stride + (int64_t)g * N + n, most);
         }
         x[q] = static_cast<const TX*>(a.x)[seq * a.x_stride + d];
         dt[q] = static_cast<const TDT*>(a.dt)[seq * a.dt_stride + d];
         z[q] = a.z ? static_cast<const TX*>(a.z)[seq * a.z_stride + d] : TX{};
     }
-    if (mine) A = load4(a.A + (int64_t)d * N + n, 4);
+    if (mine) A = load4(a.A + (int64_t)d * N + n, most);
     const float skip = a.skip ? a.skip[d] : 0.f, bias = a.dt_bias ? a.dt_bias[d] : 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -175,9 +135,9 @@ __global__ __launch_bounds__(kThreads) void scan_step4_kernel(ScanArgs a, int ti
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * rate(A.get(i))), h[q].get(i), in * B[q].get(i));
-            y = __builtin_fmaf(C[q].get(i), v[i], y);
+            y = !FOURS && i < twice ? y : __builtin_fmaf(C[q].get(i), v[i], y);
         }
-        if (mine && a.ht) store4(a.ht + ((seq0 + q) * a.D + d) * N + n, 4, v);
+        if (mine && a.ht) store4(a.ht + ((seq0 + q) * a.D + d) * N + n, most, v);
         if constexpr (P > 1) y += dpp_mov<0xB1>(y);   // quad_perm [1,0,3,2]
         if constexpr (P > 2) y += dpp_mov<0x4E>(y);   // quad_perm [2,3,0,1]
         if constexpr (P > 4) y += dpp_mov<0x141>(y);  // row_half_mirror
@@ -602,7 +562,7 @@ bool valid(const ScanArgs& a) {
 }
 
 template <typename TX, typename TDT, int P>
-hipError_t launch_step4(const ScanArgs& a) {
+hipError_t launch_step(const ScanArgs& a) {
     constexpr int channels = kThreads / P;
     const int tiles = (a.D + channels - 1) / channels;
     auto go = [&](auto kernel, int q) {
@@ -610,31 +570,20 @@ hipError_t launch_step4(const ScanArgs& a) {
             hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, a.stream, a, tiles, first);
         });
     };
-    return (int64_t)a.B * tiles >= 8192 ? go(scan_step4_kernel<TX, TDT, P, 4>, 4) : go(scan_step4_kernel<TX, TDT, P, 1>, 1);
+    if (a.N % 4) return go(scan_step_kernel<TX, TDT, P, 1, false>, 1);
+    // Two sequences for a workgroup where that leaves enough of them.  us at 1 / 2 / 4, states from memory:
+    // 256 x 4096 x 16 34.0 / 31.1 / 30.9, 256 x 4096 x 8 20.1 / 18.4 / 21.5, 128 x 4096 x 16 19.5 / 17.8 / 18.8.
+    return (int64_t)a.B * tiles >= 8192 ? go(scan_step_kernel<TX, TDT, P, 2, true>, 2) : go(scan_step_kernel<TX, TDT, P, 1, true>, 1);
 }
 
 template <typename TX, typename TDT>
 hipError_t launch_step(const ScanArgs& a) {
-    if (a.N % 4 == 0) {
-        if (a.N <= 4) return launch_step4<TX, TDT, 1>(a);
-        if (a.N <= 8) return launch_step4<TX, TDT, 2>(a);
-        if (a.N <= 16) return launch_step4<TX, TDT, 4>(a);
-        if (a.N <= 32) return launch_step4<TX, TDT, 8>(a);
-        if (a.N <= 64) return launch_step4<TX, TDT, 16>(a);
-        return launch_step4<TX, TDT, 32>(a);
-    }
-    const int tiles = (a.D + kThreads / 16 - 1) / (kThreads / 16);
-    return by_blocks((int64_t)a.B * tiles, kThreads, [&](int64_t first, unsigned count) {
-        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, a.stream, a, tiles, first); };
-        if (a.N <= 16)
-            go(scan_step_kernel<TX, TDT, 1>);
-        else if (a.N <= 32)
-            go(scan_step_kernel<TX, TDT, 2>);
-        else if (a.N <= 64)
-            go(scan_step_kernel<TX, TDT, 4>);
-        else
-            go(scan_step_kernel<TX, TDT, 8>);
-    });
+    if (a.N <= 4) return launch_step<TX, TDT, 1>(a);
+    if (a.N <= 8) return launch_step<TX, TDT, 2>(a);
+    if (a.N <= 16) return launch_step<TX, TDT, 4>(a);
+    if (a.N <= 32) return launch_step<TX, TDT, 8>(a);
+    if (a.N <= 64) return launch_step<TX, TDT, 16>(a);
+    return launch_step<TX, TDT, 32>(a);
 }
 
 template <typename TX, typename TDT, int L, int S>

@@ -538,7 +538,7 @@ def test_scan_strided_and_in_place():
 
 @pytest.mark.parametrize("B,D,N,G,xt,dtt", [(1, 4096, 16, 1, BF, BF), (33, 72, 16, 2, BF, F32), (5, 37, 10, 1, F32, F32),
                                             (70, 64, 64, 1, BF, BF), (3, 20, 128, 4, F32, F32), (2, 9, 1, 1, BF, BF), (17, 130, 7, 1, BF, BF),
-                                            (8195, 5, 8, 1, BF, BF), (9, 40, 4, 1, F32, F32), (6, 30, 28, 2, BF, BF)])
+                                            (8195, 5, 8, 1, BF, BF), (3, 70, 19, 1, BF, F32), (4, 33, 2, 1, F32, F32), (5, 20, 101, 1, BF, BF), (9, 30, 34, 2, F32, F32), (9, 40, 4, 1, F32, F32), (6, 30, 28, 2, BF, BF)])
 def test_scan_step(B, D, N, G, xt, dtt):
     """Token by token within the whole sequence's bounds, the state in place."""
     note(f"selective_scan_step {B}x{D} N={N} G={G} {xt}")
