@@ -452,18 +452,28 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     }
     const float skip = mine && a.skip && MODE != kEnds ? a.skip[d0 + c] : 0.f;
     // The state behind a segment, from zero, and its sum of steps lie in the workspace, [slot][D][N] and
-    // [slot][D]: with them the state before this segment follows from the sequence's first one.
+    // [slot][D]: with them the state before this segment follows from the sequence's first one.  A hundred
+    // segments are a chain of loads unless several are asked for together (B 1, T 6468, D 64, N 16: 38 us
+    // one by one, 20 us eight at a time).
     float* const ends = a.workspace;
     float* const steps = ends + (int64_t)a.B * a.segs * a.D * N;
     if constexpr (MODE == kSegments) {
-        if (mine)
-            for (int64_t e = slot - seg; e < slot; ++e) {
-                const float sum = steps[e * a.D + d0 + c];
-                const float* end = ends + (e * a.D + d0 + c) * N + lane * S;
+        constexpr int kAtOnce = S <= 2 ? 8 : 2;  // few states a lane: the registers are there
+        for (int64_t e0 = slot - seg; mine && e0 < slot; e0 += kAtOnce) {
+            float sums[kAtOnce], end[kAtOnce][S];
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(sum * A[s]), h[s], lane * S + s < N ? end[s] : 0.f);
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int64_t e = e0 + i < slot ? e0 + i : e0;
+                sums[i] = steps[e * a.D + d0 + c];
+#pragma unroll
+                for (int s = 0; s < S; ++s) end[i][s] = lane * S + s < N ? ends[(e * a.D + d0 + c) * N + lane * S + s] : 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (e0 + i < slot)
+#pragma unroll
+                    for (int s = 0; s < S; ++s) h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(sums[i] * A[s]), h[s], end[i][s]);
+        }
     }
     // What was loaded so far is waited for here: left to its first use in the loop, the wait would be
     // there in every pass.
