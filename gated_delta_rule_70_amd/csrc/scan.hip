@@ -247,7 +247,8 @@ struct Tile {
 };
 
 // What a launch does: whole sequences, or sequences cut into segments of a.seg_len tokens, the
-// states behind each first (from zero, without outputs), then each segment from its start.
+// states behind each first (from zero, without outputs), then each segment from its start.  The first
+// launch also puts h0 by: ht may be h0, and the second one's last segment writes it while others begin.
 enum { kWhole, kEnds, kSegments };
 
 template <typename TX, typename TDT, int L, int S, int MODE>
@@ -272,11 +273,17 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         first = s.first, len = s.count;
     }
     bool last = true;  // segment of the sequence
+    int64_t begin = seq;  // where its first state lies
     if constexpr (MODE != kWhole) {
         const int64_t behind = (int64_t)seg * a.seg_len;
         if (seg > 0 && behind >= len) return;
         last = behind + a.seg_len >= len;
-        if (MODE == kEnds && last) return;  // no segment starts from it
+        if (MODE == kEnds && last) {  // no segment starts from it; its place holds h0 for the others
+            const int64_t from = (int64_t)seq * a.D + d0, to = slot * a.D + d0, n = (int64_t)min(CT, left) * a.N;
+            for (int64_t i = threadIdx.x; a.h0 && i < n; i += 2 * kThreads) a.workspace[to * a.N + i] = a.h0[from * a.N + i];
+            return;
+        }
+        if (MODE == kSegments) begin = slot - seg + (len > 0 ? (len - 1) / a.seg_len : 0);
         first += behind;
         len = last ? len - (int)behind : a.seg_len;
     }
@@ -444,17 +451,18 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     const bool mine = c < left;
     float A[S], h[S];
     const int64_t state = ((int64_t)seq * a.D + d0 + c) * N + lane * S;
+    const float* h0 = a.h0 && MODE != kEnds ? (MODE == kSegments ? a.workspace : a.h0) + (begin * a.D + d0 + c) * N + lane * S : nullptr;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const bool there = mine && lane * S + s < N;
         A[s] = there && len > 0 ? rate(a.A[(int64_t)(d0 + c) * N + lane * S + s]) : 0.f;
-        h[s] = there && a.h0 && MODE != kEnds ? a.h0[state + s] : 0.f;
+        h[s] = there && h0 ? h0[s] : 0.f;
     }
     const float skip = mine && a.skip && MODE != kEnds ? a.skip[d0 + c] : 0.f;
     // The state behind a segment, from zero, and its sum of steps lie in the workspace, [slot][D][N] and
     // [slot][D]: with them the state before this segment follows from the sequence's first one.  A hundred
     // segments are a chain of loads unless several are asked for together (B 1, T 6468, D 64, N 16: 38 us
-    // one by one, 20 us eight at a time).
+    // one by one, 22 us eight at a time).
     float* const ends = a.workspace;
     float* const steps = ends + (int64_t)a.B * a.segs * a.D * N;
     if constexpr (MODE == kSegments) {
@@ -472,7 +480,12 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             for (int i = 0; i < kAtOnce; ++i)
                 if (e0 + i < slot)
 #pragma unroll
-                    for (int s = 0; s < S; ++s) h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(sums[i] * A[s]), h[s], end[i][s]);
+                    for (int s = 0; s < S; ++s) {
+                        // A whole segment's factor may pass fp32's range where the state does not: it is taken in
+                        // two halves, finite ones for the sake of a state of zero (a NaN of the steps is in `end`, too).
+                        const float half = fminf(__builtin_amdgcn_exp2f(0.5f * sums[i] * A[s]), 3.402823466e38f);
+                        h[s] = __builtin_fmaf(half * h[s], half, end[i][s]);
+                    }
         }
     }
     // What was loaded so far is waited for here: left to its first use in the loop, the wait would be

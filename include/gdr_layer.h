@@ -128,7 +128,8 @@ typedef struct {
  * x, dt, z, out [B][T][D]; B and C [B][T][G][N] (a row's groups contiguous); A [D][N], Dskip and
  * dt_bias [D] fp32, dense (these two may be NULL); h0 and ht [B][D][N] fp32, dense.  States are fp32
  * throughout.  ht (if not NULL) receives the last state; it may be h0 itself.  A is expected not
- * to be positive; where it is, the state grows as the formula says.  -infinity counts as the lowest
+ * to be positive; where it is, the state grows as the formula says (a token's factor past fp32's
+ * range is infinity, and NaN on a state of zero).  -infinity counts as the lowest
  * finite value (a state that each token of a positive step begins anew).
  */
 int gdr_selective_scan(const gdr_scan_dims* dims, const int32_t* cu_seqlens, const void* x, const void* dt,

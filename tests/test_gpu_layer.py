@@ -462,6 +462,48 @@ def test_scan_packed_in_segments(lens, xt, D, N, G):
     assert (y[:front] == SENTINEL).all() and (y[front + T:] == SENTINEL).all()
 
 
+@pytest.mark.parametrize("lens", [[700, 0, 65, 1029, 3, 640], [1, 1, 1600, 33, 33]])
+def test_scan_packed_in_segments_in_place(lens):
+    """The state replaced by the last segment of each sequence, which the others begin from."""
+    note(f"packed selective_scan in segments, in place {lens}")
+    D, N, T = 20, 16, sum(lens) + 4000
+    assert gdr.selective_scan_workspace_bytes(len(lens), T, D, N, packed=True) > 0
+    a = scan_inputs((T,), len(lens), D, N, 1, BF, F32, True, True, True, True, True, seed=12)
+    a["dt_bias"] -= 2
+    cu = cu_of(lens, 0)
+    cut = {k: v[:sum(lens)] if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+    want, bound, end, end_bound = scan_reference(cut, lens)
+    y, ht = gdr.selective_scan(**a, cu_seqlens=cu)
+    ref.close(y[:sum(lens)], want, bound)
+    ref.close(ht, end, end_bound)
+    for _ in range(5):
+        state = a["h0"].clone()
+        y2, h2 = gdr.selective_scan(**{**a, "h0": state}, cu_seqlens=cu, ht=state)
+        assert h2 is state and torch.equal(state, ht) and torch.equal(y2[:sum(lens)], y[:sum(lens)])
+
+
+@pytest.mark.parametrize("A,on,h0", [(2., 640, 0.), (1.5, 64, 2. ** -100), (-3., 640, 2. ** 100)])
+def test_scan_in_segments_past_the_range_of_a_factor(A, on, h0):
+    """Factors of a whole segment past fp32's range, states within it: zeros, or a small one."""
+    note(f"selective_scan in segments, A {A}")
+    T, D, N = 640, 16, 4
+    assert gdr.selective_scan_workspace_bytes(1, T, D, N) > 0
+    a = dict(x=torch.zeros(1, T, D, device="cuda"), dt=torch.zeros(1, T, D, device="cuda"),
+             A=torch.full((D, N), A, device="cuda"), B=torch.ones(1, T, 1, N, device="cuda"), C=torch.ones(1, T, 1, N, device="cuda"),
+             D=None, z=None, dt_bias=None, dt_softplus=False, h0=torch.full((1, D, N), h0, device="cuda"))
+    a["dt"][:, :on] = 1.
+    skip = 0
+    if h0 == 0:  # nothing until the last 20 tokens, which stand for all
+        skip = T - 20
+        a["x"][:, skip:] = 1.
+    want, bound, end, end_bound = scan_reference({k: v[:, skip:] if k in ("x", "dt", "B", "C") else v for k, v in a.items()})
+    assert want.isfinite().all() and end.isfinite().all() and bound.isfinite().all()
+    y, ht = gdr.selective_scan(**a)
+    assert (y[:, :skip] == 0).all()
+    ref.close(y[:, skip:], want, bound)
+    ref.close(ht, end, end_bound)
+
+
 @pytest.mark.parametrize("B,T,D,N,xt", [(17, 40, 1000, 16, BF), (64, 21, 520, 7, F32), (16, 35, 1024, 16, BF), (32, 21, 500, 13, F32)])
 def test_scan_of_many_channels(B, T, D, N, xt):
     """Enough for four lanes a channel in some, sixteen in others."""
