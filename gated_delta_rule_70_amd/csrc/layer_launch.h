@@ -56,18 +56,23 @@ struct ScanArgs {
 // a CU and 42 for two.  Where they leave half the CUs idle, segments run side by side: first the states
 // behind each from zero, 55 % of a run's work, then each segment from its start.  Two workgroups a CU,
 // at 1.55 * 42 ns for each segment's tokens, pay from three segments on, if a sequence is long enough to
-// win back the second launch, and segments of 64 tokens or more.  In a packed batch any sequence may
-// have all rows, so each has workgroups for all of them, most of which find nothing to do: that is
-// limited.
+// win back the second launch, and segments of 64 tokens or more.  us whole / cut, N = 16: 1 x 511 x 64 15.5 / 9.9,
+// 1 x 260 x 64 10.9 / 9.9, 1 x 130 x 64 8.4 / 9.8; two workgroups a CU, 4 x 300 x 256 11.0 / 12.4.
+//
+// In a packed batch any sequence may have all rows.  Sequence i, from row c on, has the slots from c / seg_len + i
+// on: at least as many as segments, and T / seg_len + B in all, whatever the lengths.  Segments pay earlier
+// there, since the longest sequence counts: 64 channels, lengths 957, 503, 269, 189 and six short ones 25.6 / 12.2;
+// equal lengths may lose, twenty of 600 tokens of 128 channels 20.9 / 32.4, ten of 64 channels 18.6 / 15.5.
 struct ScanCut {
-    int segs, seg_len;
+    int segs, seg_len;  // packed: segs * B slots
 };
 inline ScanCut scan_cut(int64_t B, int64_t T, int64_t D, int64_t G, bool packed) {
     const int64_t groups = G * ((D / G + 15) / 16), blocks = B * groups;
     const int64_t n = 512 / blocks, mean = packed ? T / B : T;
-    if (n < 3 || mean < 512) return {1, 0};
-    const int64_t len = ((mean + n - 1) / n + 63) / 64 * 64, segs = (T + len - 1) / len;
-    if (segs < 2 || (packed && segs * blocks > 8192)) return {1, 0};
+    if (n < 3 || mean < (packed ? 128 : 256)) return {1, 0};
+    const int64_t len = ((mean + n - 1) / n + 63) / 64 * 64;
+    const int64_t segs = packed ? (T / len + 2 * B - 1) / B : (T + len - 1) / len;
+    if (segs < 2 || (!packed && T < 512 && segs * blocks > 256)) return {1, 0};
     return {static_cast<int>(segs), static_cast<int>(len)};
 }
 

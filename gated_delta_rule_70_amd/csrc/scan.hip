@@ -251,6 +251,11 @@ struct Tile {
 // launch also puts h0 by: ht may be h0, and the second one's last segment writes it while others begin.
 enum { kWhole, kEnds, kSegments };
 
+// First slot of a packed batch's sequence i: strictly ascending, fewer than T / seg_len + B.
+__device__ __forceinline__ int64_t packed_slot(const ScanArgs& a, int i) {
+    return min(max(a.cu[i], 0), a.T) / a.seg_len + i;
+}
+
 template <typename TX, typename TDT, int L, int S, int MODE>
 __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, int tiles, int64_t block0) {
     using K = Tile<L, S>;
@@ -263,7 +268,23 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     const int64_t slot = b / (tiles * a.G);  // sequence, and segment
     // each sequence on all XCDs, neighbouring channels, whose values share lines, on one
     const int gt = (int)xcd_order(b % (tiles * a.G), tiles * a.G);
-    const int seq = (int)(MODE == kWhole ? slot : slot / a.segs), seg = (int)(MODE == kWhole ? 0 : slot % a.segs);
+    int seq = (int)slot, seg = 0;
+    if (MODE != kWhole) {
+        seq = (int)(slot / a.segs), seg = (int)(slot % a.segs);
+        if (a.cu) {  // the last sequence whose slots begin at or before this one
+            int hi = a.B - 1;
+            seq = 0;
+            while (seq < hi) {
+                const int mid = (seq + hi + 1) >> 1;
+                if (packed_slot(a, mid) <= slot)
+                    seq = mid;
+                else
+                    hi = mid - 1;
+            }
+            seg = (int)(slot - packed_slot(a, seq));
+            if (seg < 0) return;  // before the first row
+        }
+    }
     const int g = gt / tiles, per = a.D / a.G, c0 = gt % tiles * CT;  // first channel in the group
     const int d0 = g * per + c0, left = per - c0;                     // in all; channels from there on
     int64_t first = (int64_t)seq * a.T;
