@@ -658,3 +658,26 @@ def test_scan_boundaries_of_anything():
         room = torch.full((3 * T, D), SENTINEL, dtype=BF, device="cuda")
         gdr.selective_scan(**a, cu_seqlens=torch.tensor(cu, dtype=I32, device="cuda"), out=room[T:2 * T])
         assert (room[:T] == SENTINEL).all() and (room[2 * T:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("D", [40, 1200])
+def test_entries_outside_the_batch(D):
+    """Bounds of sequences that are none lead nowhere outside the tensors, in segments (few channels) or whole."""
+    T, N, front = 1500, 16, 7
+    for entries in ([-5, 900, 300, 10 ** 9], [T + 1, T + 2, T + 3, T + 4], [-3, -2, -1, 0], [1000, 500, 200, 2 ** 31 - 1]):
+        note(f"packed operators, D {D}, bounds {entries}")
+        cu = torch.tensor(entries, dtype=torch.int32, device="cuda")
+        assert (gdr.selective_scan_workspace_bytes(3, T, D, N, packed=True) > 0) == (D == 40)
+        a = scan_inputs((T,), 3, D, N, 1, BF, BF, True, True, True, True, True, seed=13)
+        room = torch.full((front + T + front, D), SENTINEL, dtype=BF, device="cuda")
+        ends = torch.full((5, D, N), SENTINEL, device="cuda")
+        gdr.selective_scan(**a, cu_seqlens=cu, out=room[front:front + T], ht=ends[1:4])
+        torch.cuda.synchronize()
+        x, w, b, s = conv_inputs(3, 1, D, 4, BF, BF, True, True)
+        room2, ends2 = torch.full_like(room, SENTINEL), torch.full((5, 3, D), SENTINEL, dtype=BF, device="cuda")
+        gdr.causal_conv(a["x"], w, bias=b, state=s, cu_seqlens=cu, out=room2[front:front + T], out_state=ends2[1:4])
+        torch.cuda.synchronize()
+        for r in (room, room2):
+            assert (r[:front] == SENTINEL).all() and (r[front + T:] == SENTINEL).all()
+        for e in (ends, ends2):
+            assert (e[0] == SENTINEL).all() and (e[4] == SENTINEL).all()
