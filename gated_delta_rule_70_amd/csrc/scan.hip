@@ -135,9 +135,10 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int til
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(step * rate(A.get(i))), h[q].get(i), in * B[q].get(i));
-            y = !FOURS && i < twice ? y : __builtin_fmaf(C[q].get(i), v[i], y);
+            y = !FOURS && (i < twice || n + i >= N) ? y : __builtin_fmaf(C[q].get(i), v[i], y);
         }
         if (mine && a.ht) store4(a.ht + ((seq0 + q) * a.D + d) * N + n, most, v);
+        if (!mine) y = 0.f;  // an infinite step x times its B and C of zero is none
         if constexpr (P > 1) y += dpp_mov<0xB1>(y);   // quad_perm [1,0,3,2]
         if constexpr (P > 2) y += dpp_mov<0x4E>(y);   // quad_perm [2,3,0,1]
         if constexpr (P > 4) y += dpp_mov<0x141>(y);  // row_half_mirror

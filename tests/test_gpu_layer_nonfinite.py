@@ -1,0 +1,61 @@
+"""Infinite inputs, steps, products and states of the selective scan: infinities where the formula has them, at
+state counts that do and do not fill the lanes of a channel, in every form."""
+import pytest
+import torch
+
+import gated_delta_rule_70_amd as gdr
+import layer_reference as ref
+from gpu_util import note
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+INF = float("inf")
+LARGEST = torch.finfo(F32).max
+
+
+def inputs(B, T, D, N, seed):
+    """fp32, B and C positive, so that states of one sign give a sum that is infinite and no NaN."""
+    g = torch.Generator().manual_seed(seed)
+    rand = lambda *s: torch.rand(*s, generator=g)  # noqa: E731
+    return dict(x=torch.randn(B, T, D, generator=g), dt=0.2 * rand(B, T, D), A=-(0.1 + 2 * rand(D, N)), B=0.5 + rand(B, T, 1, N),
+                C=1 + rand(B, T, 1, N), D=0.5 + rand(D), z=0.5 + rand(B, T, D), h0=torch.randn(B, D, N, generator=g))
+
+
+def infinite(a, t):
+    """Into the first sequence: an infinite input at token t of channel 3, an infinite step in channel 5, and in
+    channel 7 finite ones whose product passes fp32's range, in a state that hardly decays."""
+    a["x"][0, t, 3] = INF
+    a["dt"][0, t, 5], a["x"][0, t, 5] = INF, 1.
+    a["dt"][0, t, 7], a["x"][0, t, 7] = 4., 3e38
+    a["A"][7] = -1e-6
+    return a
+
+
+def expected(a):
+    """The formula's values, what passes fp32's range as infinity."""
+    want, bound, end, end_bound = ref.scan(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], a["z"], None, False, a["h0"])
+    want, end = (torch.where(t.abs() > LARGEST, INF * t.sign(), t) for t in (want, end))
+    return want, bound, end, end_bound
+
+
+def on_gpu(a):
+    return {k: v.cuda() for k, v in a.items()}
+
+
+STATES = [1, 2, 3, 4, 5, 8, 10, 12, 15, 16, 17, 20, 32, 33, 64, 100, 128]
+
+
+@pytest.mark.parametrize("N", STATES)
+def test_single_tokens(N):
+    """Token by token, the state in place."""
+    note(f"selective_scan_step with infinities, N={N}")
+    T, t0 = 6, 2
+    a = infinite(inputs(2, T, 40, N, 1), t0)
+    want, bound, end, end_bound = expected(a)
+    assert not want.isnan().any() and want[0, t0:, [3, 5, 7]].isinf().all()
+    g = on_gpu(a)
+    state = g.pop("h0")
+    for t in range(T):
+        one = {k: v[:, t].contiguous() if k in ("x", "dt", "B", "C", "z") else v for k, v in g.items()}
+        ref.close(gdr.selective_scan_step(**one, state=state), want[:, t], bound[:, t])
+    ref.close(state, end, end_bound)
