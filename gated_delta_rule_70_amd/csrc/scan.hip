@@ -231,7 +231,7 @@ template <int L, int S>
 struct Tile {
     static constexpr int CT = kThreads / L;
     static constexpr int TT = L == 4 ? 32 : S <= 2 ? 64 : S == 4 ? 48 : 16;  // two workgroups share a CU's LDS
-    static constexpr int NP = L * S;                                         // states, padded with zeros
+    static constexpr int NP = L * S;                                         // places for states
     static constexpr int bc = L == 16 ? NP * (TT + 4) : TT * NP;
     static constexpr int groups = (TT * CT / 4 + kThreads - 1) / kThreads;   // of four channels, for a thread to bring
     static constexpr int bc_groups = (TT * NP / 4 + kThreads - 1) / kThreads;  // of four states
@@ -247,6 +247,45 @@ struct Tile {
     }
 };
 
+// Which of a channel's N states is in each of its NP places, where they are more.  A place without a state would
+// hold zeros, and an infinite input times those is NaN, in the sum y too; so every place has one.  States go in
+// fours (as they are brought), the last four possibly beginning earlier: each four 2^k times, and the first
+// `more` of them as often again, which makes every state's copies a power of two.  Its C is divided by their
+// number, and their parts of y add up to its own exactly.  (The last fours that share states are there equally
+// often: fours + more is even, so `more` never ends between them.)  4097 x 4096 us with copies / zeros in those
+// places: N = 10 106 / 106, 20 148 / 149, 48 264 / 263, 100 555 / 528.
+struct Places {
+    int N, fours, k, more;
+    __device__ __forceinline__ Places(int n, int np) : N(n), fours((n + 3) / 4), k(0) {
+        while (2 * fours << k <= np / 4) ++k;
+        more = (np / 4 >> k) - fours;
+    }
+    // The first state of the four in places 4 g to 4 g + 3.
+    __device__ __forceinline__ int first(int g) const {
+        const int w = g >> k;
+        return N < 4 ? 0 : min(4 * (w < fours ? w : w - fours), N - 4);
+    }
+    __device__ __forceinline__ int state(int place) const {
+        const int j = place % 4;
+        return N < 4 ? j < N ? j : N == 2 ? j - 2 : 0 : first(place / 4) + j;
+    }
+    // Fewer than four states in four places, as `state` has them; what belongs to a copy is that of the state.
+    __device__ __forceinline__ f32x4 repeat(f32x4 v) const {
+        return f32x4{v[0], N == 1 ? v[0] : v[1], N < 3 ? v[0] : v[2], N == 2 ? v[1] : v[0]};
+    }
+    // Whether it is the first copy of its four.
+    __device__ __forceinline__ bool own(int place) const {
+        const int g = place / 4;
+        return g < fours << k && g % (1 << k) == 0;
+    }
+    __device__ __forceinline__ float share(int state) const {
+        const int w = state / 4, last = 1 << k << (fours - 1 < more);
+        const int copies = N < 4 ? (N == 3 ? 1 + (state == 0) : 4 / N) << k
+                                 : (w < fours - 1 ? 1 << k << (w < more) : 0) + (state >= N - 4 ? last : 0);
+        return __builtin_ldexpf(1.f, -__builtin_ctz(copies));
+    }
+};
+
 // What a launch does: whole sequences, or sequences cut into segments of a.seg_len tokens, the
 // states behind each first (from zero, without outputs), then each segment from its start.  The first
 // launch also puts h0 by: ht may be h0, and the second one's last segment writes it while others begin.
@@ -257,7 +296,8 @@ __device__ __forceinline__ int64_t packed_slot(const ScanArgs& a, int i) {
     return min(max(a.cu[i], 0), a.T) / a.seg_len + i;
 }
 
-template <typename TX, typename TDT, int L, int S, int MODE>
+// COPIES: N states are fewer than places.
+template <typename TX, typename TDT, int L, int S, int MODE, bool COPIES>
 __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, int tiles, int64_t block0) {
     using K = Tile<L, S>;
     constexpr int CT = K::CT, TT = K::TT, NP = K::NP;
@@ -310,10 +350,11 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         len = last ? len - (int)behind : a.seg_len;
     }
     const int tid = threadIdx.x % kThreads, N = a.N;
-
-    for (int i = threadIdx.x; i < K::bc; i += 2 * kThreads)  // the states past N stay zero
-        sB[0][i] = sB[1][i] = sC[0][i] = sC[1][i] = 0.f;
-    lds_barrier();
+    const Places places(N, NP);
+    if constexpr (MODE == kEnds) {  // has no sums: places past N only need to hold something
+        for (int i = threadIdx.x; i < K::bc; i += 2 * kThreads) sB[0][i] = sB[1][i] = 0.f;
+        lds_barrier();
+    }
 
     if (threadIdx.x >= kThreads) {
         // What this thread brings of a tile: groups of four channels, of tokens rowsApart from each other,
@@ -325,8 +366,11 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         const TX* z = a.z && MODE != kEnds ? static_cast<const TX*>(a.z) + (first + gt0) * a.z_stride + d0 + gc : nullptr;
         TX* out = static_cast<TX*>(a.out) + (first + gt0) * a.out_stride + d0 + gc;
         // the last four states where N is no multiple of four: some are then brought twice
-        const int bt = tid / (NP / 4), group = tid % (NP / 4) * 4, bn = N < 4 ? group : min(group, N - 4);
-        const bool brings = group < N;
+        const int bt = tid / (NP / 4), group = tid % (NP / 4) * 4, bn = COPIES ? places.first(group / 4) : N < 4 ? group : min(group, N - 4);
+        const bool brings = COPIES || group < N;
+        float share[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) share[j] = COPIES ? places.share(places.state(group + j)) : 1.f;
         const TX* B = static_cast<const TX*>(a.b) + (first + bt) * a.b_stride + (int64_t)g * N + bn;
         const TX* C = static_cast<const TX*>(a.c) + (first + bt) * a.c_stride + (int64_t)g * N + bn;
         struct Held {  // of a tile, on its way
@@ -400,11 +444,18 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             for (int i = 0; i < K::bc_groups; ++i) {
                 const int t = bt + i * bcApart;
                 if (t >= TT || !brings) break;
+                f32x4 b, c = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int to = K::at_state(t, bn + j);
-                    sB[buf][to] = r.b[i].get(j);
-                    if constexpr (MODE != kEnds) sC[buf][to] = r.c[i].get(j);
+                    b[j] = r.b[i].get(j);
+                    if constexpr (MODE != kEnds) c[j] = COPIES ? r.c[i].get(j) * share[j] : r.c[i].get(j);
+                }
+                if (COPIES && NP <= 16 && N < 4) b = places.repeat(b), c = places.repeat(c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int to = COPIES ? K::at_state(t, group + j) : K::at_state(t, bn + j);
+                    sB[buf][to] = b[j];
+                    if constexpr (MODE != kEnds) sC[buf][to] = c[j];
                 }
             }
         };
@@ -472,13 +523,16 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     const int lane = tid % L, c = tid / L;
     const bool mine = c < left;
     float A[S], h[S];
-    const int64_t state = ((int64_t)seq * a.D + d0 + c) * N + lane * S;
-    const float* h0 = a.h0 && MODE != kEnds ? (MODE == kSegments ? a.workspace : a.h0) + (begin * a.D + d0 + c) * N + lane * S : nullptr;
+    const int64_t channel = ((int64_t)seq * a.D + d0 + c) * N;
+    const float* h0 = a.h0 && MODE != kEnds ? (MODE == kSegments ? a.workspace : a.h0) + (begin * a.D + d0 + c) * N : nullptr;
+    int state[S];  // in this lane's places
+#pragma unroll
+    for (int s = 0; s < S; ++s) state[s] = COPIES ? places.state(lane * S + s) : lane * S + s;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        const bool there = mine && lane * S + s < N;
-        A[s] = there && len > 0 ? rate(a.A[(int64_t)(d0 + c) * N + lane * S + s]) : 0.f;
-        h[s] = there && h0 ? h0[s] : 0.f;
+        const bool there = mine && state[s] < N;
+        A[s] = there && len > 0 ? rate(a.A[(int64_t)(d0 + c) * N + state[s]]) : 0.f;
+        h[s] = there && h0 ? h0[state[s]] : 0.f;
     }
     const float skip = mine && a.skip && MODE != kEnds ? a.skip[d0 + c] : 0.f;
     // The state behind a segment, from zero, and its sum of steps lie in the workspace, [slot][D][N] and
@@ -496,7 +550,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                 const int64_t e = e0 + i < slot ? e0 + i : e0;
                 sums[i] = steps[e * a.D + d0 + c];
 #pragma unroll
-                for (int s = 0; s < S; ++s) end[i][s] = lane * S + s < N ? ends[(e * a.D + d0 + c) * N + lane * S + s] : 0.f;
+                for (int s = 0; s < S; ++s) end[i][s] = state[s] < N ? ends[(e * a.D + d0 + c) * N + state[s]] : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i)
@@ -598,7 +652,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     } else if (a.ht && mine && last) {
 #pragma unroll
         for (int s = 0; s < S; ++s)
-            if (lane * S + s < N) a.ht[state + s] = h[s];
+            if (COPIES ? places.own(lane * S + s) : lane * S + s < N) a.ht[channel + state[s]] = h[s];
     }
 }
 
@@ -640,13 +694,15 @@ hipError_t launch_tiles(const ScanArgs& a) {
             hipLaunchKernelGGL(kernel, dim3(count), dim3(2 * kThreads), 0, a.stream, a, tiles, first);
         });
     };
+    const bool copies = a.N < L * S;
     if constexpr (L == 16) {
         if (a.segs > 1) {
-            const hipError_t e = go((int64_t)a.B * a.segs, scan_kernel<TX, TDT, L, S, kEnds>);
-            return e != hipSuccess ? e : go((int64_t)a.B * a.segs, scan_kernel<TX, TDT, L, S, kSegments>);
+            const hipError_t e = go((int64_t)a.B * a.segs, scan_kernel<TX, TDT, L, S, kEnds, false>);
+            if (e != hipSuccess) return e;
+            return go((int64_t)a.B * a.segs, copies ? scan_kernel<TX, TDT, L, S, kSegments, true> : scan_kernel<TX, TDT, L, S, kSegments, false>);
         }
     }
-    return go(a.B, scan_kernel<TX, TDT, L, S, kWhole>);
+    return go(a.B, copies ? scan_kernel<TX, TDT, L, S, kWhole, true> : scan_kernel<TX, TDT, L, S, kWhole, false>);
 }
 
 // Lanes for a channel.  ns a token, by workgroups for each CU (each of the dense batch's sequences as

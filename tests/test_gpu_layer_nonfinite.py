@@ -59,3 +59,23 @@ def test_single_tokens(N):
         one = {k: v[:, t].contiguous() if k in ("x", "dt", "B", "C", "z") else v for k, v in g.items()}
         ref.close(gdr.selective_scan_step(**one, state=state), want[:, t], bound[:, t])
     ref.close(state, end, end_bound)
+
+
+@pytest.mark.parametrize("N", STATES)
+@pytest.mark.parametrize("B,T,D", [(2, 40, 40), (16, 37, 1000), (2, 700, 24)], ids=["sixteen_lanes", "four_lanes", "segments"])
+def test_prompts(B, T, D, N):
+    """Whole, with sixteen and (up to 16 states) with four lanes for a channel, and in segments; a token's y and
+    every later one."""
+    note(f"selective_scan with infinities {B}x{T}x{D}, N={N}")
+    assert (gdr.selective_scan_workspace_bytes(B, T, D, N) > 0) == (T == 700)
+    for t in (0, T // 2, T - 1):
+        a = inputs(B, T, D, N, 2)
+        a["z"] += 1.  # what passes the range stays past it at the gate
+        if T == 700:
+            a["dt"] *= 0.2  # states that last for segments
+        infinite(a, t)
+        want, bound, end, end_bound = expected(a)
+        assert not want.isnan().any() and want[0, t:, [3, 5, 7]].isinf().all()
+        y, ht = gdr.selective_scan(**on_gpu(a))
+        ref.close(y, want, bound)
+        ref.close(ht, end, end_bound)
