@@ -563,6 +563,35 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                         h[s] = __builtin_fmaf(half * h[s], half, end[i][s]);
                     }
         }
+        // NaN may come of an infinite state and a segment's factor that is zero.  Token by token such a state stays,
+        // unless a token's own factor is zero: this thread goes through the segments again and looks.
+        bool lost = false;
+#pragma unroll
+        for (int s = 0; s < S; ++s) lost |= h[s] != h[s];
+        if (lost) {
+            const TDT* dt = static_cast<const TDT*>(a.dt) + (first - (int64_t)seg * a.seg_len) * a.dt_stride + d0 + c;
+            const float bias = a.dt_bias ? a.dt_bias[d0 + c] : 0.f;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float v = h0 ? h0[state[s]] : 0.f;
+#pragma unroll 1
+                for (int i = 0; i < seg; ++i) {
+                    const int64_t e = slot - seg + i;
+                    const float half = fminf(__builtin_amdgcn_exp2f(0.5f * steps[e * a.D + d0 + c] * A[s]), 3.402823466e38f);
+                    const float end = ends[(e * a.D + d0 + c) * N + state[s]];
+                    bool stays = half == 0.f && fabsf(v) > 3.402823466e38f;
+                    float next = stays ? v + end : __builtin_fmaf(half * v, half, end);
+#pragma unroll 1
+                    for (int t = 0; stays && t < a.seg_len; ++t) {
+                        float step = to_f32(dt[((int64_t)i * a.seg_len + t) * a.dt_stride]) + bias;
+                        if (a.softplus) step = softplus(step);
+                        if (__builtin_amdgcn_exp2f(step * A[s]) == 0.f) stays = false, next = __builtin_nanf("");
+                    }
+                    v = next;
+                }
+                h[s] = v;
+            }
+        }
     }
     // What was loaded so far is waited for here: left to its first use in the loop, the wait would be
     // there in every pass.

@@ -79,3 +79,37 @@ def test_prompts(B, T, D, N):
         y, ht = gdr.selective_scan(**on_gpu(a))
         ref.close(y, want, bound)
         ref.close(ht, end, end_bound)
+
+
+@pytest.mark.parametrize("N", STATES)
+@pytest.mark.parametrize("T", [60, 700])
+def test_infinite_states(T, N):
+    """A first state of infinity stays, however much of a finite one a segment would leave."""
+    note(f"selective_scan from infinite states, T={T}, N={N}")
+    a = inputs(2, T, 24, N, 3)
+    a["h0"][0, 4, N - 1], a["h0"][1, 9, 0], a["h0"][1, 10, N // 2] = INF, -INF, INF
+    a["A"][9], a["A"][10] = -60., -30.
+    want, bound, end, end_bound = expected(a)
+    assert not want.isnan().any() and want[0, :, 4].isinf().all() and want[1, :, 9:11].isinf().all()
+    y, ht = gdr.selective_scan(**on_gpu(a))
+    ref.close(y, want, bound)
+    ref.close(ht, end, end_bound)
+
+
+def test_a_state_that_a_token_wipes_out():
+    """A token's factor below fp32's normal range counts as zero, and makes NaN of an infinite state; in segments
+    as at once, wherever in them it is."""
+    note("infinite states and factors of zero")
+    N, D = 20, 24
+    for T, t in ((60, 0), (60, 59), (700, 0), (700, 63), (700, 64), (700, 300), (700, 699)):
+        a = inputs(1, T, D, N, 4)
+        a["h0"][0, 2, 5], a["h0"][0, 6, 7], a["A"][6, 7] = INF, INF, -1e-3
+        a["dt"][0, t] = 300.  # a factor of e^-600 and less, e^-0.3 in channel 6
+        a["A"][2, 5] = -2.
+        a["x"][0, t] = 0.
+        y, ht = gdr.selective_scan(**on_gpu(a))
+        bad = torch.zeros(T, D, dtype=torch.bool)
+        bad[t:, 2] = True
+        assert torch.equal(y[0].isnan().cpu(), bad)
+        assert ht[0, 2, 5].isnan() and ht[0, 6, 7] == INF and ht.isnan().sum() == 1
+        assert (y[0, :, 6] == INF).all() and (y[0, :t, 2] == INF).all()
