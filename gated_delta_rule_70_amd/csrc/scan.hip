@@ -80,11 +80,12 @@ __device__ __forceinline__ void store4(bf16_t* p, int n, f32x4 v) {
     }
 }
 
-// A in units of log2.  -infinity becomes the lowest finite value: the same for every step but zero,
-// which tokens past a sequence's end have.
+// A in units of log2, within the finite values: an infinite one is the same for every step but zero, which
+// tokens past a sequence's end have.
 __device__ __forceinline__ float rate(float a) {
+    constexpr float most = 3.402823466e38f;
     a *= kLog2e;
-    return a < -3.402823466e38f ? -3.402823466e38f : a;
+    return a < -most ? -most : a > most ? most : a;
 }
 
 // ---- single tokens -------------------------------------------------------------------------------

@@ -130,8 +130,8 @@ typedef struct {
  * throughout.  ht (if not NULL) receives the last state; it may be h0 itself.  A is expected not
  * to be positive; where it is, the state grows as the formula says (a token's factor past fp32's
  * range is infinity, and NaN on a state of zero; in a call with a workspace on any state).  A token's
- * factor below fp32's normal range is zero, and NaN on an infinite state.  -infinity counts as the lowest
- * finite value (a state that each token of a positive step begins anew).
+ * factor below fp32's normal range is zero, and NaN on an infinite state.  Infinities in A count as the
+ * finite values next to them (-infinity: a state that each token of a positive step begins anew).
  */
 int gdr_selective_scan(const gdr_scan_dims* dims, const int32_t* cu_seqlens, const void* x, const void* dt,
                        const float* A, const void* B, const void* C, const float* Dskip, const void* z,

@@ -113,3 +113,21 @@ def test_a_state_that_a_token_wipes_out():
         assert torch.equal(y[0].isnan().cpu(), bad)
         assert ht[0, 2, 5].isnan() and ht[0, 6, 7] == INF and ht.isnan().sum() == 1
         assert (y[0, :, 6] == INF).all() and (y[0, :t, 2] == INF).all()
+
+
+@pytest.mark.parametrize("rate", [INF, LARGEST, 2.5e38])
+@pytest.mark.parametrize("B,T,D", [(2, 3, 40), (16, 37, 1000), (2, 64, 40)])
+def test_rates_past_the_range(B, T, D, rate):
+    """A of infinity, and of values whose product with log2(e) passes fp32's range: a state that is not zero is
+    infinite behind the first token, and stays so, whatever lies behind a sequence's end in a tile."""
+    note(f"selective_scan {B}x{T}x{D}, A {rate}")
+    a = inputs(B, T, D, 16, 5)
+    a["A"][3, 2] = rate
+    a["dt"] += 0.01
+    a["h0"][:, 3, 2] = 1.
+    y, ht = gdr.selective_scan(**on_gpu(a))
+    assert (y[:, :, 3] == INF).all() and (ht[:, 3, 2] == INF).all()
+    assert not y.isnan().any() and not ht.isnan().any() and ht.isinf().sum() == B
+    one = {k: v[:, 0].contiguous().cuda() if k in ("x", "dt", "B", "C", "z") else v.cuda() for k, v in a.items() if k != "h0"}
+    state = a["h0"].cuda()
+    assert (gdr.selective_scan_step(**one, state=state)[:, 3] == INF).all() and (state[:, 3, 2] == INF).all()
