@@ -231,7 +231,7 @@ __device__ __forceinline__ void unrolled(std::integer_sequence<int, J...>, F f) 
 template <int L, int S>
 struct Tile {
     static constexpr int CT = kThreads / L;
-    static constexpr int TT = L == 4 ? 32 : S <= 2 ? 64 : S == 4 ? 48 : 16;  // two workgroups share a CU's LDS
+    static constexpr int TT = scan_tile_tokens(L, S);
     static constexpr int NP = L * S;                                         // places for states
     static constexpr int bc = L == 16 ? NP * (TT + 4) : TT * NP;
     static constexpr int groups = (TT * CT / 4 + kThreads - 1) / kThreads;   // of four channels, for a thread to bring
@@ -735,26 +735,14 @@ hipError_t launch_tiles(const ScanArgs& a) {
     return go(a.B, copies ? scan_kernel<TX, TDT, L, S, kWhole, true> : scan_kernel<TX, TDT, L, S, kWhole, false>);
 }
 
-// Lanes for a channel.  ns a token, by workgroups for each CU (each of the dense batch's sequences as
-// long; 256 CUs): 16 lanes, workgroups of 16 channels: 25, 42, 60, 78, 116 for 1, 2, 3, 4, 6; 4 lanes, workgroups
-// of 64 channels, N = 16: 74, 135, 270 for 1, 2, 4, N = 8: 103 for 2.  So 4 lanes take less where they
-// fill the CUs evenly: 4 x 2048 x 4096 152 us (16 lanes 161), 6 x 1024 x 4096 133 (119), 8 x 512 x 4096
-// 69 (81).  Sequences of a packed batch end at different times: there only from four workgroups a CU on.
-bool few_lanes(const ScanArgs& a) {
-    if (a.N > 16 || a.segs > 1) return false;
-    const int64_t per = a.D / a.G, parts = (int64_t)a.B * a.G, wide = parts * ((per + 63) / 64), narrow = parts * ((per + 15) / 16);
-    if (a.cu) return wide >= 1024;
-    const int64_t rounds4 = (wide + 255) / 256, rounds16 = (narrow + 255) / 256;
-    return rounds4 * (a.N > 8 ? 67 : 51) < rounds16 * 19;
-}
-
 template <typename TX, typename TDT>
 hipError_t launch(const ScanArgs& a) {
-    if (few_lanes(a)) return a.N <= 8 ? launch_tiles<TX, TDT, 4, 2>(a) : launch_tiles<TX, TDT, 4, 4>(a);
-    if (a.N <= 16) return launch_tiles<TX, TDT, 16, 1>(a);
-    if (a.N <= 32) return launch_tiles<TX, TDT, 16, 2>(a);
-    if (a.N <= 64) return launch_tiles<TX, TDT, 16, 4>(a);
-    return launch_tiles<TX, TDT, 16, 8>(a);
+    const ScanTile t = scan_tile(a.B, a.D, a.N, a.G, a.cu != nullptr, a.segs);
+    if (t.lanes == 4) return t.states == 2 ? launch_tiles<TX, TDT, 4, 2>(a) : launch_tiles<TX, TDT, 4, 4>(a);
+    return t.states == 1   ? launch_tiles<TX, TDT, 16, 1>(a)
+           : t.states == 2 ? launch_tiles<TX, TDT, 16, 2>(a)
+           : t.states == 4 ? launch_tiles<TX, TDT, 16, 4>(a)
+                           : launch_tiles<TX, TDT, 16, 8>(a);
 }
 
 }  // namespace

@@ -1,0 +1,62 @@
+// Which kernel runs a selective scan, and whether its sequences are cut into segments, by the sizes alone.
+#pragma once
+
+#include <stdint.h>
+
+namespace gdr {
+
+// Segments that the sequences of a scan are cut into, by the sizes alone.
+//
+// A scan runs a token after the other in workgroups of 16 channels, 25 ns a token for one workgroup on
+// a CU and 42 for two.  Where they leave half the CUs idle, segments run side by side: first the states
+// behind each from zero, 55 % of a run's work, then each segment from its start.  Two workgroups a CU,
+// at 1.55 * 42 ns for each segment's tokens, pay from three segments on, if a sequence is long enough to
+// win back the second launch, and segments of 64 tokens or more.  us whole / cut, N = 16: 1 x 511 x 64 15.5 / 9.9,
+// 1 x 260 x 64 10.9 / 9.9, 1 x 130 x 64 8.4 / 9.8; two workgroups a CU, 4 x 300 x 256 11.0 / 12.4.
+//
+// In a packed batch any sequence may have all rows.  Sequence i, from row c on, has the slots from c / seg_len + i
+// on: at least as many as segments, and T / seg_len + B in all, whatever the lengths.  Segments pay earlier
+// there, since the longest sequence counts: 64 channels, lengths 957, 503, 269, 189 and six short ones 25.6 / 12.2;
+// equal lengths may lose, twenty of 600 tokens of 128 channels 20.9 / 32.4, ten of 64 channels 18.6 / 15.5.
+struct ScanCut {
+    int segs, seg_len;  // packed: segs * B slots
+};
+inline ScanCut scan_cut(int64_t B, int64_t T, int64_t D, int64_t G, bool packed) {
+    const int64_t groups = G * ((D / G + 15) / 16), blocks = B * groups;
+    const int64_t n = 512 / blocks, mean = packed ? T / B : T;
+    if (n < 3 || mean < (packed ? 128 : 256)) return {1, 0};
+    const int64_t len = ((mean + n - 1) / n + 63) / 64 * 64;
+    const int64_t segs = packed ? (T / len + 2 * B - 1) / B : (T + len - 1) / len;
+    if (segs < 2 || (!packed && T < 512 && segs * blocks > 256)) return {1, 0};
+    return {static_cast<int>(segs), static_cast<int>(len)};
+}
+
+// Lanes that share a channel in a workgroup of 256 (a channel each 16 or 4 of them), and state values in each.
+struct ScanTile {
+    int lanes, states;
+};
+
+// Tokens of a tile, whose operands lie in LDS twice: two workgroups share a CU's.
+constexpr int scan_tile_tokens(int lanes, int states) {
+    return lanes == 4 ? 32 : states <= 2 ? 64 : states == 4 ? 48 : 16;
+}
+
+// Lanes for a channel.  ns a token, by workgroups for each CU (each of the dense batch's sequences as
+// long; 256 CUs): 16 lanes, workgroups of 16 channels: 25, 42, 60, 78, 116 for 1, 2, 3, 4, 6; 4 lanes, workgroups
+// of 64 channels, N = 16: 74, 135, 270 for 1, 2, 4, N = 8: 103 for 2.  So 4 lanes take less where they
+// fill the CUs evenly: 4 x 2048 x 4096 152 us (16 lanes 161), 6 x 1024 x 4096 133 (119), 8 x 512 x 4096
+// 69 (81).  Sequences of a packed batch end at different times: there only from four workgroups a CU on.
+inline bool scan_few_lanes(int64_t B, int64_t D, int64_t N, int64_t G, bool packed, int64_t segs) {
+    if (N > 16 || segs > 1) return false;
+    const int64_t per = D / G, parts = B * G, wide = parts * ((per + 63) / 64), narrow = parts * ((per + 15) / 16);
+    if (packed) return wide >= 1024;
+    const int64_t rounds4 = (wide + 255) / 256, rounds16 = (narrow + 255) / 256;
+    return rounds4 * (N > 8 ? 67 : 51) < rounds16 * 19;
+}
+
+inline ScanTile scan_tile(int64_t B, int64_t D, int64_t N, int64_t G, bool packed, int64_t segs) {
+    if (scan_few_lanes(B, D, N, G, packed, segs)) return {4, N <= 8 ? 2 : 4};
+    return {16, N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8};
+}
+
+}  // namespace gdr

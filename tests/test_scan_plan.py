@@ -1,0 +1,47 @@
+"""Which kernel runs a selective scan (csrc/scan_plan.h), on the host."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from scan_forms import FORMS, lengths
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CXX = shutil.which("g++") or shutil.which("c++")
+
+
+@pytest.fixture(scope="module")
+def plans(tmp_path_factory):
+    if CXX is None:
+        pytest.skip("no C++ compiler")
+    exe = str(tmp_path_factory.mktemp("plan") / "scan_plan")
+    subprocess.run([CXX, "-O1", "-Wall", "-Wextra", "-Werror", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all",
+                    "-I", os.path.join(ROOT, "gated_delta_rule_70_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "c_abi", "scan_plan.cpp"), "-o", exe], check=True)
+
+    def run(scans):
+        """(lanes, states, tokens of a tile, segments, tokens of a segment) for each (B, T, D, N, G, packed)."""
+        text = "\n".join(" ".join(str(int(n)) for n in s) for s in scans)
+        out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
+        assert len(out) == len(scans)
+        return [tuple(int(n) for n in line.split()) for line in out]
+    return run
+
+
+def test_sizes_run_the_form_they_are_there_for(plans):
+    cases = [lengths(c) for c in FORMS]
+    got = plans([(len(lens), sum(lens) if packed else lens[0], c[4], c[5], c[6], packed) for c, (lens, packed) in zip(FORMS, cases)])
+    for c, (lens, packed), (lanes, states, tokens, segs, seg_len) in zip(FORMS, cases, got):
+        assert (lanes, states, segs > 1) == c[:3], c
+        run = [n for n in ((min(seg_len, n) for n in lens) if segs > 1 else lens) if n > 5]
+        assert all(n >= 5 * tokens for n in run), (c, tokens, seg_len)
+        # a rest in some tile
+        assert any(n % (seg_len if segs > 1 else tokens) % tokens for n in lens), c
+    # every form, dense and packed, with channels and states that fill their places and that do not
+    for lanes, states in ((4, 2), (4, 4), (16, 1), (16, 2), (16, 4), (16, 8)):
+        for cut in (False, True) if lanes == 16 else (False,):
+            mine = [c for c in FORMS if c[:3] == (lanes, states, cut)]
+            assert {lengths(c)[1] for c in mine} == {False, True}
+            assert {c[5] == lanes * states for c in mine} == {False, True}
+            assert any(c[4] % (256 // lanes) for c in mine) and {c[7] for c in mine} == {"bf16", "f32"}
