@@ -72,7 +72,7 @@ int scan(const gdr_scan_dims* dims, const int32_t* cu, bool step, const void* x,
         return GDR_ERR_SHAPE;
     if (d.B == 0) return GDR_OK;
     const int64_t e = elt_of(d.dtype), some = rows > 0, gn = (int64_t)d.G * d.N, dn = (int64_t)d.D * d.N;
-    const ScanCut cut = step || rows == 0 ? ScanCut{1, 0} : scan_cut(d.B, d.T, d.D, d.G, cu != nullptr);
+    const ScanCut cut = step || rows == 0 ? ScanCut{1, 0} : scan_cut(d.B, d.T, d.D, d.G, d.N, cu != nullptr);
     const int64_t need = scan_workspace(d, cut);
     enum { X, DT, BB, CC, Z, AA, SKIP, BIAS, H0, OUT, HT, CU, WORK };
     Operand o[] = {{x, rows, d.D, d.x_stride, e, some != 0, {}},
@@ -246,7 +246,7 @@ size_t gdr_selective_scan_workspace_bytes(const gdr_scan_dims* dims, int packed)
     int64_t rows;
     static const int32_t some = 0;
     if (!dims || scan_rows(*dims, packed ? &some : nullptr, &rows) != GDR_OK || dims->N > GDR_SCAN_MAX_STATES || rows == 0) return 0;
-    return 4 * static_cast<size_t>(scan_workspace(*dims, scan_cut(dims->B, dims->T, dims->D, dims->G, packed != 0)));
+    return 4 * static_cast<size_t>(scan_workspace(*dims, scan_cut(dims->B, dims->T, dims->D, dims->G, dims->N, packed != 0)));
 }
 
 int gdr_selective_scan(const gdr_scan_dims* dims, const int32_t* cu_seqlens, const void* x, const void* dt,

@@ -7,12 +7,13 @@ namespace gdr {
 
 // Segments that the sequences of a scan are cut into, by the sizes alone.
 //
-// A scan runs a token after the other in workgroups of 16 channels, 25 ns a token for one workgroup on
-// a CU and 42 for two.  Where they leave half the CUs idle, segments run side by side: first the states
-// behind each from zero, 55 % of a run's work, then each segment from its start.  Two workgroups a CU,
-// at 1.55 * 42 ns for each segment's tokens, pay from three segments on, if a sequence is long enough to
-// win back the second launch, and segments of 64 tokens or more.  us whole / cut, N = 16: 1 x 511 x 64 15.5 / 9.9,
-// 1 x 260 x 64 10.9 / 9.9, 1 x 130 x 64 8.4 / 9.8; two workgroups a CU, 4 x 300 x 256 11.0 / 12.4.
+// A scan runs a token after the other in workgroups of 16 channels: 25 ns a token for one workgroup on a CU, 36,
+// 63 and 128 with more than 16, 32 and 64 states.  Where they leave half the CUs idle, segments run side by
+// side: first the states behind each from zero, then each segment from its start.  The two launches take the
+// time of 125 tokens of a run, and each token of a segment that of 2, or 3.1 with two workgroups on a CU (more
+// than 64 states: only one fits, of its registers).  us whole / cut, N = 16: 1 x 511 x 64 15.5 / 9.9, 4097 x 1024 100 / 50,
+// 4097 x 2000 100 / 82, 8 x 600 x 256 19.2 / 22.3, 4 x 300 x 256 11.0 / 12.4; N = 32: 4097 x 1024 148 / 74, 3026 x 2592 112 / 122;
+// N = 64: 4097 x 1024 258 / 125, 3 x 3496 x 944 224 / 367; N = 128: 4097 x 1024 527 / 285, 8 x 600 x 256 83 / 110.
 //
 // In a packed batch any sequence may have all rows.  Sequence i, from row c on, has the slots from c / seg_len + i
 // on: at least as many as segments, and T / seg_len + B in all, whatever the lengths.  Segments pay earlier
@@ -21,13 +22,17 @@ namespace gdr {
 struct ScanCut {
     int segs, seg_len;  // packed: segs * B slots
 };
-inline ScanCut scan_cut(int64_t B, int64_t T, int64_t D, int64_t G, bool packed) {
+inline ScanCut scan_cut(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed) {
     const int64_t groups = G * ((D / G + 15) / 16), blocks = B * groups;
-    const int64_t n = 512 / blocks, mean = packed ? T / B : T;
+    const int64_t n = (N > 64 && !packed ? 256 : 512) / blocks, mean = packed ? T / B : T;
     if (n < 3 || mean < (packed ? 128 : 256)) return {1, 0};
     const int64_t len = ((mean + n - 1) / n + 63) / 64 * 64;
     const int64_t segs = packed ? (T / len + 2 * B - 1) / B : (T + len - 1) / len;
-    if (segs < 2 || (!packed && T < 512 && segs * blocks > 256)) return {1, 0};
+    if (segs < 2) return {1, 0};
+    if (!packed) {
+        const bool two = segs * blocks > 256;
+        if ((two && T < 512) || 125 + len * (two ? 31 : 20) / 10 >= T) return {1, 0};
+    }
     return {static_cast<int>(segs), static_cast<int>(len)};
 }
 

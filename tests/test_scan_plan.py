@@ -1,5 +1,6 @@
 """Which kernel runs a selective scan (csrc/scan_plan.h), on the host."""
 import os
+import random
 import shutil
 import subprocess
 
@@ -45,3 +46,35 @@ def test_sizes_run_the_form_they_are_there_for(plans):
             assert {lengths(c)[1] for c in mine} == {False, True}
             assert {c[5] == lanes * states for c in mine} == {False, True}
             assert any(c[4] % (256 // lanes) for c in mine) and {c[7] for c in mine} == {"bf16", "f32"}
+
+
+# Dense scans (B, T, D, N) that were faster cut, and whole.
+CUT = [(1, 520, 64, 4), (1, 1100, 512, 16), (1, 4097, 2000, 16), (2, 4000, 512, 24), (4, 1000, 256, 32), (1, 4097, 2000, 64),
+       (4, 1000, 256, 64), (1, 1100, 512, 96), (1, 4097, 1024, 128), (4, 1000, 256, 128), (1, 300, 64, 128)]
+WHOLE = [(8, 600, 256, 4), (8, 600, 256, 16), (8, 600, 256, 32), (8, 600, 256, 64), (8, 600, 256, 96), (8, 600, 256, 128),
+         (8, 1043, 416, 30), (1, 3026, 2592, 30), (1, 1340, 2768, 30), (3, 3496, 944, 64), (3, 2779, 688, 64), (8, 1071, 448, 8),
+         (4, 585, 512, 64), (4, 543, 368, 128), (1, 510, 2896, 16), (4, 300, 256, 16)]
+
+
+def test_dense_scans_are_cut_where_that_pays(plans):
+    for sizes, cut in ((CUT, True), (WHOLE, False)):
+        for case, plan in zip(sizes, plans([(*s, 1, 0) for s in sizes])):
+            assert (plan[3] > 1) == cut, case
+
+
+def test_segments_make_up_the_sequences(plans):
+    """A dense sequence has as many segments as its tokens need; a packed batch's slots suffice for any lengths."""
+    rng = random.Random(2)
+    some = lambda lo, hi: int(round(2 ** rng.uniform(lo, hi)))  # noqa: E731
+    scans = []
+    for _ in range(20000):
+        G = rng.choice([1, 1, 2, 3])
+        scans.append((some(0, 8), some(0, 20), G * some(0, 11), some(0, 7), G, rng.random() < 0.5))
+    for (B, T, D, N, G, packed), (_, _, _, segs, seg_len) in zip(scans, plans(scans)):
+        if segs == 1:
+            continue
+        assert seg_len % 64 == 0
+        if packed:
+            assert segs * B >= T // seg_len + B
+        else:
+            assert (segs - 1) * seg_len < T <= segs * seg_len
