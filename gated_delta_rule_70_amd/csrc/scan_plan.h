@@ -16,9 +16,13 @@ namespace gdr {
 // N = 64: 4097 x 1024 258 / 125, 3 x 3496 x 944 224 / 367; N = 128: 4097 x 1024 527 / 285, 8 x 600 x 256 83 / 110.
 //
 // In a packed batch any sequence may have all rows.  Sequence i, from row c on, has the slots from c / seg_len + i
-// on: at least as many as segments, and T / seg_len + B in all, whatever the lengths.  Segments pay earlier
-// there, since the longest sequence counts: 64 channels, lengths 957, 503, 269, 189 and six short ones 25.6 / 12.2;
-// equal lengths may lose, twenty of 600 tokens of 128 channels 20.9 / 32.4, ten of 64 channels 18.6 / 15.5.
+// on: at least as many as segments, and T / seg_len + B in all, whatever the lengths, which the host does not know.
+// Cutting is for lengths that differ; equal ones may lose by it.  us whole / cut, N = 16, equal lengths, and half of the
+// rows in one: 10 x 300 x 64 11.6 / 12.3 and 39 / 13.8, 10 x 1200 x 128 33.8 / 30.9 and 141 / 32.3, 20 x 300 x 128 12.4 / 22.8 and
+// 72.5 / 23.0, 20 x 600 x 128 22.2 / 33.3 and 142 / 33.2, 40 x 300 x 64 12.8 / 25.3 and 141 / 25.6; N = 128: 20 x 300 x 64 45 / 56 and
+// 384 / 77.  Below 512 rows in all both lose, of up to 64 states: 3 x 130 x 64 9.1 / 11.3 and 10.0 / 11.3, N = 64 13.9 / 20.9 and
+// 19.5 / 20.9; from there on one of the two wins: 4 x 130 x 64 9.0 / 11.4 and 11.6 / 11.4, 8 x 130 x 64 9.1 / 11.7 and 17.5 / 11.9.
+// With more, a run is long enough at once: 2 x 250 x 64, N = 128, 37.9 / 31.1.
 struct ScanCut {
     int segs, seg_len;  // packed: segs * B slots
 };
@@ -28,7 +32,7 @@ inline ScanCut scan_cut(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, b
     if (n < 3 || mean < (packed ? 128 : 256)) return {1, 0};
     const int64_t len = ((mean + n - 1) / n + 63) / 64 * 64;
     const int64_t segs = packed ? (T / len + 2 * B - 1) / B : (T + len - 1) / len;
-    if (segs < 2) return {1, 0};
+    if (segs < 2 || (packed && T < 512 && N <= 64)) return {1, 0};
     if (!packed) {
         const bool two = segs * blocks > 256;
         if ((two && T < 512) || 125 + len * (two ? 31 : 20) / 10 >= T) return {1, 0};

@@ -62,6 +62,16 @@ def test_dense_scans_are_cut_where_that_pays(plans):
             assert (plan[3] > 1) == cut, case
 
 
+def test_packed_batches_are_cut_where_that_pays(plans):
+    """Few rows are not worth a second launch, whatever the lengths; batches in which one sequence may be far longer
+    than the others are cut."""
+    few = [(2, 260, 64, 16), (2, 500, 64, 16), (3, 390, 64, 16), (3, 480, 64, 16), (3, 390, 64, 64)]
+    many = [(10, 3000, 64, 16), (20, 6000, 128, 16), (40, 12000, 64, 16), (20, 6000, 64, 128), (8, 1040, 64, 16), (2, 500, 64, 128)]
+    for sizes, cut in ((few, False), (many, True)):
+        for case, plan in zip(sizes, plans([(*s, 1, 1) for s in sizes])):
+            assert (plan[3] > 1) == cut, case
+
+
 def test_segments_make_up_the_sequences(plans):
     """A dense sequence has as many segments as its tokens need; a packed batch's slots suffice for any lengths."""
     rng = random.Random(2)
