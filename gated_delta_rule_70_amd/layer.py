@@ -163,8 +163,10 @@ def causal_conv(x, weight, bias=None, state=None, cu_seqlens=None, activation="s
             if status:
                 _fail(status)
             return (out if isinstance(out, torch.Tensor) else tuple(out)), out_state
-    elif (not _given(out) or out_state is None and want_state) and _elsewhere(stream, x):
-        return _on(stream, causal_conv, x, weight, bias, state, cu_seqlens, activation, out, out_state, want_state)
+    else:
+        out = _listed(out)
+        if (not _given(out) or out_state is None and want_state) and _elsewhere(stream, x):
+            return _on(stream, causal_conv, x, weight, bias, state, cu_seqlens, activation, out, out_state, want_state)
     return _conv(x, weight, bias, state, cu_seqlens, activation, out, out_state, want_state, stream,
                  *_batch(x, cu_seqlens))
 
@@ -180,9 +182,16 @@ def causal_conv_step(x, weight, state, bias=None, activation="silu", out=None, o
             if status:
                 _fail(status)
             return out if isinstance(out, torch.Tensor) else tuple(out)
-    elif not _given(out) and _elsewhere(stream, x):
-        return _on(stream, causal_conv_step, x, weight, state, bias, activation, out, out_state)
+    else:
+        out = _listed(out)
+        if not _given(out) and _elsewhere(stream, x):
+            return _on(stream, causal_conv_step, x, weight, state, bias, activation, out, out_state)
     return _conv(x, weight, bias, state, None, activation, out, end, False, stream, *_tokens(x))[0]
+
+
+def _listed(out):
+    """``out`` as something that can be gone through more than once."""
+    return out if out is None or isinstance(out, (torch.Tensor, tuple, list)) else list(out)
 
 
 def _given(out):
