@@ -374,6 +374,7 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
                 _fail(status)
             return out if isinstance(out, torch.Tensor) else tuple(out)
     elif not isinstance(out, torch.Tensor) and _elsewhere(stream, a):
+        out = out if out is None or isinstance(out, (tuple, list)) else list(out)  # whose tensors _on looks for
         return _on(stream, matmul_i8, a, a_scale, w, w_scale, bias, out, out_dtype)
     shape, wshape = a.shape, w.shape
     if not shape or len(wshape) != 2 or shape[-1] != wshape[1]:
