@@ -159,15 +159,6 @@ __device__ __forceinline__ float softplus(float v) {
     return v != v ? v : r;
 }
 
-// Sum over the 16 lanes of a row, in all of them.
-__device__ __forceinline__ float row_sum(float x) {
-    x += dpp_mov<0xB1>(x);   // quad_perm [1,0,3,2]
-    x += dpp_mov<0x4E>(x);   // quad_perm [2,3,0,1]
-    x += dpp_mov<0x141>(x);  // row_half_mirror: the other quad of 8 lanes
-    x += dpp_mov<0x140>(x);  // row_mirror: the other half of 16 lanes
-    return x;
-}
-
 constexpr int kXcds = 8;
 
 // Work item of block b of n, so that each XCD (block b is on XCD b % 8) has a contiguous range: what
