@@ -145,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a, int til
         if constexpr (P > 4) y += dpp_mov<0x141>(y);  // row_half_mirror
         if constexpr (P > 8) y += dpp_mov<0x140>(y);  // row_mirror
         if constexpr (P > 16) y += __shfl_xor(y, 16);
-        y = __builtin_fmaf(skip, xv, y);
+        if (a.skip) y = __builtin_fmaf(skip, xv, y);  // not 0 x, which is NaN where x is infinite
         TX* out = static_cast<TX*>(a.out) + (seq0 + q) * a.out_stride + d;
         if (a.z) y *= silu_for(to_f32(z[q]), out);
         if (lane == 0) store1(out, y);
@@ -653,7 +653,10 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                         if constexpr (MODE != kEnds) p[J] = s ? __builtin_fmaf(now.c[s][J % 4], h[s], p[J]) : now.c[s][J % 4] * h[s];
                     }
                 });
-                if constexpr (MODE != kEnds) sY[buf][K::at(here + lane, c)] = __builtin_fmaf(skip, xv, sum_scatter<L>(p, lane));
+                if constexpr (MODE != kEnds) {
+                    const float y = sum_scatter<L>(p, lane);
+                    sY[buf][K::at(here + lane, c)] = a.skip ? __builtin_fmaf(skip, xv, y) : y;
+                }
                 step = step1, xv = xv1;
             }
         }

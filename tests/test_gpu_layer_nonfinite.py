@@ -131,3 +131,27 @@ def test_rates_past_the_range(B, T, D, rate):
     one = {k: v[:, 0].contiguous().cuda() if k in ("x", "dt", "B", "C", "z") else v.cuda() for k, v in a.items() if k != "h0"}
     state = a["h0"].cuda()
     assert (gdr.selective_scan_step(**one, state=state)[:, 3] == INF).all() and (state[:, 3, 2] == INF).all()
+
+
+@pytest.mark.parametrize("N", [3, 16, 20])
+@pytest.mark.parametrize("B,T,D", [(2, 40, 40), (16, 37, 1000), (2, 700, 24)], ids=["sixteen_lanes", "four_lanes", "segments"])
+def test_without_a_skip(B, T, D, N):
+    """Where D is not given, an infinite input reaches y by the states alone, with a gate and without."""
+    note(f"selective_scan with infinities and without D {B}x{T}x{D}, N={N}")
+    for gate in (True, False):
+        a = inputs(B, T, D, N, 6)
+        a["z"] += 1.
+        if T == 700:
+            a["dt"] *= 0.2
+        infinite(a, T // 2)
+        a["D"], a["z"] = None, a["z"] if gate else None
+        want, bound, end, end_bound = expected(a)
+        assert not want.isnan().any() and want[0, T // 2:, [3, 5, 7]].isinf().all()
+        g = {k: None if v is None else v.cuda() for k, v in a.items()}
+        y, ht = gdr.selective_scan(**g)
+        ref.close(y, want, bound)
+        ref.close(ht, end, end_bound)
+        state = g.pop("h0")
+        for t in range(T // 2 + 2 if T == 40 else 0):
+            one = {k: v[:, t].contiguous() if v is not None and k in ("x", "dt", "B", "C", "z") else v for k, v in g.items()}
+            ref.close(gdr.selective_scan_step(**one, state=state), want[:, t], bound[:, t])
