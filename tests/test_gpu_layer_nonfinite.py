@@ -155,3 +155,35 @@ def test_without_a_skip(B, T, D, N):
         for t in range(T // 2 + 2 if T == 40 else 0):
             one = {k: v[:, t].contiguous() if v is not None and k in ("x", "dt", "B", "C", "z") else v for k, v in g.items()}
             ref.close(gdr.selective_scan_step(**one, state=state), want[:, t], bound[:, t])
+
+
+@pytest.mark.parametrize("N", [5, 16, 30])
+def test_infinite_states_of_a_packed_batch(N):
+    """In segments of several sequences, steps through softplus: states that stay, one that a token wipes out, and
+    an infinite input, in the sequences that they belong to."""
+    note(f"packed selective_scan in segments with infinite states, N={N}")
+    lens, D = [700, 0, 3, 650], 24
+    starts = [0, 700, 700, 703]
+    assert gdr.selective_scan_workspace_bytes(len(lens), sum(lens), D, N, packed=True) > 0
+    a = inputs(1, sum(lens), D, N, 7)
+    a["h0"] = inputs(4, 1, D, N, 8)["h0"]
+    a = {k: v[0] if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+    a["dt"], a["x"], a["z"] = 4 * a["dt"] - 3, a["x"].bfloat16(), a["z"].bfloat16()
+    a["B"], a["C"] = a["B"].bfloat16(), a["C"].bfloat16()
+    a["h0"][0, 4, 1], a["h0"][3, 9, 0], a["h0"][3, 2, 2] = INF, -INF, INF
+    a["A"][9], a["A"][4, 1], a["A"][2, 2] = -60., -0.5, -2.
+    gone = starts[3] + 200
+    a["dt"][gone, 2] = 300.
+    a["x"][starts[3] + 100, 3] = INF
+    cu = torch.tensor([*starts, sum(lens)], dtype=torch.int32, device="cuda")
+    y, ht = gdr.selective_scan(**on_gpu(a), dt_softplus=True, cu_seqlens=cu)
+    y, ht = y.float().cpu(), ht.cpu()
+    nan, inf = torch.zeros(y.shape, dtype=torch.bool), torch.zeros(y.shape, dtype=torch.bool)
+    nan[gone:, 2] = True
+    inf[:700, 4] = inf[starts[3]:, 9] = inf[starts[3]:gone, 2] = inf[starts[3] + 100:, 3] = True
+    assert torch.equal(y.isnan(), nan) and torch.equal(y.isinf(), inf)
+    assert (y[starts[3]:, 9] < 0).all() and (y[:700, 4] > 0).all() and (y[starts[3] + 100:, 3] > 0).all()
+    hn, hi = torch.zeros(ht.shape, dtype=torch.bool), torch.zeros(ht.shape, dtype=torch.bool)
+    hn[3, 2, 2] = hi[0, 4, 1] = hi[3, 9, 0] = True
+    hi[3, 3] = True
+    assert torch.equal(ht.isnan(), hn) and torch.equal(ht.isinf(), hi)
