@@ -9,11 +9,11 @@
 //
 // Prompts are bound by that: for each token and wave of 64 states six cycles of four (the exponential two),
 // a token's softplus, gate and sum over its states on top.  us from one call to the next (inputs from
-// memory): 4097 tokens of 4096 channels of 16, bf16, 101 (110), where a copy of the inputs and
-// outputs would take 27; 8 sequences of 512 70 (76); 4097 x 1024 48 (50); 32768 x 4096 840.  At 8 x 4096 x 4096 the ALU
-// issued in 93 % of the cycles.  fp32 matrix instructions do not run beside the ALU here: one of 4 x 4 x 1
-// takes as long as 3.6 additions, so neither step x B nor the sums over states gain by them.  Single tokens are
-// bound by the states' bytes: 256 sequences of 4096 x 16 27 us (31 from memory, 4.6 TB/s).
+// memory): 4097 tokens of 4096 channels of 16, bf16, 105 (114), where a copy of the inputs and
+// outputs would take 27; 8 sequences of 512 70 (76); 4097 x 1024 49 (49); 32768 x 4096 850.  At eight packed sequences
+// of 4096 channels the ALU issued in 94 % of the cycles.  fp32 matrix instructions do not run beside the ALU here: one
+// of 4 x 4 x 1 takes as long as 3.6 additions, so neither step x B nor the sums over states gain by them.  Single tokens
+// are bound by the states' bytes: 256 sequences of 4096 x 16 27 us (31 from memory, 4.6 TB/s).
 #include "layer_launch.h"
 
 #include <type_traits>
@@ -224,8 +224,8 @@ __device__ __forceinline__ void unrolled(std::integer_sequence<int, J...>, F f) 
 // y for every token; sum_scatter leaves the j-th token's y in lane j.
 //
 // Half of the waves do nothing but that; the others load, compute steps, and gate and store a tile behind.
-// With one set of waves for all of it, 4097 x 4096 x 16 took 160 us instead of 113 and 8 x 4096 x 4096 725 instead
-// of 556: a wave that is alone on its SIMD issues every 5 to 6 cycles at best.  Leaving the sums over lanes to
+// With one set of waves for all of it, 4097 x 4096 x 16 took 160 us instead of 113 (105 since) and 8 x 4096 x 4096 725
+// instead of 556: a wave that is alone on its SIMD issues every 5 to 6 cycles at best.  Leaving the sums over lanes to
 // the storing waves too (parts of y through LDS) took 127.  Tiles of 32 tokens instead of 64 took 195 (memory's
 // latency shows), TT = 48 for S = 4 263 instead of 291 (N = 64).
 template <int L, int S>
@@ -242,7 +242,8 @@ struct Tile {
         return L == 16 ? (n % S * 16 + n / S) * (TT + 4) + t : t * NP + n;
     }
     // Where token t's channel c lies: channels are exchanged in fours so that the lanes of a wave,
-    // on L tokens of 64 / L channels, meet no bank twice.
+    // on L tokens of 64 / L channels, read 64 words that differ modulo 64.  (The counters have 0.5 to 0.9 cycles of
+    // bank conflicts for each LDS instruction all the same, 1.7 in the launch for the states behind segments.)
     static __device__ __forceinline__ int at(int t, int c) {
         return t * CT + (c ^ (L == 16 ? (t >> 2 & 3) << 2 : (t & 3) << 4));
     }

@@ -45,7 +45,8 @@ struct ScanTile {
     int lanes, states;
 };
 
-// Tokens of a tile, whose operands lie in LDS twice: two workgroups share a CU's.
+// Tokens of a tile, whose operands lie in LDS twice: two workgroups share a CU's (of more than 64 states one fits by its
+// registers, and longer tiles than 16 were not measured).
 constexpr int scan_tile_tokens(int lanes, int states) {
     return lanes == 4 ? 32 : states <= 2 ? 64 : states == 4 ? 48 : 16;
 }
@@ -53,8 +54,9 @@ constexpr int scan_tile_tokens(int lanes, int states) {
 // Lanes for a channel.  ns a token, by workgroups for each CU (each of the dense batch's sequences as
 // long; 256 CUs): 16 lanes, workgroups of 16 channels: 25, 42, 60, 78, 116 for 1, 2, 3, 4, 6; 4 lanes, workgroups
 // of 64 channels, N = 16: 74, 135, 270 for 1, 2, 4, N = 8: 103 for 2.  So 4 lanes take less where they
-// fill the CUs evenly: 4 x 2048 x 4096 152 us (16 lanes 161), 6 x 1024 x 4096 133 (119), 8 x 512 x 4096
-// 69 (81).  Sequences of a packed batch end at different times: there only from four workgroups a CU on.
+// fill the CUs evenly.  us with 4 lanes / 16: 8 x 512 x 4096 73 / 82, N = 8 55 / 84, 16 x 256 x 4096 77 / 86, 4 x 2048 x 4096 171 / 170;
+// 6 x 1024 x 4096 140 / 120, 2 x 2048 x 4096 152 / 94.  Sequences of a packed batch end at different times: there only
+// from four workgroups a CU on.
 inline bool scan_few_lanes(int64_t B, int64_t D, int64_t N, int64_t G, bool packed, int64_t segs) {
     if (N > 16 || segs > 1) return false;
     const int64_t per = D / G, parts = B * G, wide = parts * ((per + 63) / 64), narrow = parts * ((per + 15) / 16);

@@ -354,8 +354,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     uint8 tensor on x's GPU; one is allocated, in each call, if it is None.  Calls that overlap in time, or graphs
     replayed so, need one each.
 
-    Infinite inputs give what the formula gives.  A token's factor ``exp(step * A)`` below fp32's normal range is
-    zero, and NaN on an infinite state.
+    Infinite inputs and states give what the formula gives, but that what lies below fp32's normal range counts as
+    zero: infinity times such a token's factor ``exp(step * A)``, or such a gate, is NaN.
     """
     if stream is None:
         status = (_qz._B or _qz._binding()).selective_scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, cu_seqlens, out, ht,

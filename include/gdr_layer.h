@@ -129,8 +129,9 @@ typedef struct {
  * dt_bias [D] fp32, dense (these two may be NULL); h0 and ht [B][D][N] fp32, dense.  States are fp32
  * throughout.  ht (if not NULL) receives the last state; it may be h0 itself.  A is expected not
  * to be positive; where it is, the state grows as the formula says (a token's factor past fp32's
- * range is infinity, and NaN on a state of zero; in a call with a workspace on any state).  A token's
- * factor below fp32's normal range is zero, and NaN on an infinite state.  Infinities in A count as the
+ * range is infinity, and NaN on a state of zero, or in a call that needs a workspace on any state).
+ * Infinite inputs and states give what the formula gives, but that what lies below fp32's normal range
+ * counts as zero: infinity times such a factor of a token, or such a gate, is NaN.  Infinities in A count as the
  * finite values next to them (-infinity: a state that each token of a positive step begins anew).
  */
 int gdr_selective_scan(const gdr_scan_dims* dims, const int32_t* cu_seqlens, const void* x, const void* dt,
