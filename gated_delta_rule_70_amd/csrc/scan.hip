@@ -565,11 +565,12 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                         h[s] = __builtin_fmaf(half * h[s], half, end[i][s]);
                     }
         }
-        // NaN may come of an infinite state and a segment's factor that is zero.  Token by token such a state stays,
-        // unless a token's own factor is zero: this thread goes through the segments again and looks.
+        // An infinite state stays so, token by token, unless a token's own factor is zero: a segment's whole factor
+        // does not tell.  A thread that has come to infinity, or to NaN by zero times it, goes through the segments
+        // again and looks.
         bool lost = false;
 #pragma unroll
-        for (int s = 0; s < S; ++s) lost |= h[s] != h[s];
+        for (int s = 0; s < S; ++s) lost |= !(fabsf(h[s]) <= 3.402823466e38f);
         if (lost) {
             const TDT* dt = static_cast<const TDT*>(a.dt) + (first - (int64_t)seg * a.seg_len) * a.dt_stride + d0 + c;
             const float bias = a.dt_bias ? a.dt_bias[d0 + c] : 0.f;
@@ -581,7 +582,7 @@ __global__ __launch_bounds__(2 * kThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
                     const int64_t e = slot - seg + i;
                     const float half = fminf(__builtin_amdgcn_exp2f(0.5f * steps[e * a.D + d0 + c] * A[s]), 3.402823466e38f);
                     const float end = ends[(e * a.D + d0 + c) * N + state[s]];
-                    bool stays = half == 0.f && fabsf(v) > 3.402823466e38f;
+                    bool stays = fabsf(v) > 3.402823466e38f;
                     float next = stays ? v + end : __builtin_fmaf(half * v, half, end);
 #pragma unroll 1
                     for (int t = 0; stays && t < a.seg_len; ++t) {

@@ -187,3 +187,18 @@ def test_infinite_states_of_a_packed_batch(N):
     hn[3, 2, 2] = hi[0, 4, 1] = hi[3, 9, 0] = True
     hi[3, 3] = True
     assert torch.equal(ht.isnan(), hn) and torch.equal(ht.isinf(), hi)
+
+
+@pytest.mark.parametrize("T,t", [(60, 30), (700, 10), (700, 63), (700, 500)])
+def test_a_token_wipes_out_where_its_segment_would_not(T, t):
+    """A token's factor of 2^-144 and nothing near that around it: the half of its segment's is in range."""
+    note(f"infinite states and a factor of zero in a segment's halves, T={T}, t={t}")
+    N, D = 16, 24
+    a = inputs(1, T, D, N, 9)
+    a["h0"][0, 2, 5], a["A"][2, 5] = INF, -2.
+    a["dt"][0, t], a["x"][0, t] = 50., 0.
+    y, ht = gdr.selective_scan(**on_gpu(a))
+    bad = torch.zeros(T, D, dtype=torch.bool)
+    bad[t:, 2] = True
+    assert torch.equal(y[0].isnan().cpu(), bad) and (y[0, :t, 2] == INF).all()
+    assert ht[0, 2, 5].isnan() and ht.isnan().sum() == 1
